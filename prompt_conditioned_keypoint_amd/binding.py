@@ -23,12 +23,22 @@ GKD_HEATMAP_BF16 = 0x1       # gkd_kernel_heatmap flag: bfloat16 heatmaps
 GKD_UPSAMPLE_CORNERS = 0x2   # gkd_kernel_heatmap flag: align_corners=True upsample
 GKD_COORDS_CORNERS = 0x4     # decode flag: corner-aligned -1..1 coordinates
 GKD_QUERY_TOKENS = 0x8       # query as [B, skip + H*W, C] tokens; skip in bits 8..15
+GKD_TOKENS_VERSION = 1       # include/gkdtokens.h
+GKD_ROPE_INTERLEAVED = 0x1   # gkd_qk_norm_rope flag: pairs (2i, 2i + 1)
+GKD_ATTN_CAUSAL = 0x1        # gkd_prefix_attention flag: own keys up to the query's place
+GKD_ACTS = {"none": 0, "relu": 1, "gelu": 2, "quick_gelu": 3, "silu": 4}
 STATUS = {0: "GKD_OK", 1: "GKD_ERR_NULL", 2: "GKD_ERR_SHAPE", 3: "GKD_ERR_DTYPE",
           4: "GKD_ERR_VALUE", 5: "GKD_ERR_UNSUPPORTED", 6: "GKD_ERR_HIP",
           7: "GKD_ERR_ALIGN"}
 
 _lib = None
 _P, _I, _U32, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32, ctypes.c_float
+
+
+class GkdHeads(ctypes.Structure):
+    """gkd_heads: data pointer and element strides of a [B,T,H,D] operand."""
+    _fields_ = [("data", _P), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
+                ("head", ctypes.c_int64)]
 
 
 class GkdError(RuntimeError):
@@ -73,8 +83,25 @@ def load():
     lib.gkd_kg_transformer_noalloc.restype = _I
     lib.gkd_kg_transformer_noalloc.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I,
                                                _I, _I, _U32, _P, _P]
+    _L, _Z, _H = ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(GkdHeads)
+    lib.gkd_tokens_version.restype = _I
+    lib.gkd_linear_workspace_size.restype = _Z
+    lib.gkd_linear_workspace_size.argtypes = [_I, _I, _I, _L, _L]
+    lib.gkd_linear.restype = _I
+    lib.gkd_linear.argtypes = [_P, _L, _P, _L, _P, _P, _L, _I, _I, _I, _I, _I, _I, _U32, _P, _L,
+                               _P, _Z, _P]
+    lib.gkd_qk_norm_rope.restype = _I
+    lib.gkd_qk_norm_rope.argtypes = [_H, _I, _H, _I, _I, _I, _I, _P, _L, _I, _P, _I, _P, _P, _F,
+                                     _I, _U32, _H, _H, _P]
+    lib.gkd_prefix_attention_workspace_size.restype = _Z
+    lib.gkd_prefix_attention_workspace_size.argtypes = [_I] * 7
+    lib.gkd_prefix_attention.restype = _I
+    lib.gkd_prefix_attention.argtypes = [_H, _H, _H, _I, _H, _H, _I, _P, _P, _P, _I, _I, _I, _I,
+                                         _I, _F, _I, _U32, _H, _P, _Z, _P]
     if lib.gkd_abi_version() != GKD_ABI_VERSION:
         raise ImportError("libgkdhead ABI version mismatch")
+    if lib.gkd_tokens_version() != GKD_TOKENS_VERSION:
+        raise ImportError("libgkdhead token operators' version mismatch")
     _lib = lib
     return lib
 
@@ -359,4 +386,236 @@ def kg_transformer(query: torch.Tensor, weights: torch.Tensor, kern_vis=None, ma
     _dev(workspace, "workspace", torch.uint8, 1)
     _check(lib.gkd_kg_transformer(*args, _ptr(workspace), workspace.numel(),
                                   _stream(query.device)))
+    return out
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _on_current(dev):
+    # kernels are launched on the current device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _heads(t, name, dtype=None, ndim=4):
+    """A [B,T,H,D] (ndim 3: [T,H,D]) operand with any strides but adjacent
+    head elements, as gkd_heads."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a head must be adjacent")
+    return GkdHeads(t.data_ptr(), st[0] if ndim == 4 else 0, st[-3], st[-2])
+
+
+def _workspace(workspace, need, dev):
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _dev(workspace, "workspace", torch.uint8, 1)
+    _same_device(dev, workspace=workspace)
+    return workspace, workspace.numel()
+
+
+def _row_stride(t, name):
+    """Row stride of a [..., n] tensor whose rows are evenly spaced."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    ld, span = None, 1
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != ld * span:
+            raise ValueError(f"{name}: its rows must be evenly spaced")
+        span *= size
+    return t.shape[-1] if ld is None else ld
+
+
+def linear_workspace_size(M: int, N: int, K: int, ldx: int | None = None,
+                          ldw: int | None = None) -> int:
+    """Bytes of workspace gkd_linear needs for these sizes and row strides."""
+    return int(load().gkd_linear_workspace_size(M, N, K, K if ldx is None else ldx,
+                                                K if ldw is None else ldw))
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act: str = "none",
+           out_dtype=None, out=None, workspace=None) -> torch.Tensor:
+    """act(x @ weight.T + bias) + residual: x [..., K] bf16, weight [N, K]
+    bf16, bias [N] bf16, residual [..., N] in the output's dtype (bf16, or
+    float32 by out_dtype, out or residual) -> [..., N]. Rows may be strided.
+    act: "none", "relu", "gelu", "quick_gelu" or "silu". `out` may be
+    `residual` itself. workspace: a uint8 GPU tensor of at least
+    linear_workspace_size() bytes (allocated here when None)."""
+    lib = _lib or load()
+    if not (x.is_cuda and weight.is_cuda):
+        raise ValueError("x and weight must be GPU tensors")
+    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError(f"x and weight must be bfloat16, got {x.dtype} and {weight.dtype}")
+    if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x must be [..., K] and weight [N, K], got {tuple(x.shape)} and "
+                         f"{tuple(weight.shape)}")
+    if act not in GKD_ACTS:
+        raise ValueError(f"act must be one of {sorted(GKD_ACTS)}")
+    N, K = weight.shape
+    shape = (*x.shape[:-1], N)
+    M = x.numel() // K if K else 0
+    if out_dtype is None:
+        out_dtype = (out.dtype if out is not None else
+                     residual.dtype if residual is not None else torch.bfloat16)
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+    dev = x.device
+    _on_current(dev)
+    _same_device(dev, weight=weight, bias=bias, residual=residual, out=out)
+    if out.shape != shape or out.dtype != out_dtype:
+        raise ValueError(f"out must be {shape} of {out_dtype}")
+    if residual is not None and (residual.shape != shape or residual.dtype != out_dtype):
+        raise ValueError(f"residual must be {shape} of {out_dtype}")
+    if bias is not None and (bias.shape != (N,) or bias.dtype != torch.bfloat16 or
+                             not bias.is_contiguous()):
+        raise ValueError("bias must be [N] bfloat16, contiguous")
+    ldx, ldw, ldo = _row_stride(x, "x"), _row_stride(weight, "weight"), _row_stride(out, "out")
+    ldr = _row_stride(residual, "residual") if residual is not None else 0
+    ws, ws_bytes = None, 0
+    if K % 8 or ldx % 8 or ldw % 8:
+        ws, ws_bytes = _workspace(workspace, lib.gkd_linear_workspace_size(M, N, K, ldx, ldw), dev)
+    _check(lib.gkd_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, _ptr(bias), _ptr(residual),
+                          ldr, M, N, K, GKD_ACTS[act], 1, 1 if out_dtype == torch.bfloat16 else 0,
+                          0, out.data_ptr(), ldo, _ptr(ws), ws_bytes, _stream(dev)))
+    return out
+
+
+def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                 k_out=None):
+    """Head norm and rotary positions in one pass: q [B,T,Hq,D] and k
+    [B,T,Hk,D] (or None), float32 or bf16, strided views welcome; pos
+    [T,n_axes] or [B,T,n_axes] float32; freqs [n_axes, rot/2] float32 (0
+    where a frequency does not belong to an axis); q_weight, k_weight [D] or
+    None (no norm). Returns (q_out, k_out), new and dense unless given; an
+    output may be its input (in place)."""
+    lib = _lib or load()
+    dev, dtype = q.device, q.dtype
+    code = _dtype_code(q)
+    hq = _heads(q, "q")
+    B, T, Hq, D = q.shape
+    Hk = 0
+    hk = hko = None
+    if k is not None:
+        hk = _heads(k, "k", dtype)
+        Hk = k.shape[2]
+        if k.shape != (B, T, Hk, D) or Hk < 1:
+            raise ValueError(f"k must be [B,T,Hk,D], got {tuple(k.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _dev(pos, "pos", torch.float32)
+    _dev(freqs, "freqs", torch.float32, 2)
+    A, half = freqs.shape
+    if tuple(pos.shape) not in ((T, A), (B, T, A)):
+        raise ValueError(f"pos must be [T,n_axes] or [B,T,n_axes], got {tuple(pos.shape)}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _dev(w, name, dtype, 1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must be [D]")
+    if q_out is None:
+        q_out = torch.empty((B, T, Hq, D), dtype=dtype, device=dev)
+    hqo = _heads(q_out, "q_out", dtype)
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty((B, T, Hk, D), dtype=dtype, device=dev)
+        hko = _heads(k_out, "k_out", dtype)
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+    _on_current(dev)
+    _same_device(dev, k=k, pos=pos, freqs=freqs, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
+                 k_out=k_out)
+    _check(lib.gkd_qk_norm_rope(hq, Hq, hk, Hk, B, T, D, pos.data_ptr(),
+                                T * A if pos.dim() == 3 else 0, A, freqs.data_ptr(), 2 * half,
+                                _ptr(q_weight), _ptr(k_weight), eps, code,
+                                GKD_ROPE_INTERLEAVED if interleaved else 0, hqo, hko,
+                                _stream(dev)))
+    return q_out, k_out
+
+
+def prefix_attention_workspace_size(B: int, Tq: int, Hq: int, Hk: int, D: int, P: int,
+                                    S: int) -> int:
+    """Bytes of workspace gkd_prefix_attention needs for these sizes."""
+    return int(load().gkd_prefix_attention_workspace_size(B, Tq, Hq, Hk, D, P, S))
+
+
+def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, v_own=None,
+                     own_len=None, q_len=None, own_mask=None, causal: bool = False, scale=None,
+                     out=None, workspace=None) -> torch.Tensor:
+    """Attention of q [B,Tq,Hq,D] bf16 over a prefix k_prefix, v_prefix
+    [P,Hk,D] shared by the batch and each sequence's own keys k_own, v_own
+    [B,S,Hk,D] (either pair may be None), of which the first own_len[b]
+    (int32) with own_mask[b,j] (uint8) set count. causal: the q_len[b]
+    (int32, default Tq) queries are the last of the own_len[b] own tokens and
+    see own keys up to their place. Queries past q_len[b] leave their rows of
+    out as they are. scale: default D**-0.5. Returns out [B,Tq,Hq,D]; a query
+    without keys gives zeros."""
+    lib = _lib or load()
+    bf16 = torch.bfloat16
+    hq = _heads(q, "q", bf16)
+    B, Tq, Hq, D = q.shape
+    dev = q.device
+    if (k_prefix is None) != (v_prefix is None) or (k_own is None) != (v_own is None):
+        raise ValueError("keys and values go together")
+    P = S = 0
+    Hk = None
+    kp = vp = ko = vo = None
+    if k_prefix is not None:
+        kp, vp = _heads(k_prefix, "k_prefix", bf16, 3), _heads(v_prefix, "v_prefix", bf16, 3)
+        P, Hk = k_prefix.shape[:2]
+        if k_prefix.shape[2] != D or v_prefix.shape != k_prefix.shape:
+            raise ValueError("k_prefix and v_prefix must be [P,Hk,D]")
+    if k_own is not None:
+        ko, vo = _heads(k_own, "k_own", bf16), _heads(v_own, "v_own", bf16)
+        S = k_own.shape[1]
+        Hk = k_own.shape[2] if Hk is None else Hk
+        if k_own.shape != (B, S, Hk, D) or v_own.shape != k_own.shape:
+            raise ValueError("k_own and v_own must be [B,S,Hk,D]")
+    if Hk is None:
+        raise ValueError("give prefix keys, own keys or both")
+    for t, name in ((own_len, "own_len"), (q_len, "q_len")):
+        if t is not None:
+            _dev(t, name, torch.int32, 1)
+            if t.shape[0] != B:
+                raise ValueError(f"{name} must be [B]")
+    if own_mask is not None:
+        _dev(own_mask, "own_mask", torch.uint8, 2)
+        if own_mask.shape != (B, S):
+            raise ValueError("own_mask must be [B,S]")
+    if out is None:
+        out = torch.empty((B, Tq, Hq, D), dtype=bf16, device=dev)
+    ho = _heads(out, "out", bf16)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _on_current(dev)
+    _same_device(dev, k_prefix=k_prefix, v_prefix=v_prefix, k_own=k_own, v_own=v_own,
+                 own_len=own_len, q_len=q_len, own_mask=own_mask, out=out)
+    ws, ws_bytes = _workspace(workspace, lib.gkd_prefix_attention_workspace_size(
+        B, Tq, Hq, Hk, D, P, S), dev)
+    _check(lib.gkd_prefix_attention(hq, kp, vp, P, ko, vo, S, _ptr(own_len), _ptr(q_len),
+                                    _ptr(own_mask), B, Tq, Hq, Hk, D,
+                                    D ** -0.5 if scale is None else float(scale), 1,
+                                    GKD_ATTN_CAUSAL if causal else 0, ho, _ptr(ws), ws_bytes,
+                                    _stream(dev)))
     return out

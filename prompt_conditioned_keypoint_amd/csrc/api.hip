@@ -6,6 +6,7 @@
 #include "gkdhead.h"
 #include "launch.hpp"
 #include "kg_launch.hpp"
+#include "status.hpp"
 
 #include <atomic>
 #include <cmath>
@@ -14,9 +15,9 @@
 #include <cstdint>
 #include <cstdio>
 
-namespace {
+namespace gkd {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 gkd_status fail(gkd_status s, const char* fmt, ...) {
   va_list ap;
@@ -31,15 +32,23 @@ gkd_status ok() {
   return GKD_OK;
 }
 
-constexpr long long kMaxElems = 0x7fffffffLL;  // element counts < 2^31
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
 gkd_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return ok();
   return fail(GKD_ERR_HIP, "%s: launch failed: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace gkd
+
+namespace {
+
+using gkd::fail;
+using gkd::hip_status;
+using gkd::ok;
+
+constexpr long long kMaxElems = 0x7fffffffLL;  // element counts < 2^31
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 
@@ -61,7 +70,7 @@ const char* gkd_status_string(int status) {
   }
 }
 
-const char* gkd_last_error(void) { return g_err; }
+const char* gkd_last_error(void) { return gkd::g_err; }
 
 gkd_status gkd_vkp_pool(const void* support, const float* kpts_px, const uint8_t* kpt_valid,
                         int B, int C, int H, int W, int R, float stride_px, float sigma_px,

@@ -1,0 +1,507 @@
+"""GPU parity of the token operators (HIP through the C ABI) against the
+float64 oracle on the same inputs, at the sizes, strides and masks where
+they can go wrong, and a run of them together.
+
+Tolerances, from the arithmetic (a rounding is off by at most half a step:
+2^-8 relative in bfloat16, 2^-24 in float32; a float32 sum is counted at a
+whole step, 2^-23, an addition, as the matrix pipes' order and rounding
+inside one instruction are their own):
+ linear     a sum of K products goes through K/32 instructions and at most
+            32 additions inside one: (K/32 + 32) 2^-23 sum |x w|; the
+            activations have slopes up to 1.13 and are evaluated to
+            2^-20 |z|; residual and output round once each.
+ rope       the angle is right to 2^-25 of a turn and the cosine to 2 steps:
+            4e-7; the norm's sum and quotient to 14 steps: 8e-7; together
+            below 2^-19 (|u_p| + |u_q|) with the products' own rounding.
+ attention  probabilities round to bfloat16 (2^-8 each, so 2^-8 of the
+            weighted mean of |v|); scores (D <= 128: 4 instructions, 32
+            additions) to 36 2^-23 sum |q k|, which exp passes on as a
+            relative error, twice (sum and product); 1e-5 for the float32
+            sums over up to 2^12 keys and the joins.
+Outputs round to their type at the end.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import tokens as ot
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+STEP = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def gkd():
+    import prompt_conditioned_keypoint_amd as m
+    m.load()
+    assert torch.cuda.is_available()
+    return m
+
+
+def randn(gen, *shape, dtype=BF, scale=1.0):
+    return (torch.randn(*shape, generator=gen, device="cuda") * scale).to(dtype)
+
+
+def rng(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def np64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def rounded(y, tol, dtype):
+    return tol + STEP[dtype] * (np.abs(y) + tol)
+
+
+# ------------------------------------------------------------------ linear
+def linear_tol(y, size, K, dtype, residual):
+    tol = 1.13 * (K / 32 + 32) * 2.0 ** -23 * size + 2.0 ** -20 * size
+    if residual is not None:
+        tol = tol + 2.0 ** -23 * (np.abs(y) + np.abs(residual))
+    return rounded(y, tol, dtype)
+
+
+def check_linear(gkd, M, K, N, act="none", bias=True, residual=True, out=BF, seed=0, **kw):
+    print(f"[linear] M={M} K={K} N={N} {act} bias={bias} residual={residual} {out}", flush=True)
+    g = rng(seed)
+    x, w = randn(g, M, K), randn(g, N, K, scale=K ** -0.5)
+    b = randn(g, N) if bias else None
+    r = randn(g, M, N, dtype=out) if residual else None
+    y = gkd.linear(x, w, bias=b, residual=r, act=act, out_dtype=out, **kw)
+    assert y.dtype == out and y.shape == (M, N)
+    want, size = ot.linear(np64(x), np64(w), np64(b), np64(r), act)
+    err = np.abs(np64(y) - want)
+    assert np.all(err <= linear_tol(want, size, K, out, np64(r))), err.max()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "quick_gelu", "silu"])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_linear_activations(gkd, act, out):
+    check_linear(gkd, 70, 192, 136, act, out=out)
+    check_linear(gkd, 3, 192, 136, act, out=out, residual=False)
+
+
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 33, 64, 65, 127, 129, 200, 257, 300])
+@pytest.mark.parametrize("K,N", [(64, 16), (264, 257), (1000, 130), (8, 300)])
+def test_linear_ragged_sizes(gkd, M, K, N):
+    check_linear(gkd, M, K, N, seed=M)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 1, 1), (5, 7, 3), (40, 33, 65), (130, 65, 129), (1, 1001, 40),
+                                   (300, 517, 259)])
+def test_linear_odd_widths_are_copied_first(gkd, M, K, N):
+    check_linear(gkd, M, K, N, "silu", seed=K)
+    check_linear(gkd, M, K, N, bias=False, residual=False, out=F32, seed=K)
+
+
+@pytest.mark.parametrize("M,K,N", [(4200, 1024, 4096), (4097, 328, 4100), (1025, 4096, 1024),
+                                   (19, 4096, 1030), (700, 2048, 320)])
+def test_linear_large(gkd, M, K, N):
+    check_linear(gkd, M, K, N, "gelu", seed=N)
+
+
+def test_linear_extreme_activations(gkd):
+    """Activations far out: their limits, and NaN stays where it is."""
+    x = torch.tensor([[200.0], [-200.0], [1e30], [-1e30], [0.0], [float("nan")]], device="cuda").to(BF)
+    x = torch.nn.functional.pad(x, (0, 7))
+    w = torch.nn.functional.pad(torch.ones(4, 1, device="cuda"), (0, 7)).to(BF)
+    big = float(torch.tensor(1e30).to(BF))
+    for act in ("relu", "gelu", "quick_gelu", "silu"):
+        y = gkd.linear(x, w, act=act, out_dtype=F32).cpu()
+        assert torch.equal(y[:5, 0], torch.tensor([200.0, 0.0, big, 0.0, 0.0])), (act, y)
+        assert bool(torch.isnan(y[5]).all()), act
+
+
+def test_linear_strided_rows_in_place_residual_and_untouched_padding(gkd):
+    g = rng(3)
+    M, K, N = 45, 72, 36
+    xs, ws = randn(g, 3, 15, 2 * K), randn(g, N, K + 8)
+    x, w = xs[:, :, K:], ws[:, :K]
+    for out in (BF, F32):
+        buf = torch.full((3, 15, N + 5), 7.0, dtype=out, device="cuda")
+        y = buf[:, :, :N]
+        y.copy_(randn(g, 3, 15, N))
+        r = np64(y).reshape(M, N)
+        got = gkd.linear(x, w, residual=y, out=y)
+        assert got.data_ptr() == buf.data_ptr()
+        want, size = ot.linear(np64(x).reshape(M, K), np64(w), None, r)
+        assert np.all(np.abs(np64(y).reshape(M, N) - want) <= linear_tol(want, size, K, out, r))
+        assert bool((buf[:, :, N:] == 7).all())
+    # rows that start off 16-byte places: copied, same results
+    xo = torch.empty(M, K + 1, dtype=BF, device="cuda")
+    xo[:, :K] = x.reshape(M, K)
+    a = gkd.linear(xo[:, :K], w)
+    assert torch.equal(a, gkd.linear(x.reshape(M, K), w))
+
+
+def test_linear_empty_and_refusals(gkd):
+    w = torch.zeros(8, 16, dtype=BF, device="cuda")
+    assert gkd.linear(torch.zeros(0, 16, dtype=BF, device="cuda"), w).shape == (0, 8)
+    assert gkd.linear(torch.zeros(3, 16, dtype=BF, device="cuda"), w[:0]).shape == (3, 0)
+    x = torch.zeros(4, 16, dtype=BF, device="cuda")
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.linear(x[:1].expand(4, 16), w)
+    assert e.value.status == 2
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.linear(torch.zeros(65, dtype=BF, device="cuda")[1:].view(4, 16), w)
+    assert e.value.status == 7
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.linear(x[:, :15], w[:, :15], workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 4
+    with pytest.raises(ValueError):
+        gkd.linear(x, w, act="tanh")
+    with pytest.raises(ValueError):
+        gkd.linear(x, w, residual=torch.zeros(4, 8, dtype=F32, device="cuda"), out_dtype=BF)
+    with pytest.raises(TypeError):
+        gkd.linear(x.float(), w)
+
+
+# -------------------------------------------------------------------- rope
+def rope_inputs(g, B, T, Hq, Hk, D, rot, A, dtype, far=1000):
+    rows = randn(g, B, T, (Hq + Hk) * D, dtype=dtype)
+    q, k = rows[..., :Hq * D].unflatten(2, (Hq, D)), rows[..., Hq * D:].unflatten(2, (Hk, D))
+    pos = (torch.rand(B, T, A, generator=g, device="cuda") * far).floor()
+    freqs = torch.rand(A, rot // 2, generator=g, device="cuda")
+    wq = randn(g, D, dtype=dtype)
+    wk = randn(g, D, dtype=dtype)
+    return q, k, pos, freqs, wq, wk
+
+
+def check_rope(gkd, B, T, Hq, Hk, D, rot, A, dtype, norm, inter, seed=0, far=1000):
+    print(f"[rope] {B}x{T} {Hq}/{Hk} heads of {D} rot {rot} axes {A} {dtype} norm={norm} inter={inter}",
+          flush=True)
+    q, k, pos, freqs, wq, wk = rope_inputs(rng(seed), B, T, Hq, Hk, D, rot, A, dtype, far)
+    kw = dict(q_weight=wq, k_weight=wk) if norm else {}
+    qo, ko = gkd.qk_norm_rope(q, k, pos, freqs, interleaved=inter, **kw)
+    for x, y, w in ((q, qo, wq), (k, ko, wk)):
+        want, size = ot.rope(np64(x), pos.cpu().numpy(), freqs.cpu().numpy(), np64(w) if norm else None,
+                             1e-6, inter)
+        err = np.abs(np64(y) - want)
+        assert np.all(err <= rounded(want, 2.0 ** -19 * size, dtype)), err.max()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 64), (128, 128), (64, 32), (96, 64), (80, 80), (80, 48), (256, 256),
+                                   (512, 512), (40, 8), (24, 16)])
+def test_rope_head_widths(gkd, dtype, inter, D, rot):
+    check_rope(gkd, 2, 5, 3, 2, D, rot, 2, dtype, True, inter, seed=D)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,rot", [(2, 2), (7, 4), (65, 62), (100, 6), (36, 20), (500, 500), (63, 2)])
+def test_rope_any_width(gkd, dtype, D, rot):
+    """Widths that are no whole 16-byte pieces, one by one."""
+    check_rope(gkd, 2, 3, 2, 1, D, rot, 1, dtype, True, False, seed=D)
+    check_rope(gkd, 1, 3, 1, 2, D, rot, 3, dtype, False, True, seed=D)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hk,A", [(1, 1, 1, 1, 1), (1, 1, 32, 8, 1), (3, 129, 1, 1, 3), (2, 77, 5, 1, 8),
+                                         (1, 700, 16, 16, 2)])
+def test_rope_counts(gkd, B, T, Hq, Hk, A):
+    check_rope(gkd, B, T, Hq, Hk, 64, 64, A, BF, True, False, seed=T)
+    check_rope(gkd, B, T, Hq, Hk, 64, 64, A, BF, False, False, seed=T)
+
+
+def test_rope_far_positions(gkd):
+    """Positions of a million and more keep their angle (float32)."""
+    check_rope(gkd, 1, 50, 2, 1, 64, 64, 1, F32, False, False, far=1 << 23)
+    check_rope(gkd, 1, 50, 2, 1, 66, 64, 2, F32, False, False, far=1 << 23)
+
+
+def test_rope_in_place_shared_table_queries_alone_and_strided_out(gkd):
+    g = rng(5)
+    q, k, pos, freqs, wq, wk = rope_inputs(g, 3, 9, 4, 2, 64, 64, 2, BF)
+    pos = pos[0].contiguous()
+    want = gkd.qk_norm_rope(q, k, pos.expand(3, 9, 2).contiguous(), freqs, wq, wk)
+    alone, none = gkd.qk_norm_rope(q, None, pos, freqs, wq)
+    assert none is None and torch.equal(alone, want[0])
+    # a cache's slots, heads before tokens
+    cache = torch.full((3, 2, 20, 64), 7.0, dtype=BF, device="cuda")
+    view = cache.transpose(1, 2)[:, 4:13]
+    got = gkd.qk_norm_rope(q, k, pos, freqs, wq, wk, k_out=view)
+    assert torch.equal(got[0], want[0]) and torch.equal(view, want[1])
+    assert bool((cache[:, :, :4] == 7).all()) and bool((cache[:, :, 13:] == 7).all())
+    # off 16-byte places: the same values one by one
+    off = torch.empty(3 * 9 * 4 * 64 + 1, dtype=BF, device="cuda")[1:].view(3, 9, 4, 64)
+    off.copy_(q)
+    o2, _ = gkd.qk_norm_rope(off, None, pos, freqs, wq)
+    err = (o2.float() - want[0].float()).abs()
+    assert bool((err <= 2 ** -7 * want[0].float().abs() + 1e-6).all())
+    # in place, both kernels
+    gkd.qk_norm_rope(q, k, pos, freqs, wq, wk, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    gkd.qk_norm_rope(off, None, pos, freqs, wq, q_out=off)
+    assert torch.equal(off, o2)
+
+
+def test_rope_zero_rows_and_refusals(gkd):
+    z = torch.zeros(1, 2, 1, 64, dtype=BF, device="cuda")
+    pos, freqs = torch.zeros(2, 1, device="cuda"), torch.ones(1, 32, device="cuda")
+    w = torch.ones(64, dtype=BF, device="cuda")
+    assert not bool(gkd.qk_norm_rope(z, None, pos, freqs, w)[0].any())     # eps keeps zero rows zero
+    assert gkd.qk_norm_rope(z[:0], None, pos, freqs)[0].shape == (0, 2, 1, 64)
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.qk_norm_rope(z, None, pos, torch.ones(1, 33, device="cuda"))
+    assert e.value.status == 2
+    with pytest.raises(ValueError):
+        gkd.qk_norm_rope(z, None, pos[:1], freqs)
+    with pytest.raises(ValueError):
+        gkd.qk_norm_rope(z.transpose(1, 3), None, pos, freqs)
+    with pytest.raises(TypeError):
+        gkd.qk_norm_rope(z, z.float(), pos, freqs)
+    with pytest.raises(TypeError):
+        gkd.qk_norm_rope(z, None, pos.int(), freqs)
+
+
+# --------------------------------------------------------------- attention
+def attn_inputs(g, B, Tq, Hq, Hk, D, P, S):
+    q = randn(g, B, Tq, Hq, D)
+    kv = randn(g, max(P, 1), 2, Hk, D)[:P]
+    own = randn(g, B, max(S, 1), 2, Hk, D)[:, :S]
+    return q, kv[:, 0], kv[:, 1], own[:, :, 0], own[:, :, 1]
+
+
+def attn_tol(out, mean_abs, worst, D):
+    delta = 36 * 2.0 ** -23 * worst + 1e-5
+    return rounded(out, (2.0 ** -8 + 2 * delta) * mean_abs, BF)
+
+
+def check_attn(gkd, B, Tq, Hq, Hk, D, P, S, own_len=None, q_len=None, mask=None, causal=False, scale=None,
+               seed=0):
+    print(f"[attn] B={B} Tq={Tq} {Hq}/{Hk} of {D} P={P} S={S} own_len={own_len} q_len={q_len} "
+          f"mask={mask is not None} causal={causal}", flush=True)
+    g = rng(seed)
+    q, kp, vp, ko, vo = attn_inputs(g, B, Tq, Hq, Hk, D, P, S)
+    dev = lambda v: None if v is None else torch.tensor(v, dtype=torch.int32, device="cuda")
+    out = torch.full((B, Tq, Hq, D), 7.0, dtype=BF, device="cuda")
+    got = gkd.prefix_attention(q, kp if P else None, vp if P else None, ko if S else None, vo if S else None,
+                               own_len=dev(own_len), q_len=dev(q_len), own_mask=mask, causal=causal,
+                               scale=scale, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    want, mean_abs, worst = ot.prefix_attention(
+        *(np64(t) for t in (q, kp, vp, ko, vo)), own_len, q_len, None if mask is None else mask.cpu().numpy(),
+        causal, scale)
+    y = np64(out)
+    if q_len is not None:       # rows not asked for stay as they were
+        for b, n in enumerate(q_len):
+            assert (y[b, min(max(n, 0), Tq):] == 7).all()
+            y[b, min(max(n, 0), Tq):] = 0
+    err = np.abs(y - want)
+    assert np.all(err <= attn_tol(want, mean_abs, worst, D)), err.max()
+
+
+def masks(seed, B, S, p=0.6):
+    return (torch.rand(B, S, generator=rng(seed), device="cuda") < p).to(torch.uint8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(4, 4), (4, 2), (7, 1)])
+@pytest.mark.parametrize("P,S", [(1, 1), (63, 65), (64, 64), (130, 0), (0, 130), (200, 31), (17, 257)])
+@pytest.mark.parametrize("B,Tq", [(1, 1), (3, 1), (2, 5), (2, 70)])
+def test_attention_shapes(gkd, D, Hq, Hk, P, S, B, Tq):
+    check_attn(gkd, B, Tq, Hq, Hk, D, P, S, seed=P + S)
+
+
+@pytest.mark.parametrize("D,Hq,Hk", [(64, 4, 2), (128, 6, 2)])
+@pytest.mark.parametrize("Tq", [1, 3, 40, 90])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("P", [0, 150])
+def test_attention_ragged_masked(gkd, D, Hq, Hk, Tq, causal, P):
+    S = 140
+    own_len = [140, Tq, 0, 77, 200, -3]
+    q_len = [Tq, max(Tq - 2, 0), Tq, 1, Tq + 9, 0]
+    check_attn(gkd, 6, Tq, Hq, Hk, D, P, S, own_len, q_len, masks(1, 6, S), causal, seed=Tq)
+    check_attn(gkd, 6, Tq, Hq, Hk, D, P, S, own_len, None, None, causal, seed=Tq)
+
+
+def test_attention_rows_without_keys_are_zero(gkd):
+    m = torch.ones(3, 20, dtype=torch.uint8, device="cuda")
+    m[1] = 0
+    for Tq in (1, 2, 70):
+        check_attn(gkd, 3, Tq, 4, 2, 64, 0, 20, [20, 20, 0], None, m)
+        check_attn(gkd, 3, Tq, 4, 2, 64, 0, 20, [1, 0, 20], None, None, True)
+
+
+@pytest.mark.parametrize("Tq", [1, 4, 70])
+def test_attention_hidden_places_may_hold_anything(gkd, Tq):
+    """NaN and infinities past own_len, under the mask and past q_len."""
+    g = rng(11)
+    B, Hq, Hk, D, P, S = 3, 4, 2, 128, 70, 100
+    q, kp, vp, ko, vo = attn_inputs(g, B, Tq, Hq, Hk, D, P, S)
+    own_len = torch.tensor([100, 33, 0], dtype=torch.int32, device="cuda")
+    q_len = torch.tensor([Tq, max(1, Tq - 1), Tq], dtype=torch.int32, device="cuda")
+    m = masks(2, B, S)
+    kw = dict(own_len=own_len, q_len=q_len, own_mask=m)
+    want = gkd.prefix_attention(q, kp, vp, ko, vo, out=torch.zeros_like(q), **kw)
+    hidden = (m == 0) | (torch.arange(S, device="cuda") >= own_len[:, None])
+    ko, vo, q = ko.clone(), vo.clone(), q.clone()
+    ko[hidden], vo[hidden] = float("nan"), float("inf")
+    vo[..., ::2][hidden] = float("nan")
+    q[torch.arange(Tq, device="cuda") >= q_len[:, None]] = float("nan")
+    got = gkd.prefix_attention(q, kp, vp, ko, vo, out=torch.zeros_like(q), **kw)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("B,Tq,Hq,Hk,D,P,S", [(5, 1, 8, 2, 128, 4000, 300), (2, 33, 4, 4, 64, 2304, 80),
+                                              (1, 1, 16, 16, 64, 576, 80), (1, 2, 8, 1, 128, 9000, 64),
+                                              (2, 260, 2, 1, 128, 700, 300)])
+def test_attention_split_ranges(gkd, B, Tq, Hq, Hk, D, P, S):
+    check_attn(gkd, B, Tq, Hq, Hk, D, P, S, [S - 7 * b for b in range(B)], None, None, True, seed=P)
+
+
+def test_attention_large_scores_and_scales(gkd):
+    """Scores that jump by hundreds from chunk to chunk; a small and a large scale."""
+    g = rng(9)
+    q, kp, vp, ko, vo = attn_inputs(g, 2, 3, 4, 2, 64, 300, 100)
+    kp = kp * torch.linspace(0.1, 12, 300, device="cuda").to(BF)[:, None, None]
+    for scale in (1.0, 1e-6):
+        got = np64(gkd.prefix_attention(q, kp, vp, ko, vo, scale=scale))
+        want, mean_abs, worst = ot.prefix_attention(*(np64(t) for t in (q, kp, vp, ko, vo)), scale=scale)
+        err = np.abs(got - want)
+        assert np.all(err <= attn_tol(want, mean_abs, worst, 64)), err.max()
+
+
+def test_attention_repeats_exactly_and_on_another_stream(gkd):
+    g = rng(21)
+    q, kp, vp, ko, vo = attn_inputs(g, 7, 1, 8, 2, 128, 3000, 200)
+    a = gkd.prefix_attention(q, kp, vp, ko, vo)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        b = gkd.prefix_attention(q, kp, vp, ko, vo)
+    st.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_attention_long_cache_past_32_bit_offsets(gkd):
+    """A token stride that puts the last keys more than 2^32 elements away."""
+    S, stride = 70, 1 << 26          # 70 tokens, 2^26 elements apart: 9.4 GB of keys
+    g = rng(2)
+    ko = torch.zeros(S * stride, dtype=BF, device="cuda").view(1, S, stride)[:, :, :128].unflatten(2, (1, 128))
+    src = randn(g, 1, S, 1, 128)
+    ko.copy_(src)
+    vo = randn(g, 1, S, 1, 128)
+    q = randn(g, 1, 1, 2, 128)
+    got = gkd.prefix_attention(q, None, None, ko, vo)
+    want = gkd.prefix_attention(q, None, None, src, vo)
+    assert torch.equal(got, want)
+
+
+def test_attention_refusals(gkd):
+    q = torch.zeros(2, 3, 4, 64, dtype=BF, device="cuda")
+    kv = torch.zeros(5, 2, 64, dtype=BF, device="cuda")
+    for bad in (dict(k_prefix=kv), dict(), dict(k_prefix=kv, v_prefix=kv[:4])):
+        with pytest.raises(ValueError):
+            gkd.prefix_attention(q, **bad)
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.prefix_attention(q[:, :, :3], kv, kv)
+    assert e.value.status == 5
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.prefix_attention(q, kv, kv, scale=0.0)
+    assert e.value.status == 4
+    with pytest.raises(TypeError):
+        gkd.prefix_attention(q, kv, kv, own_len=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(TypeError):
+        gkd.prefix_attention(q.float(), kv, kv)
+
+
+# ------------------------------------------------------------ together
+def test_a_block_over_image_tokens_and_prompt_rows(gkd):
+    """A pre-projection block as a user builds it: image tokens give the
+    shared keys, prompt sets attend to them and to their own rows, and a
+    feed-forward pair follows, with a float32 residual stream; then the
+    rows go to the heatmap call as kernels over the same tokens. Compared
+    stage by stage with the oracle on the stage's own inputs."""
+    B, R, C, H, W, Hq, Hk, D, F = 3, 12, 256, 6, 8, 4, 2, 64, 320
+    g = rng(77)
+    tokens = randn(g, 1, 5 + H * W, C)
+    rows = randn(g, B, R, C)
+    valid = masks(3, B, R, 0.7)
+    wq, wkv = randn(g, Hq * D, C, scale=C ** -0.5), randn(g, 2 * Hk * D, C, scale=C ** -0.5)
+    wo, w1, w2 = (randn(g, *s, scale=s[1] ** -0.5) for s in ((C, Hq * D), (F, C), (C, F)))
+    bq, bkv, bo, b1, b2 = (randn(g, n, scale=0.1) for n in (Hq * D, 2 * Hk * D, C, F, C))
+    gq, gk = (1 + 0.1 * randn(g, D, dtype=F32)).to(BF), (1 + 0.1 * randn(g, D, dtype=F32)).to(BF)
+    # two axes; class and storage tokens and prompt rows have no place
+    yx = torch.stack(torch.meshgrid(torch.arange(H), torch.arange(W), indexing="ij"), -1).reshape(-1, 2)
+    pos = torch.cat([torch.zeros(5, 2), yx.float()]).cuda()
+    base = 100.0 ** (-torch.arange(16) / 16)
+    freqs = torch.zeros(2, 32)
+    freqs[0, :16], freqs[1, 16:] = base, base
+    freqs, none = freqs.cuda(), torch.zeros(R, 2, device="cuda")
+
+    def run():
+        kv = gkd.linear(tokens, wkv, bias=bkv).unflatten(2, (2, Hk, D))
+        own = gkd.linear(rows, wkv, bias=bkv).unflatten(2, (2, Hk, D))
+        q = gkd.linear(rows, wq, bias=bq).unflatten(2, (Hq, D))
+        _, kp = gkd.qk_norm_rope(kv[:, :, 0], kv[:, :, 0], pos, freqs, None, gk)
+        q, ko = gkd.qk_norm_rope(q, own[:, :, 0], none, freqs, gq, gk)
+        o = gkd.prefix_attention(q, kp[0], kv[0, :, 1], ko, own[:, :, 1], own_mask=valid)
+        x = gkd.linear(o.flatten(2), wo, bias=bo, residual=rows.float())
+        h = gkd.linear(x.to(BF), w1, bias=b1, act="gelu")
+        y = gkd.linear(h, w2, bias=b2, residual=x, out=torch.empty_like(x))
+        return kv, own, q, kp, ko, o, x, h, y
+
+    kv, own, q, kp, ko, o, x, h, y = run()
+    heat, (idx, _, score) = gkd.kernel_heatmap(tokens.expand(B, -1, -1).contiguous(), kern_txt=y.to(BF),
+                                               mask_txt=valid, token_hw=(H, W), token_skip=5)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(score[valid > 0]).all()) and bool((idx[valid > 0] >= 0).all())
+
+    def lin(got, xin, w, b, act="none", r=None):
+        want, size = ot.linear(np64(xin).reshape(-1, xin.shape[-1]), np64(w), np64(b),
+                               None if r is None else np64(r).reshape(-1, w.shape[0]), act)
+        err = np.abs(np64(got).reshape(want.shape) - want)
+        assert np.all(err <= linear_tol(want, size, w.shape[1], got.dtype,
+                                        None if r is None else np64(r).reshape(want.shape)))
+    lin(kv.flatten(2), tokens, wkv, bkv)
+    lin(own.flatten(2), rows, wkv, bkv)
+    want, size = ot.rope(np64(kv[:, :, 0]), pos[None].cpu().numpy(), freqs.cpu().numpy(), np64(gk))
+    assert np.all(np.abs(np64(kp) - want) <= rounded(want, 2.0 ** -19 * size, BF))
+    want, mean_abs, worst = ot.prefix_attention(np64(q), np64(kp[0]), np64(kv[0, :, 1]), np64(ko),
+                                                np64(own[:, :, 1]), own_mask=valid.cpu().numpy())
+    assert np.all(np.abs(np64(o) - want) <= attn_tol(want, mean_abs, worst, D))
+    lin(x, o.flatten(2), wo, bo, r=rows)
+    lin(h, x.to(BF), w1, b1, "gelu")
+    lin(y, h, w2, b2, r=x)
+
+    # the same run captured and replayed on new inputs, with eager work between
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = run()[-1]
+    for seed in (1, 2, 3):
+        tokens.copy_(randn(rng(seed), *tokens.shape))
+        rows.copy_(randn(rng(seed + 50), *rows.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res, run()[-1])
+
+
+def test_two_captured_graphs_and_eager_calls_do_not_share_a_workspace(gkd):
+    """Calls without a workspace argument get one each, in a graph too."""
+    g = rng(8)
+    sets = [attn_inputs(g, 6, 1, 8, 2, 64, 1500, 100) for _ in range(2)]
+    want = [gkd.prefix_attention(*s) for s in sets]
+    graphs, outs = [], []
+    for s in sets:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(gkd.prefix_attention(*s))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for st, gr in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                gr.replay()
+        gkd.prefix_attention(*sets[0])
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
