@@ -13,6 +13,8 @@
 #include "gkdtokens.h"
 #include "tokens_launch.hpp"
 
+#include <type_traits>
+
 namespace gkd {
 namespace {
 
@@ -27,7 +29,7 @@ struct LinParams {
   int M, N, K;         // K a multiple of 8
   int act;
   int out_f32;
-  int vec_out, vec_res;  // four adjacent columns are one aligned piece
+  int vec;             // finish() may move whole pieces
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -41,72 +43,103 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 
-// erf to 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical Functions,
-// 7.1.26): below a float32 step of the activations that use it.
-__device__ __forceinline__ float erf_as(float x) {
-  const float a = fabsf(x);
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, a, 1.f));
-  float y = fmaf(1.061405429f, t, -1.453152027f);
-  y = fmaf(y, t, 1.421413741f);
-  y = fmaf(y, t, -0.284496736f);
-  y = fmaf(y, t, 0.254829592f);
-  const float e = 1.f - y * t * __builtin_amdgcn_exp2f(-1.4426950408889634f * a * a);
-  return copysignf(e, x);
+// z Phi(z), Phi(-|z|) = erfc(|z| / sqrt 2) / 2 from Abramowitz and Stegun,
+// Handbook of Mathematical Functions, 7.1.26 (erf to 1.5e-7): z Phi(z) =
+// max(z, 0) - |z| Phi(-|z|), which needs no sign of erf and loses nothing for
+// z far below 0. 12 VALU operations and two quarter-rate ones.
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fabsf(z);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, a, 1.f));
+  float y = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  y = fmaf(y, t, 0.5f * 1.421413741f);
+  y = fmaf(y, t, 0.5f * -0.284496736f);
+  y = fmaf(y, t, 0.5f * 0.254829592f);
+  const float e = __builtin_amdgcn_exp2f(-0.5f * 1.4426950408889634f * z * z);
+  const float q = y * t * e;  // Phi(-|z|)
+  // where Phi is 0 the product is 0, also for an infinite a
+  return (z < 0.f ? 0.f : z) - (q > 0.f ? a * q : q);
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == GKD_ACT_RELU) return z < 0.f ? 0.f : z;  // a NaN stays one
+  if constexpr (ACT == GKD_ACT_GELU) return gelu(z);
+  // z / (1 + exp(-c z)): for z far below 0 exp gives infinity and the quotient 0
+  if constexpr (ACT == GKD_ACT_QUICK_GELU)
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.702f * 1.4426950408889634f * z));
+  if constexpr (ACT == GKD_ACT_SILU)
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
+  return z;
+}
+
+// Calls f with the activation as a compile-time constant.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
   switch (act) {
-    case GKD_ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
-    case GKD_ACT_GELU: return 0.5f * z * (1.f + erf_as(z * 0.70710678118654752f));
-    // z / (1 + exp(-c z)): for z very negative exp gives infinity and the quotient 0
-    case GKD_ACT_QUICK_GELU:
-      return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.702f * 1.4426950408889634f * z));
-    case GKD_ACT_SILU:
-      return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
-    default: return z;
+    case GKD_ACT_RELU: f(std::integral_constant<int, GKD_ACT_RELU>{}); break;
+    case GKD_ACT_GELU: f(std::integral_constant<int, GKD_ACT_GELU>{}); break;
+    case GKD_ACT_QUICK_GELU: f(std::integral_constant<int, GKD_ACT_QUICK_GELU>{}); break;
+    case GKD_ACT_SILU: f(std::integral_constant<int, GKD_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, GKD_ACT_NONE>{}); break;
   }
 }
 
-// Bias, activation, residual and the store of columns n .. n + 3 of row m
-// (m < M; columns past N are left out).
-__device__ __forceinline__ void finish(const LinParams& p, int m, int n, f32x4 v) {
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// bias[n .. n + W), zeros without one and past N
+template <int W>
+__device__ __forceinline__ void load_bias(const LinParams& p, int n, float (&b)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; ++e) b[e] = p.bias && n + e < p.N ? bf16_bits_to_f32(p.bias[n + e]) : 0.f;
+}
+
+// Bias, activation, residual and the store of the W (4 or 8) columns from n
+// of row m < M; columns past N are left out. Whole pieces where the rows
+// allow it (p.vec: W adjacent columns are aligned in out and residual), else
+// one by one.
+template <int ACT, int W>
+__device__ __forceinline__ void finish(const LinParams& p, int m, int n, float (&v)[W], const float (&b)[W]) {
   if (n >= p.N) return;
   const long long o = (long long)m * p.ldo + n, r = (long long)m * p.ldr + n;
-  if (n + 4 <= p.N && p.vec_out && (p.res == nullptr || p.vec_res)) {
-    if (p.bias) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += bf16_bits_to_f32(p.bias[n + e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = activate(v[e], p.act);
+  for (int e = 0; e < W; ++e) v[e] = activate<ACT>(v[e] + b[e]);
+  if (n + W <= p.N && p.vec) {
     if (p.out_f32) {
-      if (p.res) v += *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.res) + r);
-      *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o) = v;
-    } else {
-      if (p.res) {
-        const u32x2 q = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p.res) + r);
-        v += f32x4{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xffff0000u),
-                   __uint_as_float(q[1] << 16), __uint_as_float(q[1] & 0xffff0000u)};
+#pragma unroll
+      for (int q = 0; q < W / 4; ++q) {
+        f32x4 t = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+        if (p.res) t += *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.res) + r + 4 * q);
+        *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o + 4 * q) = t;
       }
-      const bf16x2 lo = {static_cast<__bf16>(v[0]), static_cast<__bf16>(v[1])};
-      const bf16x2 hi = {static_cast<__bf16>(v[2]), static_cast<__bf16>(v[3])};
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + o) =
-          u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    } else {
+      typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+      if (p.res) {
+        const words q = *reinterpret_cast<const words*>(static_cast<const uint16_t*>(p.res) + r);
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) {
+          v[2 * e] += __uint_as_float(q[e] << 16);
+          v[2 * e + 1] += __uint_as_float(q[e] & 0xffff0000u);
+        }
+      }
+      words t;
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e) t[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
+      *reinterpret_cast<words*>(static_cast<uint16_t*>(p.out) + o) = t;
     }
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < W; ++e) {
     if (n + e >= p.N) break;
-    float z = v[e];
-    if (p.bias) z += bf16_bits_to_f32(p.bias[n + e]);
-    z = activate(z, p.act);
     if (p.out_f32) {
-      if (p.res) z += static_cast<const float*>(p.res)[r + e];
-      static_cast<float*>(p.out)[o + e] = z;
+      if (p.res) v[e] += static_cast<const float*>(p.res)[r + e];
+      static_cast<float*>(p.out)[o + e] = v[e];
     } else {
-      if (p.res) z += bf16_bits_to_f32(static_cast<const uint16_t*>(p.res)[r + e]);
-      static_cast<uint16_t*>(p.out)[o + e] = f32_to_bf16_bits(z);
+      if (p.res) v[e] += bf16_bits_to_f32(static_cast<const uint16_t*>(p.res)[r + e]);
+      static_cast<uint16_t*>(p.out)[o + e] = f32_to_bf16_bits(v[e]);
     }
   }
 }
@@ -202,13 +235,255 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinParams p) 
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
     }
   }
+  with_act(p.act, [&](auto act) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = m0 + wm0 + 16 * i + fr;
-    if (m >= p.M) continue;
+    for (int j = 0; j < NT; ++j) {
+      const int n = n0 + wn0 + 16 * j + 4 * g;
+      float b[4];
+      load_bias(p, n, b);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) finish(p, m, n0 + wn0 + 16 * j + 4 * g, acc[i][j]);
+      for (int i = 0; i < MT; ++i) {
+        const int m = m0 + wm0 + 16 * i + fr;
+        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if (m < p.M) finish<act, 4>(p, m, n, v, b);
+      }
+    }
+  });
+}
+
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles, K in steps of 64: eight waves of 128 x 64, two on each
+// SIMD, which take turns: while one runs the 16 MFMAs of a phase, the other
+// reads the LDS operands of its own next phase, so the matrix pipe does not
+// wait for LDS. Waves 4..7 run one barrier behind waves 0..3 for that.
+//
+// A step of K is four phases; the x rows (A) and w rows (B) of the tile are
+// halves A0, A1, B0, B1 of 128 rows, of which a wave owns 64 and 32:
+//   phase       1        2        3        4
+//   reads       A0       B1       A1       B0 of the next step
+//   product     A0 B0    A0 B1    A1 B0    A1 B1
+//   loads       A1 s+1   B0 s+2   A0 s+2   B1 s+2     (of step s, into LDS)
+// LDS holds two steps (128 KB). A half is overwritten two phases after its
+// last read (the late waves' operands are in registers by then) and is
+// waited for, with ten younger loads of the wave still flying, one phase and
+// a barrier before its first read: a load has five phases to land.
+//
+// Piece c of an A row r sits at place c ^ (r & 7). A lane's operand row of w
+// is 8 (fr / 4) + fr % 4 (+ 4 in the second tile of a pair), so that it ends
+// with eight adjacent columns; piece c of a B row sits at
+// c ^ (r & 3 | (r & 8) / 2), which spreads those rows over the banks.
+// ---------------------------------------------------------------------------
+constexpr int kHalfBytes = 128 * kBK * 2;
+
+__device__ __forceinline__ void phase_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm_here() {
+  asm volatile("" ::: "memory");
+  wait_vm<N>();
+  asm volatile("" ::: "memory");
+}
+
+// s_waitcnt lgkmcnt(0), the other counters left alone
+__device__ __forceinline__ void wait_lds_here() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
+}
+
+__global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15, g = lane >> 4;
+  const int wm = wave >> 2, wn = wave & 3;
+  const int tiles_n = (p.N + 255) / 256;
+  const int total = gridDim.x;
+  const int bid = blockIdx.x, xcd = bid % kXcds, qx = total / kXcds, rem = total % kXcds;
+  const int lin = xcd * qx + min(xcd, rem) + bid / kXcds;
+  const int m0 = (lin / tiles_n) * 256, n0 = (lin % tiles_n) * 256;
+  const char* xb = reinterpret_cast<const char*>(p.x + (long long)m0 * p.ldx);
+  const char* wb = reinterpret_cast<const char*>(p.w + (long long)n0 * p.ldw);
+
+  // byte offsets of the pieces this lane loads: halves A0, A1, B0, B1
+  const int lr = lane >> 3;
+  const int acol = (lane & 7) ^ lr, bcol = (lane & 7) ^ ((lr & 3) | ((wave & 1) << 2));
+  uint32_t off[4][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = h * 128 + (wave + 8 * i) * 8 + lr;
+      off[h][i] = (uint32_t)(min(r, p.M - 1 - m0) * p.ldx + 8 * acol) * 2u;
+      off[2 + h][i] = (uint32_t)(min(r, p.N - 1 - n0) * p.ldw + 8 * bcol) * 2u;
+    }
+  const int nk = (p.K + kBK - 1) / kBK;
+  // the last step's pieces past K load the row's last one instead
+  const int left = p.K - (nk - 1) * kBK;
+  const int aback = max(8 * acol - (left - 8), 0) * 2, bback = max(8 * bcol - (left - 8), 0) * 2;
+  auto load = [&](int h, int step) {
+    const char* base = (h < 2 ? xb : wb) + (long long)step * (kBK * 2);
+    const uint32_t back = step == nk - 1 ? (uint32_t)(h < 2 ? aback : bback) : 0u;
+    unsigned char* dst = lds + (step & 1) * (4 * kHalfBytes) + h * kHalfBytes + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_global_load_lds((glb_void*)(base + (off[h][i] - back)), (lds_void*)(dst + i * 8192), 16, 0, 0);
+  };
+
+  f32x4 acc[2][4][2][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) acc[a][i][b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int ar = wm * 64 + fr, br = wn * 32 + 8 * (fr >> 2) + (fr & 3);
+  const int aaddr = ar * 128 + ((g ^ (ar & 7)) << 4);
+  const int baddr = br * 128 + ((g ^ ((br & 3) | ((br & 8) >> 1))) << 4);
+  bf16x8 fa[2][4], fb[2][2][2];  // [K half][tile], [B half][K half][tile]
+  auto piece = [&](int at, int c, bool last) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + at);
+    return frag(!last || 8 * c < left ? v : u32x4{0u, 0u, 0u, 0u});
+  };
+  auto read_a = [&](int half, int step, bool last) {
+    const int st = (step & 1) * (4 * kHalfBytes) + half * kHalfBytes;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[k][i] = piece(st + (aaddr ^ (k << 6)) + i * 2048, 4 * k + g, last);
+  };
+  auto read_b = [&](int half, int step, bool last) {
+    const int st = (step & 1) * (4 * kHalfBytes) + (2 + half) * kHalfBytes;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) fb[half][k][t] = piece(st + (baddr ^ (k << 6)) + t * 512, 4 * k + g, last);
+  };
+  auto product = [&](int a, int b) {
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[a][i][b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[b][k][t], fa[k][i], acc[a][i][b][t], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  };
+
+  // the first two steps' halves, in the order the loop goes on with
+  load(2, 0);
+  load(0, 0);
+  load(3, 0);
+  load(1, 0);
+  if (nk > 1) {
+    load(2, 1);
+    load(0, 1);
+    load(3, 1);
+    wait_vm_here<10>();
+  } else {
+    wait_vm_here<0>();
   }
+  phase_barrier();
+  read_b(0, 0, nk == 1);
+  if (wm == 1) phase_barrier();
+
+  int s = 0;
+  for (; s + 2 < nk; ++s) {
+    read_a(0, s, false);
+    load(1, s + 1);
+    wait_vm_here<10>();
+    phase_barrier();
+    product(0, 0);
+    phase_barrier();
+    read_b(1, s, false);
+    load(2, s + 2);
+    wait_vm_here<10>();
+    phase_barrier();
+    product(0, 1);
+    phase_barrier();
+    read_a(1, s, false);
+    load(0, s + 2);
+    wait_vm_here<10>();
+    phase_barrier();
+    product(1, 0);
+    phase_barrier();
+    read_b(0, s + 1, false);
+    load(3, s + 2);
+    wait_vm_here<10>();
+    phase_barrier();
+    product(1, 1);
+    wait_lds_here();  // the next step's B0 is out of LDS before it may be overwritten
+    phase_barrier();
+  }
+  if (nk > 1) {  // the last step but one
+    read_a(0, s, false);
+    load(1, s + 1);
+    wait_vm_here<10>();
+    phase_barrier();
+    product(0, 0);
+    phase_barrier();
+    read_b(1, s, false);
+    wait_vm_here<8>();
+    phase_barrier();
+    product(0, 1);
+    phase_barrier();
+    read_a(1, s, false);
+    wait_vm_here<6>();
+    phase_barrier();
+    product(1, 0);
+    phase_barrier();
+    read_b(0, s + 1, true);
+    wait_vm_here<4>();
+    phase_barrier();
+    product(1, 1);
+    phase_barrier();
+    ++s;
+  }
+  read_a(0, s, true);
+  wait_vm_here<2>();
+  phase_barrier();
+  product(0, 0);
+  phase_barrier();
+  read_b(1, s, true);
+  wait_vm_here<0>();
+  phase_barrier();
+  product(0, 1);
+  phase_barrier();
+  read_a(1, s, true);
+  phase_barrier();
+  product(1, 0);
+  product(1, 1);
+  if (wm == 0) phase_barrier();
+
+  // lane (fr, g) holds columns 8 g .. 8 g + 7 of row fr of each 16 x 32 pair
+  with_act(p.act, [&](auto act) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int n = n0 + b * 128 + wn * 32 + 8 * g;
+      float bias[8];
+      load_bias(p, n, bias);
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = m0 + a * 128 + wm * 64 + 16 * i + fr;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = acc[a][i][b][e >> 2][e & 3];
+          if (m < p.M) finish<act, 8>(p, m, n, v, bias);
+        }
+    }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -253,8 +528,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinParams p)
     f32x4 s = part[0][i][lane];
 #pragma unroll
     for (int v = 1; v < kFewWaves; ++v) s += part[v][i][lane];
-    const int m = 16 * i + fr;
-    if (m < p.M) finish(p, m, n0 + 4 * g, s);
+    const int m = 16 * i + fr, n = n0 + 4 * g;
+    float b[4], v[4] = {s[0], s[1], s[2], s[3]};
+    load_bias(p, n, b);
+    if (m < p.M) with_act(p.act, [&](auto act) { finish<act, 4>(p, m, n, v, b); });
   }
 }
 
@@ -319,9 +596,10 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   p.K = up8(a.K);
   p.act = a.act;
   p.out_f32 = a.out_f32;
-  const unsigned mask = a.out_f32 ? 15u : 7u;
-  p.vec_out = (reinterpret_cast<uintptr_t>(a.out) & mask) == 0 && a.ldo % 4 == 0;
-  p.vec_res = (reinterpret_cast<uintptr_t>(a.residual) & mask) == 0 && a.ldr % 4 == 0;
+  // 16-byte pieces: eight bf16 columns (the 4-column kernels need half), four float32 ones
+  const int unit = a.out_f32 ? 4 : 8;
+  p.vec = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.residual)) & 15u) == 0 &&
+          a.ldo % unit == 0 && (a.residual == nullptr || a.ldr % unit == 0);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   auto pack = [&](const uint16_t*& src, int& ld, int rows) -> hipError_t {
     uint16_t* dst = reinterpret_cast<uint16_t*>(ws);
@@ -340,7 +618,11 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   if (p.M <= 16) return run_few<1>(p, st);
   if (p.M <= 32) return run_few<2>(p, st);
   if (p.M <= 64) return run_few<4>(p, st);
-  if ((long long)p.M * p.N >= 256LL * 256 * 256) return run_tiles<256, 256, 2, 4>(p, st);
+  if ((long long)p.M * p.N >= 256LL * 256 * 256) {
+    const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
+    hipLaunchKernelGGL(linear_turn_kernel, dim3((unsigned)tiles), dim3(512), 8 * kHalfBytes, st, p);
+    return hipGetLastError();
+  }
   return run_tiles<128, 128, 2, 2>(p, st);
 }
 
