@@ -43,21 +43,22 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
 }
 
-// z Phi(z), Phi(-|z|) = erfc(|z| / sqrt 2) / 2 from Abramowitz and Stegun,
-// Handbook of Mathematical Functions, 7.1.26 (erf to 1.5e-7): z Phi(z) =
-// max(z, 0) - |z| Phi(-|z|), which needs no sign of erf and loses nothing for
-// z far below 0. 12 VALU operations and two quarter-rate ones.
+// z Phi(z) = max(z, 0) - |z| Phi(-|z|) with Phi(-a) = 2^P(a): log2 Phi(-a) is
+// smooth, so a polynomial of degree 7 (minimax on 0..6.5, fitted with the
+// error weighted as it enters the result) leaves 1.8e-7 of error in z Phi(z)
+// and, as a factor, keeps 5e-5 relative in the tail down to z = -6; further
+// out P falls on without bound and the tail goes to 0. 11 VALU operations and
+// one quarter-rate one.
 __device__ __forceinline__ float gelu(float z) {
-  const float a = fabsf(z);
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678118654752f, a, 1.f));
-  float y = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
-  y = fmaf(y, t, 0.5f * 1.421413741f);
-  y = fmaf(y, t, 0.5f * -0.284496736f);
-  y = fmaf(y, t, 0.5f * 0.254829592f);
-  const float e = __builtin_amdgcn_exp2f(-0.5f * 1.4426950408889634f * z * z);
-  const float q = y * t * e;  // Phi(-|z|)
-  // where Phi is 0 the product is 0, also for an infinite a
-  return (z < 0.f ? 0.f : z) - (q > 0.f ? a * q : q);
+  const float a = fminf(fabsf(z), 64.f);  // Phi(-64) is 0 in float32
+  float y = fmaf(-1.61419405e-06f, a, 5.75573977e-05f);
+  y = fmaf(y, a, -0.000903298729f);
+  y = fmaf(y, a, 0.00842618756f);
+  y = fmaf(y, a, -0.053858351f);
+  y = fmaf(y, a, -0.458490729f);
+  y = fmaf(y, a, -1.15127611f);
+  y = fmaf(y, a, -0.999987483f);
+  return fmaf(-a, __builtin_amdgcn_exp2f(y), z < 0.f ? 0.f : z);
 }
 
 template <int ACT>
@@ -96,6 +97,34 @@ __device__ __forceinline__ void load_bias(const LinParams& p, int n, float (&b)[
   for (int e = 0; e < W; ++e) b[e] = p.bias && n + e < p.N ? bf16_bits_to_f32(p.bias[n + e]) : 0.f;
 }
 
+// The residual and the store of W columns in whole pieces, at elements o
+// (out) and r (residual).
+template <int W>
+__device__ __forceinline__ void finish_pieces(const LinParams& p, long long o, long long r, float (&v)[W]) {
+  if (p.out_f32) {
+#pragma unroll
+    for (int q = 0; q < W / 4; ++q) {
+      f32x4 t = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      if (p.res) t += *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.res) + r + 4 * q);
+      *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o + 4 * q) = t;
+    }
+  } else {
+    typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+    if (p.res) {
+      const words q = *reinterpret_cast<const words*>(static_cast<const uint16_t*>(p.res) + r);
+#pragma unroll
+      for (int e = 0; e < W / 2; ++e) {
+        v[2 * e] += __uint_as_float(q[e] << 16);
+        v[2 * e + 1] += __uint_as_float(q[e] & 0xffff0000u);
+      }
+    }
+    words t;
+#pragma unroll
+    for (int e = 0; e < W / 2; ++e) t[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
+    *reinterpret_cast<words*>(static_cast<uint16_t*>(p.out) + o) = t;
+  }
+}
+
 // Bias, activation, residual and the store of the W (4 or 8) columns from n
 // of row m < M; columns past N are left out. Whole pieces where the rows
 // allow it (p.vec: W adjacent columns are aligned in out and residual), else
@@ -107,28 +136,7 @@ __device__ __forceinline__ void finish(const LinParams& p, int m, int n, float (
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = activate<ACT>(v[e] + b[e]);
   if (n + W <= p.N && p.vec) {
-    if (p.out_f32) {
-#pragma unroll
-      for (int q = 0; q < W / 4; ++q) {
-        f32x4 t = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-        if (p.res) t += *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.res) + r + 4 * q);
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o + 4 * q) = t;
-      }
-    } else {
-      typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
-      if (p.res) {
-        const words q = *reinterpret_cast<const words*>(static_cast<const uint16_t*>(p.res) + r);
-#pragma unroll
-        for (int e = 0; e < W / 2; ++e) {
-          v[2 * e] += __uint_as_float(q[e] << 16);
-          v[2 * e + 1] += __uint_as_float(q[e] & 0xffff0000u);
-        }
-      }
-      words t;
-#pragma unroll
-      for (int e = 0; e < W / 2; ++e) t[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
-      *reinterpret_cast<words*>(static_cast<uint16_t*>(p.out) + o) = t;
-    }
+    finish_pieces<W>(p, o, r, v);
     return;
   }
 #pragma unroll
@@ -268,12 +276,24 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinParams p) 
 // waited for, with ten younger loads of the wave still flying, one phase and
 // a barrier before its first read: a load has five phases to land.
 //
+// A workgroup stays on its CU and takes tile after tile: the first halves of
+// the next tile are loaded before the finished one goes through its epilogue,
+// whose 16 or more stores per wave then drain under the next tile's first
+// five phases (their waits count those 16 too; where a tile ends the matrix
+// and the stores are not counted, the epilogue ends with an empty queue).
+// The tiles of an XCD are taken in bands of 8 rows of tiles, columns outside:
+// the 32 tiles that its CUs work on at a time share 8 x-bands and 4 w-bands
+// in its L2.
+//
 // Piece c of an A row r sits at place c ^ (r & 7). A lane's operand row of w
 // is 8 (fr / 4) + fr % 4 (+ 4 in the second tile of a pair), so that it ends
 // with eight adjacent columns; piece c of a B row sits at
 // c ^ (r & 3 | (r & 8) / 2), which spreads those rows over the banks.
 // ---------------------------------------------------------------------------
 constexpr int kHalfBytes = 128 * kBK * 2;
+constexpr int kTurnCus = 256;     // one workgroup a CU: its LDS and registers fill it
+constexpr int kTurnBand = 8;      // rows of tiles in a band
+constexpr int kTurnMinSteps = 5;  // two steps after a tile's start and three before its end are apart
 
 __device__ __forceinline__ void phase_barrier() {
   asm volatile("" ::: "memory");
@@ -303,49 +323,72 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, g = lane >> 4;
   const int wm = wave >> 2, wn = wave & 3;
-  const int tiles_n = (p.N + 255) / 256;
-  const int total = gridDim.x;
-  const int bid = blockIdx.x, xcd = bid % kXcds, qx = total / kXcds, rem = total % kXcds;
-  const int lin = xcd * qx + min(xcd, rem) + bid / kXcds;
-  const int m0 = (lin / tiles_n) * 256, n0 = (lin % tiles_n) * 256;
-  const char* xb = reinterpret_cast<const char*>(p.x + (long long)m0 * p.ldx);
-  const char* wb = reinterpret_cast<const char*>(p.w + (long long)n0 * p.ldw);
-
-  // byte offsets of the pieces this lane loads: halves A0, A1, B0, B1
   const int lr = lane >> 3;
   const int acol = (lane & 7) ^ lr, bcol = (lane & 7) ^ ((lr & 3) | ((wave & 1) << 2));
-  uint32_t off[4][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = h * 128 + (wave + 8 * i) * 8 + lr;
-      off[h][i] = (uint32_t)(min(r, p.M - 1 - m0) * p.ldx + 8 * acol) * 2u;
-      off[2 + h][i] = (uint32_t)(min(r, p.N - 1 - n0) * p.ldw + 8 * bcol) * 2u;
-    }
   const int nk = (p.K + kBK - 1) / kBK;
   // the last step's pieces past K load the row's last one instead
   const int left = p.K - (nk - 1) * kBK;
-  const int aback = max(8 * acol - (left - 8), 0) * 2, bback = max(8 * bcol - (left - 8), 0) * 2;
-  auto load = [&](int h, int step) {
-    const char* base = (h < 2 ? xb : wb) + (long long)step * (kBK * 2);
-    const uint32_t back = step == nk - 1 ? (uint32_t)(h < 2 ? aback : bback) : 0u;
+
+  // this XCD's run of tiles (workgroups are dealt round-robin over the XCDs)
+  const int tiles_n = (p.N + 255) / 256, tiles_m = (p.M + 255) / 256;
+  const int total = tiles_m * tiles_n;
+  const int xcd = blockIdx.x % kXcds, rem = total % kXcds;
+  const int first = xcd * (total / kXcds) + min(xcd, rem);
+  const int count = total / kXcds + (xcd < rem ? 1 : 0);
+  const int slots = ((int)gridDim.x + kXcds - 1 - xcd) / kXcds;
+  int at = blockIdx.x / kXcds;
+  if (at >= count) return;
+
+  // of the tile whose loads are being issued
+  int m0, n0;
+  // the matrices from the tile's first row on; rows past the last one are past
+  // the end of the buffer (they come out as zeros, and are not stored)
+  __amdgpu_buffer_rsrc_t xb, wb;
+  auto rows_from = [&](const uint16_t* base, int row, int rows, int ld) {
+    const long long bytes = (long long)(rows - row) * ld * 2;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (long long)row * ld), 0,
+                                             (int)(uint32_t)min(bytes, 0xffffffffLL), 0x00020000);
+  };
+  auto turn_to = [&](int i) {
+    const int l = first + i, per = kTurnBand * tiles_n;
+    const int band = l / per, r = l - band * per, rows = min(kTurnBand, tiles_m - band * kTurnBand);
+    m0 = (band * kTurnBand + r % rows) * 256;
+    n0 = (r / rows) * 256;
+    xb = rows_from(p.x, m0, p.M, p.ldx);
+    wb = rows_from(p.w, n0, p.N, p.ldw);
+  };
+  // byte offsets of the pieces this lane loads: halves A0, A1, B0, B1
+  uint32_t off[4][2];
+#pragma unroll
+  for (int h = 0; h < 4; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      off[h][i] = (uint32_t)((h & 1) * 128 + (wave + 8 * i) * 8 + lr) * (uint32_t)(h < 2 ? p.ldx : p.ldw) * 2u +
+                  (h < 2 ? acol : bcol) * 16u;
+  auto load = [&](int h, int step, bool last) {
+    uint32_t back = 0;
+    if (last) {
+      back = (uint32_t)max(8 * (h < 2 ? acol : bcol) - (left - 8), 0) * 2u;
+      asm volatile("" : "+v"(back));  // the differences are made here, not kept
+    }
     unsigned char* dst = lds + (step & 1) * (4 * kHalfBytes) + h * kHalfBytes + wave * 1024;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_global_load_lds((glb_void*)(base + (off[h][i] - back)), (lds_void*)(dst + i * 8192), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(h < 2 ? xb : wb, (lds_void*)(dst + i * 8192), 16,
+                                               (int)(off[h][i] - back), step * (kBK * 2), 0, 0);
+  };
+  // a tile's first seven halves, in the order its steps go on with
+  auto load_first = [&]() {
+    load(2, 0, false);
+    load(0, 0, false);
+    load(3, 0, false);
+    load(1, 0, false);
+    load(2, 1, false);
+    load(0, 1, false);
+    load(3, 1, false);
   };
 
   f32x4 acc[2][4][2][2];
-#pragma unroll
-  for (int a = 0; a < 2; ++a)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) acc[a][i][b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-
   const int ar = wm * 64 + fr, br = wn * 32 + 8 * (fr >> 2) + (fr & 3);
   const int aaddr = ar * 128 + ((g ^ (ar & 7)) << 4);
   const int baddr = br * 128 + ((g ^ ((br & 3) | ((br & 8) >> 1))) << 4);
@@ -355,21 +398,22 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
     return frag(!last || 8 * c < left ? v : u32x4{0u, 0u, 0u, 0u});
   };
   auto read_a = [&](int half, int step, bool last) {
-    const int st = (step & 1) * (4 * kHalfBytes) + half * kHalfBytes;
+    int st = (step & 1) * (4 * kHalfBytes) + half * kHalfBytes;
+    asm volatile("" : "+s"(st));
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) fa[k][i] = piece(st + (aaddr ^ (k << 6)) + i * 2048, 4 * k + g, last);
   };
   auto read_b = [&](int half, int step, bool last) {
-    const int st = (step & 1) * (4 * kHalfBytes) + (2 + half) * kHalfBytes;
+    int st = (step & 1) * (4 * kHalfBytes) + (2 + half) * kHalfBytes;
+    asm volatile("" : "+s"(st));
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) fb[half][k][t] = piece(st + (baddr ^ (k << 6)) + t * 512, 4 * k + g, last);
   };
   auto product = [&](int a, int b) {
-    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -377,57 +421,79 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           acc[a][i][b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[b][k][t], fa[k][i], acc[a][i][b][t], 0, 0, 0);
-    __builtin_amdgcn_s_setprio(0);
   };
-
-  // the first two steps' halves, in the order the loop goes on with
-  load(2, 0);
-  load(0, 0);
-  load(3, 0);
-  load(1, 0);
-  if (nk > 1) {
-    load(2, 1);
-    load(0, 1);
-    load(3, 1);
-    wait_vm_here<10>();
-  } else {
-    wait_vm_here<0>();
-  }
-  phase_barrier();
-  read_b(0, 0, nk == 1);
-  if (wm == 1) phase_barrier();
-
-  int s = 0;
-  for (; s + 2 < nk; ++s) {
+  // One step. Ten younger loads may fly at a wait; `early` waits, a tile's first
+  // five, also leave out the last epilogue's 16 stores. `tail`: the loads are
+  // those of the last step.
+  auto wait_loads = [&](bool early) {
+    if (early) wait_vm_here<26>();
+    else wait_vm_here<10>();
+  };
+  auto full_step = [&](int s, bool early_first, bool early, bool tail) {
     read_a(0, s, false);
-    load(1, s + 1);
-    wait_vm_here<10>();
+    load(1, s + 1, false);
+    wait_loads(early_first);
     phase_barrier();
     product(0, 0);
     phase_barrier();
     read_b(1, s, false);
-    load(2, s + 2);
-    wait_vm_here<10>();
+    load(2, s + 2, tail);
+    wait_loads(early);
     phase_barrier();
     product(0, 1);
     phase_barrier();
     read_a(1, s, false);
-    load(0, s + 2);
-    wait_vm_here<10>();
+    load(0, s + 2, tail);
+    wait_loads(early);
     phase_barrier();
     product(1, 0);
     phase_barrier();
     read_b(0, s + 1, false);
-    load(3, s + 2);
-    wait_vm_here<10>();
+    load(3, s + 2, tail);
+    wait_loads(early);
     phase_barrier();
     product(1, 1);
     wait_lds_here();  // the next step's B0 is out of LDS before it may be overwritten
     phase_barrier();
-  }
-  if (nk > 1) {  // the last step but one
+  };
+
+  turn_to(at);
+  load_first();
+  wait_vm_here<0>();
+  for (;;) {
+    wait_vm_here<26>();
+    phase_barrier();
+    read_b(0, 0, false);
+    // lane (fr, g) will hold columns 8 g .. 8 g + 7 of row fr of each 16 x 32 pair
+    const int me = m0 + wm * 64 + fr, ne = n0 + wn * 32 + 8 * g;
+    const bool inside = m0 + 256 <= p.M && n0 + 256 <= p.N && p.vec;
+    u32x4 bias[2] = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+    if (inside && p.bias) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) bias[b] = *reinterpret_cast<const u32x4*>(p.bias + ne + b * 128);
+    }
+    if (wm == 1) phase_barrier();
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) acc[a][i][b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // (the steps' numbers are hidden from the compiler: peeled copies cost registers)
+    int s = 0;
+    for (; s < 2; ++s) {
+      asm volatile("" : "+s"(s));
+      full_step(s, true, s == 0, false);
+    }
+    for (; s + 3 < nk; ++s) full_step(s, false, false, false);
+    asm volatile("" : "+s"(s));
+    full_step(s, false, false, true);
+    ++s;
+    // the last step but one
     read_a(0, s, false);
-    load(1, s + 1);
+    load(1, s + 1, true);
     wait_vm_here<10>();
     phase_barrier();
     product(0, 0);
@@ -448,42 +514,67 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
     product(1, 1);
     phase_barrier();
     ++s;
-  }
-  read_a(0, s, true);
-  wait_vm_here<2>();
-  phase_barrier();
-  product(0, 0);
-  phase_barrier();
-  read_b(1, s, true);
-  wait_vm_here<0>();
-  phase_barrier();
-  product(0, 1);
-  phase_barrier();
-  read_a(1, s, true);
-  phase_barrier();
-  product(1, 0);
-  product(1, 1);
-  if (wm == 0) phase_barrier();
+    // the last
+    read_a(0, s, true);
+    wait_vm_here<2>();
+    phase_barrier();
+    product(0, 0);
+    phase_barrier();
+    read_b(1, s, true);
+    wait_vm_here<0>();
+    phase_barrier();
+    product(0, 1);
+    phase_barrier();
+    read_a(1, s, true);
+    wait_lds_here();  // nothing is read from LDS after this barrier: the next tile may come in
+    phase_barrier();
+    product(1, 0);
+    product(1, 1);
+    if (wm == 0) phase_barrier();
 
-  // lane (fr, g) holds columns 8 g .. 8 g + 7 of row fr of each 16 x 32 pair
-  with_act(p.act, [&](auto act) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int n = n0 + b * 128 + wn * 32 + 8 * g;
-      float bias[8];
-      load_bias(p, n, bias);
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = m0 + a * 128 + wm * 64 + 16 * i + fr;
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = acc[a][i][b][e >> 2][e & 3];
-          if (m < p.M) finish<act, 8>(p, m, n, v, bias);
-        }
+    asm volatile("" : "+v"(bias[0]), "+v"(bias[1]));  // landed long ago, on every path
+    at += slots;
+    const bool more = at < count;
+    if (more) {
+      turn_to(at);
+      load_first();
     }
-  });
+    with_act(p.act, [&](auto act) {
+      if (inside) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int m = me + a * 128 + 16 * i, n = ne + b * 128;
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = activate<act>(acc[a][i][b][e >> 2][e & 3] +
+                                     __uint_as_float(e & 1 ? bias[b][e >> 1] & 0xffff0000u : bias[b][e >> 1] << 16));
+              finish_pieces<8>(p, (long long)m * p.ldo + n, (long long)m * p.ldr + n, v);
+            }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float z[8];
+          load_bias(p, ne + b * 128, z);
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = acc[a][i][b][e >> 2][e & 3];
+              if (me + a * 128 + 16 * i < p.M) finish<act, 8>(p, me + a * 128 + 16 * i, ne + b * 128, v, z);
+            }
+        }
+      }
+    });
+    if (!more) break;
+    if (!inside) wait_vm_here<0>();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -598,7 +689,8 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   p.out_f32 = a.out_f32;
   // 16-byte pieces: eight bf16 columns (the 4-column kernels need half), four float32 ones
   const int unit = a.out_f32 ? 4 : 8;
-  p.vec = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.residual)) & 15u) == 0 &&
+  p.vec = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.residual) |
+            reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0 &&
           a.ldo % unit == 0 && (a.residual == nullptr || a.ldr % unit == 0);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   auto pack = [&](const uint16_t*& src, int& ld, int rows) -> hipError_t {
@@ -618,9 +710,10 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   if (p.M <= 16) return run_few<1>(p, st);
   if (p.M <= 32) return run_few<2>(p, st);
   if (p.M <= 64) return run_few<4>(p, st);
-  if ((long long)p.M * p.N >= 256LL * 256 * 256) {
+  if ((long long)p.M * p.N >= 256LL * 256 * 256 && p.K > (kTurnMinSteps - 1) * kBK) {
     const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
-    hipLaunchKernelGGL(linear_turn_kernel, dim3((unsigned)tiles), dim3(512), 8 * kHalfBytes, st, p);
+    hipLaunchKernelGGL(linear_turn_kernel, dim3((unsigned)(tiles < kTurnCus ? tiles : kTurnCus)), dim3(512),
+                       8 * kHalfBytes, st, p);
     return hipGetLastError();
   }
   return run_tiles<128, 128, 2, 2>(p, st);
