@@ -23,6 +23,7 @@ namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) void lds_void;
 
 struct PaParams {
   Heads q, kp, vp, ko, vo, out;
@@ -48,7 +49,7 @@ struct PaParams {
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 template <int D, int WR, int WK, int QT, int KC>
-struct Tile {
+struct ThinTile {
   static constexpr int kRows = 16 * QT * WR;
   static constexpr int kPieces = D / 8;                       // 16-byte pieces of a key row
   static constexpr int kNP = KC * kPieces / (64 * WR);        // pieces a thread stages, K and V each
@@ -329,6 +330,265 @@ struct Tile {
   }
 };
 
+// The reference point of a row's exponents moves only when a score passes it
+// by more than kSlack: probabilities then stay below 2^kSlack, which float32
+// sums and bfloat16 products bear as well as values below 1, and the output is
+// scaled (and the row's maximum exchanged between lanes) a few times per row
+// instead of once per chunk.
+constexpr float kSlack = 8.f;
+
+// max over the four 16-lane groups of a wave
+__device__ __forceinline__ float group_max(float x) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+template <int D, int WR, int QT>
+struct WideTile {
+  static constexpr int KC = 64;
+  static constexpr int kRows = 16 * QT * WR;
+  static constexpr int kPieces = D / 8;                 // 16-byte pieces of a key row
+  static constexpr int kMat = KC * D * 2;               // bytes of a chunk's K (or V)
+  static constexpr int kStage = 2 * kMat;
+  static constexpr int kLds = 2 * kStage;
+  static constexpr int kNT = KC / 16, kDK = D / 32, kND = D / 16;
+  static constexpr int kLoads = kMat / (WR * 1024);     // 1-KB loads a wave and matrix
+  static constexpr int kBlkRows = 64 / kPieces;         // key rows of one load
+
+  static __device__ __forceinline__ void run(const PaParams& p, unsigned char* lds, int hk, int b_own,
+                                             long long row0, long long row_end, int p0, int p1,
+                                             int s0, int s1, int slot) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wr = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int fr = lane & 15, g = lane >> 4;
+
+    bf16x8 qf[QT][kDK];
+    int lim[QT];      // own keys below this are visible
+    bool live[QT];
+    long long oaddr[QT];
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+      const long long R = row0 + (wr * QT + u) * 16 + fr;
+      live[u] = R < row_end;
+      const long long r = live[u] ? R : row_end - 1;
+      const int b = (int)(r / p.RS), rr = (int)(r - (long long)b * p.RS), t = rr / p.G;
+      const int h = hk * p.G + (rr - t * p.G);
+      const int ql = p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
+      live[u] = live[u] && t < ql;
+      lim[u] = 0x7fffffff;
+      if (p.causal && b_own >= 0) {
+        const int len = p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
+        lim[u] = len - ql + t + 1;
+      }
+      const uint16_t* src = static_cast<const uint16_t*>(p.q.p) + b * p.q.b + t * p.q.t + h * p.q.h;
+#pragma unroll
+      for (int k = 0; k < kDK; ++k)
+        qf[u][k] = frag(*reinterpret_cast<const u32x4*>(src + 32 * k + 8 * g));
+      oaddr[u] = b * p.out.b + t * p.out.t + h * p.out.h;
+    }
+    int own_end = s1, all_see = s1;  // own keys of the tile; those that every row sees
+    if (b_own >= 0) {
+      const int len = p.own_len ? min(max(p.own_len[b_own], 0), p.S) : p.S;
+      own_end = all_see = min(s1, len);
+      if (p.causal) {
+        const int ql = p.q_len ? min(max(p.q_len[b_own], 0), p.Tq) : p.Tq;
+        const long long last = min(row0 + kRows, row_end) - 1, base = (long long)b_own * p.RS;
+        own_end = min(own_end, len - ql + (int)((last - base) / p.G) + 1);
+        all_see = min(all_see, len - ql + (int)((row0 - base) / p.G) + 1);
+      }
+    }
+    const int nprefix = p1 > p0 ? (p1 - p0 + KC - 1) / KC : 0;
+    const int nown = own_end > s0 ? (own_end - s0 + KC - 1) / KC : 0;
+    const int nc = nprefix + nown;
+
+    f32x4 o[QT][kND], l[QT];
+    float m[QT];
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+      m[u] = -INFINITY;
+      l[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kND; ++j) o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // this lane's piece of the wave's first load: key row lr, piece (place ^
+    // row), so that the 16 rows of an operand read lie in different banks
+    const int lr = wr * kBlkRows + lane / kPieces;
+    const int lp = (lane % kPieces) ^ (lr & (kPieces - 1));
+    const uint32_t rows_kp = (uint32_t)p.kp.t * (WR * kBlkRows * 2), rows_vp = (uint32_t)p.vp.t * (WR * kBlkRows * 2);
+    const uint32_t rows_ko = (uint32_t)p.ko.t * (WR * kBlkRows * 2), rows_vo = (uint32_t)p.vo.t * (WR * kBlkRows * 2);
+    const uint32_t kp_off = (uint32_t)(lr * (int)p.kp.t + 8 * lp) * 2u, vp_off = (uint32_t)(lr * (int)p.vp.t + 8 * lp) * 2u;
+    const uint32_t ko_off = (uint32_t)(lr * (int)p.ko.t + 8 * lp) * 2u, vo_off = (uint32_t)(lr * (int)p.vo.t + 8 * lp) * 2u;
+    auto load = [&](int c) {
+      const bool pre = c < nprefix;
+      const int base = pre ? p0 + c * KC : s0 + (c - nprefix) * KC;
+      const int keys = min((pre ? p1 : own_end) - base, KC);
+      const Heads& hk_ = pre ? p.kp : p.ko;
+      const Heads& hv_ = pre ? p.vp : p.vo;
+      const long long ob = pre ? 0 : (long long)b_own;
+      uint16_t* ks = static_cast<uint16_t*>(hk_.p) + ob * hk_.b + hk * hk_.h + (long long)base * hk_.t;
+      uint16_t* vs = static_cast<uint16_t*>(hv_.p) + ob * hv_.b + hk * hv_.h + (long long)base * hv_.t;
+      // rows past the last key are past the buffer's end and come out as zeros
+      const auto kb = __builtin_amdgcn_make_buffer_rsrc(ks, 0, (int)((uint32_t)(keys - 1) * (uint32_t)hk_.t * 2u + D * 2), 0x00020000);
+      const auto vb = __builtin_amdgcn_make_buffer_rsrc(vs, 0, (int)((uint32_t)(keys - 1) * (uint32_t)hv_.t * 2u + D * 2), 0x00020000);
+      unsigned char* st = lds + (c & 1) * kStage + wr * 1024;
+      const uint32_t ko = pre ? kp_off : ko_off, vo = pre ? vp_off : vo_off;
+      const uint32_t kr = pre ? rows_kp : rows_ko, vr = pre ? rows_vp : rows_vo;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(kb, (lds_void*)(st + i * WR * 1024), 16, (int)(ko + i * kr), 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vb, (lds_void*)(st + kMat + i * WR * 1024), 16, (int)(vo + i * vr), 0, 0, 0);
+    };
+
+    bf16x8 ones;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ones[e] = static_cast<__bf16>(1.f);
+
+    if (nc > 0) load(0);
+    for (int c = 0; c < nc; ++c) {
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's loads of chunk c landed
+      __syncthreads();                     // everyone's, and chunk c - 1 is read
+      if (c + 1 < nc) load(c + 1);
+      const bool pre = c < nprefix;
+      const int base = pre ? p0 + c * KC : s0 + (c - nprefix) * KC;
+      const int end = pre ? p1 : own_end;
+      const unsigned char* sK = lds + (c & 1) * kStage;
+      const unsigned char* sV = sK + kMat;
+      unsigned long long bits = ~0ull;
+      if (!pre && p.mask) {
+        // masked values may hold anything: they enter the product as zeros
+        const bool on = base + lane < end && p.mask[(long long)b_own * p.S + base + lane] != 0;
+        bits = __ballot(on);
+        unsigned char* z = lds + (c & 1) * kStage + kMat;
+        for (int i = tid; i < KC * kPieces; i += 64 * WR)
+          if (!((bits >> (i / kPieces)) & 1)) *reinterpret_cast<u32x4*>(z + i * 16) = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+      }
+      f32x4 sc[QT][kNT];
+#pragma unroll
+      for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+        for (int u = 0; u < QT; ++u) sc[u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const int kr = 16 * t + fr;
+#pragma unroll
+        for (int k = 0; k < kDK; ++k) {
+          const bf16x8 kf = frag(*reinterpret_cast<const u32x4*>(
+              sK + (kr * kPieces + ((4 * k + g) ^ (kr & (kPieces - 1)))) * 16));
+#pragma unroll
+          for (int u = 0; u < QT; ++u)
+            sc[u][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[u][k], sc[u][t], 0, 0, 0);
+        }
+      }
+      // keys that no row or not every row sees
+      if (base + KC > (pre ? end : all_see) || (!pre && p.mask)) {
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          const int stop = pre ? end : min(end, lim[u]);
+#pragma unroll
+          for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int kk = 16 * t + 4 * g + e;
+              if (base + kk >= stop || !((bits >> kk) & 1)) sc[u][t][e] = -INFINITY;
+            }
+        }
+      }
+      uint32_t pk[QT][kNT][2];
+      float cm[QT];
+      bool far = false;
+#pragma unroll
+      for (int u = 0; u < QT; ++u) {
+        float x = fmaxf(fmaxf(sc[u][0][0], sc[u][0][1]), fmaxf(sc[u][0][2], sc[u][0][3]));
+#pragma unroll
+        for (int t = 1; t < kNT; ++t)
+          x = fmaxf(fmaxf(x, fmaxf(sc[u][t][0], sc[u][t][1])), fmaxf(sc[u][t][2], sc[u][t][3]));
+        cm[u] = x * p.c;  // base-2 scores (c > 0)
+        far = far || cm[u] > m[u] + kSlack;
+      }
+      if (__any(far)) {
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          const float mn = fmaxf(m[u], group_max(cm[u]));
+          const float alpha = __builtin_amdgcn_exp2f(m[u] - (mn == -INFINITY ? 0.f : mn));
+          m[u] = mn;
+          l[u] *= alpha;
+#pragma unroll
+          for (int j = 0; j < kND; ++j) o[u][j] *= alpha;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < QT; ++u) {
+        const float ref = m[u] == -INFINITY ? 0.f : m[u];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+          float e4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][t][e], p.c, -ref));
+          const bf16x2 lo = {static_cast<__bf16>(e4[0]), static_cast<__bf16>(e4[1])};
+          const bf16x2 hi = {static_cast<__bf16>(e4[2]), static_cast<__bf16>(e4[3])};
+          pk[u][t][0] = __builtin_bit_cast(uint32_t, lo);
+          pk[u][t][1] = __builtin_bit_cast(uint32_t, hi);
+        }
+      }
+      // O^T += V^T P^T: k-slots 8 g .. 8 g + 7 carry keys 32 c + 4 g + (0..3)
+      // and 32 c + 16 + 4 g + (0..3) on both sides; a row of ones in the place
+      // of V^T gives l, the sum of the probabilities as the product takes them
+      const int vkey = 4 * g + (fr >> 2);
+#pragma unroll
+      for (int cc = 0; cc < KC / 32; ++cc) {
+        const int kr = 32 * cc + vkey;
+        const unsigned char* vrow = sV + kr * D * 2 + (fr & 1) * 8;
+        bf16x8 pf[QT];
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          pf[u] = frag(u32x4{pk[u][2 * cc][0], pk[u][2 * cc][1], pk[u][2 * cc + 1][0], pk[u][2 * cc + 1][1]});
+          l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[u], l[u], 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < kND; ++j) {
+          const int pc = 2 * j + ((fr & 3) >> 1);
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)(vrow + ((pc ^ (kr & (kPieces - 1))) << 4)));
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_s16x4*)(vrow + 16 * D * 2 + ((pc ^ ((kr + 16) & (kPieces - 1))) << 4)));
+          const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+          const bf16x8 vf = frag(u32x4{l2[0], l2[1], h2[0], h2[1]});
+#pragma unroll
+          for (int u = 0; u < QT; ++u)
+            o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u], o[u][j], 0, 0, 0);
+        }
+      }
+    }
+
+    // o[u][j][e] = O^T[dim 16 j + 4 g + e][row]
+#pragma unroll
+    for (int u = 0; u < QT; ++u) {
+      if (!live[u]) continue;
+      if (p.slots == 1) {
+        const float inv = l[u][0] > 0.f ? 1.f / l[u][0] : 0.f;
+        uint16_t* dst = static_cast<uint16_t*>(p.out.p) + oaddr[u] + 4 * g;
+#pragma unroll
+        for (int j = 0; j < kND; ++j) {
+          const bf16x2 lo = {static_cast<__bf16>(o[u][j][0] * inv), static_cast<__bf16>(o[u][j][1] * inv)};
+          const bf16x2 hi = {static_cast<__bf16>(o[u][j][2] * inv), static_cast<__bf16>(o[u][j][3] * inv)};
+          *reinterpret_cast<u32x2*>(dst + 16 * j) =
+              u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+        }
+      } else {
+        const long long at = ((long long)slot * p.Hk + hk) * p.RT + row0 + (wr * QT + u) * 16 + fr;
+        if (g == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m[u], l[u][0]};
+        if (nc == 0) continue;  // the statistics say that there is nothing
+#pragma unroll
+        for (int j = 0; j < kND; ++j) *reinterpret_cast<f32x4*>(p.po + at * D + 16 * j + 4 * g) = o[u][j];
+      }
+    }
+  }
+};
+
 // One part of a list of keys n, cut at multiples of `unit`.
 __device__ __forceinline__ void part_range(int n, int parts, int part, int unit, int& lo, int& hi) {
   const int nu = (n + unit - 1) / unit;
@@ -337,9 +597,9 @@ __device__ __forceinline__ void part_range(int n, int parts, int part, int unit,
 }
 
 template <int D>
-using Wide = Tile<D, 4, 1, 2, 64>;
+using Wide = WideTile<D, 4, 2>;
 template <int D>
-using Thin = Tile<D, 1, 4, 1, 32>;
+using Thin = ThinTile<D, 1, 4, 1, 32>;
 
 template <class T>
 __device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, int item, int seq, int tiles,

@@ -32,6 +32,15 @@ gkd_status check_heads(const char* fn, const char* name, const gkd_heads* h, uns
   return GKD_OK;
 }
 
+// Keys and values of the attention: a chunk of 64 of them is addressed with
+// 32 bits.
+gkd_status check_keys(const char* fn, const char* name, const gkd_heads* h) {
+  const gkd_status st = check_heads(fn, name, h, 2, 16);
+  if (st != GKD_OK) return st;
+  if (h->token >= (1 << 25)) return fail(GKD_ERR_SHAPE, "%s: token stride of %s reaches 2^25", fn, name);
+  return GKD_OK;
+}
+
 gkd_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
   if (need == 0) return GKD_OK;
   if (ws == nullptr) return fail(GKD_ERR_NULL, "%s: NULL workspace", fn);
@@ -192,12 +201,12 @@ gkd_status gkd_prefix_attention(const gkd_heads* q, const gkd_heads* k_prefix,
   if ((st = check_heads(fn, "q", q, 2, 16)) != GKD_OK) return st;
   if ((st = check_heads(fn, "out", out, 2, 16)) != GKD_OK) return st;
   if (P > 0) {
-    if ((st = check_heads(fn, "k_prefix", k_prefix, 2, 16)) != GKD_OK) return st;
-    if ((st = check_heads(fn, "v_prefix", v_prefix, 2, 16)) != GKD_OK) return st;
+    if ((st = check_keys(fn, "k_prefix", k_prefix)) != GKD_OK) return st;
+    if ((st = check_keys(fn, "v_prefix", v_prefix)) != GKD_OK) return st;
   }
   if (S > 0) {
-    if ((st = check_heads(fn, "k_own", k_own, 2, 16)) != GKD_OK) return st;
-    if ((st = check_heads(fn, "v_own", v_own, 2, 16)) != GKD_OK) return st;
+    if ((st = check_keys(fn, "k_own", k_own)) != GKD_OK) return st;
+    if ((st = check_keys(fn, "v_own", v_own)) != GKD_OK) return st;
   }
   if (!aligned(own_len, 4) || !aligned(q_len, 4))
     return fail(GKD_ERR_ALIGN, "%s: lengths need 4-byte alignment", fn);

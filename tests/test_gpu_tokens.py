@@ -381,16 +381,18 @@ def test_attention_repeats_exactly_and_on_another_stream(gkd):
 
 def test_attention_long_cache_past_32_bit_offsets(gkd):
     """A token stride that puts the last keys more than 2^32 elements away."""
-    S, stride = 70, 1 << 26          # 70 tokens, 2^26 elements apart: 9.4 GB of keys
+    S, stride = 300, 1 << 24         # 300 tokens, 2^24 elements apart: 10 GB of keys
     g = rng(2)
     ko = torch.zeros(S * stride, dtype=BF, device="cuda").view(1, S, stride)[:, :, :128].unflatten(2, (1, 128))
     src = randn(g, 1, S, 1, 128)
     ko.copy_(src)
     vo = randn(g, 1, S, 1, 128)
-    q = randn(g, 1, 1, 2, 128)
-    got = gkd.prefix_attention(q, None, None, ko, vo)
-    want = gkd.prefix_attention(q, None, None, src, vo)
-    assert torch.equal(got, want)
+    for Tq in (1, 20):
+        q = randn(g, 1, Tq, 2, 128)
+        want = gkd.prefix_attention(q, None, None, src, vo)
+        assert torch.equal(gkd.prefix_attention(q, None, None, ko, vo), want)
+        want = gkd.prefix_attention(q, src[0], vo[0])
+        assert torch.equal(gkd.prefix_attention(q, ko[0], vo[0]), want)
 
 
 def test_attention_refusals(gkd):

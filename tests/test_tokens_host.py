@@ -178,6 +178,8 @@ def test_attention_rejects_operands(lib):
         assert attn(lib, **{name: heads(data=A + 8)}) == ALIGN, name
         assert attn(lib, **{name: heads(token=516)}) == ALIGN, name
         assert attn(lib, **{name: heads(head=-64)}) == SHAPE, name
+    for name in ("kp", "vp", "ko", "vo"):
+        assert attn(lib, **{name: heads(token=1 << 25)}) == SHAPE, name
     assert attn(lib, B=0) == OK and attn(lib, Tq=0, ws=None) == OK
 
 
