@@ -18,6 +18,8 @@
 #include "gkd_device.hpp"
 #include "tokens_launch.hpp"
 
+#include <type_traits>
+
 namespace gkd {
 namespace {
 
@@ -59,8 +61,8 @@ struct ThinTile {
   static constexpr int kNT = KC / 16, kDK = D / 32, kND = D / 16;
 
   static __device__ __forceinline__ void run(const PaParams& p, unsigned char* lds, int hk, int b_own,
-                                             long long row0, long long row_end, int p0, int p1,
-                                             int s0, int s1, int slot) {
+                                             int row0, int row_end, int p0, int p1, int s0, int s1,
+                                             int slot) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave % WR, wk = wave / WR;
@@ -69,18 +71,17 @@ struct ThinTile {
 
     // this lane's rows (query fr of each of its 16-row groups)
     bf16x8 qf[QT][kDK];
-    long long R[QT];
+    int R[QT];
     bool live[QT];
     int lim[QT];      // own keys below this are visible
     long long oaddr[QT];
     int own_end = s1;
 #pragma unroll
     for (int u = 0; u < QT; ++u) {
-      R[u] = row0 + (wr * QT + u) * 16 + fr;
-      live[u] = R[u] < row_end;
-      const long long r = live[u] ? R[u] : row_end - 1;
-      const int b = (int)(r / p.RS), rr = (int)(r - (long long)b * p.RS), t = rr / p.G;
-      const int h = hk * p.G + (rr - t * p.G);
+      live[u] = (wr * QT + u) * 16 + fr < row_end - row0;
+      R[u] = live[u] ? row0 + (wr * QT + u) * 16 + fr : row_end - 1;
+      const int b = (int)((unsigned)R[u] / (unsigned)p.RS), rr = R[u] - b * p.RS;
+      const int t = (int)((unsigned)rr / (unsigned)p.G), h = hk * p.G + (rr - t * p.G);
       const int ql = p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
       live[u] = live[u] && t < ql;
       lim[u] = 0x7fffffff;
@@ -97,8 +98,8 @@ struct ThinTile {
     if (b_own >= 0) {
       own_end = min(s1, p.own_len ? min(max(p.own_len[b_own], 0), p.S) : p.S);
       if (p.causal) {  // no row of the tile sees past its last one's limit
-        const long long last = min(row0 + kRows, row_end) - 1;
-        const int t = (int)((last - (long long)b_own * p.RS) / p.G);
+        const int first = row0 - b_own * p.RS, last = min(first + kRows, row_end - b_own * p.RS) - 1;
+        const int t = (int)((unsigned)last / (unsigned)p.G);
         const int ql = p.q_len ? min(max(p.q_len[b_own], 0), p.Tq) : p.Tq;
         const int len = p.own_len ? min(max(p.own_len[b_own], 0), p.S) : p.S;
         own_end = min(own_end, len - ql + t + 1);
@@ -330,13 +331,6 @@ struct ThinTile {
   }
 };
 
-// The reference point of a row's exponents moves only when a score passes it
-// by more than kSlack: probabilities then stay below 2^kSlack, which float32
-// sums and bfloat16 products bear as well as values below 1, and the output is
-// scaled (and the row's maximum exchanged between lanes) a few times per row
-// instead of once per chunk.
-constexpr float kSlack = 8.f;
-
 // max over the four 16-lane groups of a wave
 __device__ __forceinline__ float group_max(float x) {
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -344,6 +338,27 @@ __device__ __forceinline__ float group_max(float x) {
   const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+
+// The keys that a tile reads, chunk by chunk: first the prefix's, then own ones.
+struct KeyWalk {
+  const uint16_t *k, *v;  // the next chunk's first key
+  int kt, vt;             // token strides (below 2^25)
+  int left;               // keys from there on
+};
+
+// The reference point m of a row's exponents stays where it is while the
+// row's scores pass it by no more than 8: float32 sums and bfloat16 products
+// bear probabilities of up to 2^8 as well as those below 1. So the scores'
+// maximum is found, and l and O are scaled, on the first chunk and a few times
+// after it; elsewhere a chunk costs seven integer maxima over the rounded
+// probabilities (positive bfloat16 values order like their bits): one of 2^8
+// or more sends the wave to look, and then the rows that passed 8 move and no
+// others, so a row's results do not depend on its neighbours'.
+constexpr float kSlack = 8.f;
+constexpr uint32_t kSlackBits = 0x4380u;  // 2^8 in bfloat16
+constexpr float kNowhere = -3e38f;        // m before a row's first key: any score passes it
 
 template <int D, int WR, int QT>
 struct WideTile {
@@ -358,8 +373,8 @@ struct WideTile {
   static constexpr int kBlkRows = 64 / kPieces;         // key rows of one load
 
   static __device__ __forceinline__ void run(const PaParams& p, unsigned char* lds, int hk, int b_own,
-                                             long long row0, long long row_end, int p0, int p1,
-                                             int s0, int s1, int slot) {
+                                             int row0, int row_end, int p0, int p1, int s0, int s1,
+                                             int slot) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wr = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fr = lane & 15, g = lane >> 4;
@@ -370,22 +385,22 @@ struct WideTile {
     long long oaddr[QT];
 #pragma unroll
     for (int u = 0; u < QT; ++u) {
-      const long long R = row0 + (wr * QT + u) * 16 + fr;
-      live[u] = R < row_end;
-      const long long r = live[u] ? R : row_end - 1;
-      const int b = (int)(r / p.RS), rr = (int)(r - (long long)b * p.RS), t = rr / p.G;
-      const int h = hk * p.G + (rr - t * p.G);
+      const int n = (wr * QT + u) * 16 + fr;
+      live[u] = n < row_end - row0;
+      const unsigned r = live[u] ? row0 + n : row_end - 1;
+      const unsigned b = r / (unsigned)p.RS, rr = r - b * p.RS, t = rr / (unsigned)p.G;
+      const int h = hk * p.G + (int)(rr - t * p.G);
       const int ql = p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
-      live[u] = live[u] && t < ql;
+      live[u] = live[u] && (int)t < ql;
       lim[u] = 0x7fffffff;
       if (p.causal && b_own >= 0) {
         const int len = p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
-        lim[u] = len - ql + t + 1;
+        lim[u] = len - ql + (int)t + 1;
       }
       const uint16_t* src = static_cast<const uint16_t*>(p.q.p) + b * p.q.b + t * p.q.t + h * p.q.h;
 #pragma unroll
       for (int k = 0; k < kDK; ++k)
-        qf[u][k] = frag(*reinterpret_cast<const u32x4*>(src + 32 * k + 8 * g));
+        qf[u][k] = frag(live[u] ? *reinterpret_cast<const u32x4*>(src + 32 * k + 8 * g) : u32x4{0u, 0u, 0u, 0u});
       oaddr[u] = b * p.out.b + t * p.out.t + h * p.out.h;
     }
     int own_end = s1, all_see = s1;  // own keys of the tile; those that every row sees
@@ -394,20 +409,37 @@ struct WideTile {
       own_end = all_see = min(s1, len);
       if (p.causal) {
         const int ql = p.q_len ? min(max(p.q_len[b_own], 0), p.Tq) : p.Tq;
-        const long long last = min(row0 + kRows, row_end) - 1, base = (long long)b_own * p.RS;
-        own_end = min(own_end, len - ql + (int)((last - base) / p.G) + 1);
-        all_see = min(all_see, len - ql + (int)((row0 - base) / p.G) + 1);
+        const int first = row0 - b_own * p.RS, last = min(first + kRows, row_end - b_own * p.RS) - 1;
+        own_end = min(own_end, len - ql + (int)((unsigned)last / (unsigned)p.G) + 1);
+        all_see = min(all_see, len - ql + (int)((unsigned)first / (unsigned)p.G) + 1);
       }
     }
     const int nprefix = p1 > p0 ? (p1 - p0 + KC - 1) / KC : 0;
     const int nown = own_end > s0 ? (own_end - s0 + KC - 1) / KC : 0;
     const int nc = nprefix + nown;
+    KeyWalk own{}, walk{};
+    if (nown > 0) {
+      own.k = static_cast<const uint16_t*>(p.ko.p) + (long long)b_own * p.ko.b + hk * p.ko.h + (long long)s0 * p.ko.t;
+      own.v = static_cast<const uint16_t*>(p.vo.p) + (long long)b_own * p.vo.b + hk * p.vo.h + (long long)s0 * p.vo.t;
+      own.kt = (int)p.ko.t;
+      own.vt = (int)p.vo.t;
+      own.left = own_end - s0;
+    }
+    if (nprefix > 0) {
+      walk.k = static_cast<const uint16_t*>(p.kp.p) + hk * p.kp.h + (long long)p0 * p.kp.t;
+      walk.v = static_cast<const uint16_t*>(p.vp.p) + hk * p.vp.h + (long long)p0 * p.vp.t;
+      walk.kt = (int)p.kp.t;
+      walk.vt = (int)p.vp.t;
+      walk.left = p1 - p0;
+    } else {
+      walk = own;
+    }
 
     f32x4 o[QT][kND], l[QT];
     float m[QT];
 #pragma unroll
     for (int u = 0; u < QT; ++u) {
-      m[u] = -INFINITY;
+      m[u] = kNowhere;
       l[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kND; ++j) o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -416,152 +448,179 @@ struct WideTile {
     // this lane's piece of the wave's first load: key row lr, piece (place ^
     // row), so that the 16 rows of an operand read lie in different banks
     const int lr = wr * kBlkRows + lane / kPieces;
-    const int lp = (lane % kPieces) ^ (lr & (kPieces - 1));
-    const uint32_t rows_kp = (uint32_t)p.kp.t * (WR * kBlkRows * 2), rows_vp = (uint32_t)p.vp.t * (WR * kBlkRows * 2);
-    const uint32_t rows_ko = (uint32_t)p.ko.t * (WR * kBlkRows * 2), rows_vo = (uint32_t)p.vo.t * (WR * kBlkRows * 2);
-    const uint32_t kp_off = (uint32_t)(lr * (int)p.kp.t + 8 * lp) * 2u, vp_off = (uint32_t)(lr * (int)p.vp.t + 8 * lp) * 2u;
-    const uint32_t ko_off = (uint32_t)(lr * (int)p.ko.t + 8 * lp) * 2u, vo_off = (uint32_t)(lr * (int)p.vo.t + 8 * lp) * 2u;
-    auto load = [&](int c) {
-      const bool pre = c < nprefix;
-      const int base = pre ? p0 + c * KC : s0 + (c - nprefix) * KC;
-      const int keys = min((pre ? p1 : own_end) - base, KC);
-      const Heads& hk_ = pre ? p.kp : p.ko;
-      const Heads& hv_ = pre ? p.vp : p.vo;
-      const long long ob = pre ? 0 : (long long)b_own;
-      uint16_t* ks = static_cast<uint16_t*>(hk_.p) + ob * hk_.b + hk * hk_.h + (long long)base * hk_.t;
-      uint16_t* vs = static_cast<uint16_t*>(hv_.p) + ob * hv_.b + hk * hv_.h + (long long)base * hv_.t;
+    const int lp = 16 * ((lane % kPieces) ^ (lr & (kPieces - 1)));
+    auto load = [&](int c, int buf) {
+      if (c == nprefix) walk = own;
+      const int keys = min(walk.left, KC);
       // rows past the last key are past the buffer's end and come out as zeros
-      const auto kb = __builtin_amdgcn_make_buffer_rsrc(ks, 0, (int)((uint32_t)(keys - 1) * (uint32_t)hk_.t * 2u + D * 2), 0x00020000);
-      const auto vb = __builtin_amdgcn_make_buffer_rsrc(vs, 0, (int)((uint32_t)(keys - 1) * (uint32_t)hv_.t * 2u + D * 2), 0x00020000);
-      unsigned char* st = lds + (c & 1) * kStage + wr * 1024;
-      const uint32_t ko = pre ? kp_off : ko_off, vo = pre ? vp_off : vo_off;
-      const uint32_t kr = pre ? rows_kp : rows_ko, vr = pre ? rows_vp : rows_vo;
+      const auto kb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(walk.k), 0,
+                                                        (int)((uint32_t)(keys - 1) * (uint32_t)walk.kt * 2u + D * 2), 0x00020000);
+      const auto vb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(walk.v), 0,
+                                                        (int)((uint32_t)(keys - 1) * (uint32_t)walk.vt * 2u + D * 2), 0x00020000);
+      unsigned char* st = lds + buf * kStage + wr * 1024;
+      uint32_t off = (uint32_t)lr * (uint32_t)walk.kt * 2u + lp;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(kb, (lds_void*)(st + i * WR * 1024), 16, (int)(ko + i * kr), 0, 0, 0);
+      for (int i = 0; i < kLoads; ++i, off += (uint32_t)walk.kt * (WR * kBlkRows * 2))
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(kb, (lds_void*)(st + i * WR * 1024), 16, (int)off, 0, 0, 0);
+      off = (uint32_t)lr * (uint32_t)walk.vt * 2u + lp;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(vb, (lds_void*)(st + kMat + i * WR * 1024), 16, (int)(vo + i * vr), 0, 0, 0);
+      for (int i = 0; i < kLoads; ++i, off += (uint32_t)walk.vt * (WR * kBlkRows * 2))
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vb, (lds_void*)(st + kMat + i * WR * 1024), 16, (int)off, 0, 0, 0);
+      walk.k += (long long)walk.kt * KC;
+      walk.v += (long long)walk.vt * KC;
+      walk.left -= KC;
     };
 
+    // operand addresses in a stage: K row fr of a 16-row group, piece 4 k + g;
+    // V rows 4 g + fr / 4 (and 16 further), 8 bytes of dims 16 j + 4 (fr % 4)
+    int kat[kDK], vat[kND];
+#pragma unroll
+    for (int k = 0; k < kDK; ++k) kat[k] = (fr * kPieces + ((4 * k + g) ^ (fr & (kPieces - 1)))) * 16;
+    const int vkey = 4 * g + (fr >> 2);
+#pragma unroll
+    for (int j = 0; j < kND; ++j)
+      vat[j] = kMat + vkey * D * 2 + (((2 * j + ((fr & 3) >> 1)) ^ (vkey & (kPieces - 1))) << 4) + (fr & 1) * 8;
     bf16x8 ones;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ones[e] = static_cast<__bf16>(1.f);
 
-    if (nc > 0) load(0);
-    for (int c = 0; c < nc; ++c) {
+    auto step = [&](int c, auto buf) {
+      const unsigned char* st = lds + buf * kStage;
       __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's loads of chunk c landed
       __syncthreads();                     // everyone's, and chunk c - 1 is read
-      if (c + 1 < nc) load(c + 1);
+      if (c + 1 < nc) load(c + 1, 1 - buf);
       const bool pre = c < nprefix;
       const int base = pre ? p0 + c * KC : s0 + (c - nprefix) * KC;
       const int end = pre ? p1 : own_end;
-      const unsigned char* sK = lds + (c & 1) * kStage;
-      const unsigned char* sV = sK + kMat;
       unsigned long long bits = ~0ull;
       if (!pre && p.mask) {
         // masked values may hold anything: they enter the product as zeros
         const bool on = base + lane < end && p.mask[(long long)b_own * p.S + base + lane] != 0;
         bits = __ballot(on);
-        unsigned char* z = lds + (c & 1) * kStage + kMat;
+        unsigned char* z = lds + buf * kStage + kMat;
         for (int i = tid; i < KC * kPieces; i += 64 * WR)
           if (!((bits >> (i / kPieces)) & 1)) *reinterpret_cast<u32x4*>(z + i * 16) = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
       }
+      // S^T = K Q^T, the next 16 keys' operands read ahead of their products
       f32x4 sc[QT][kNT];
+      bf16x8 kf[2][kDK];
+      auto read_k = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < kDK; ++k)
+          kf[t & 1][k] = frag(*reinterpret_cast<const u32x4*>(st + kat[k] + t * 16 * D * 2));
+      };
+      read_k(0);
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
+        if (t + 1 < kNT) read_k(t + 1);
 #pragma unroll
         for (int u = 0; u < QT; ++u) sc[u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int kr = 16 * t + fr;
 #pragma unroll
-        for (int k = 0; k < kDK; ++k) {
-          const bf16x8 kf = frag(*reinterpret_cast<const u32x4*>(
-              sK + (kr * kPieces + ((4 * k + g) ^ (kr & (kPieces - 1)))) * 16));
+        for (int k = 0; k < kDK; ++k)
 #pragma unroll
           for (int u = 0; u < QT; ++u)
-            sc[u][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[u][k], sc[u][t], 0, 0, 0);
-        }
+            sc[u][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[t & 1][k], qf[u][k], sc[u][t], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       // keys that no row or not every row sees
       if (base + KC > (pre ? end : all_see) || (!pre && p.mask)) {
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
-          const int stop = pre ? end : min(end, lim[u]);
+          // bits of this lane's keys 16 t + 4 g + e, from the first one on
+          const int seen = min(max((pre ? end : min(end, lim[u])) - base, 0), KC);
+          const unsigned long long mine = (seen < KC ? bits & ((1ull << seen) - 1ull) : bits) >> (4 * g);
 #pragma unroll
           for (int t = 0; t < kNT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int kk = 16 * t + 4 * g + e;
-              if (base + kk >= stop || !((bits >> kk) & 1)) sc[u][t][e] = -INFINITY;
+              const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)(t < 2 ? mine : mine >> 32), (16 * t + e) & 31, 1);
+              sc[u][t][e] = __uint_as_float((__float_as_uint(sc[u][t][e]) & keep) | (0xff800000u & ~keep));
             }
         }
       }
       uint32_t pk[QT][kNT][2];
-      float cm[QT];
-      bool far = false;
-#pragma unroll
-      for (int u = 0; u < QT; ++u) {
-        float x = fmaxf(fmaxf(sc[u][0][0], sc[u][0][1]), fmaxf(sc[u][0][2], sc[u][0][3]));
-#pragma unroll
-        for (int t = 1; t < kNT; ++t)
-          x = fmaxf(fmaxf(x, fmaxf(sc[u][t][0], sc[u][t][1])), fmaxf(sc[u][t][2], sc[u][t][3]));
-        cm[u] = x * p.c;  // base-2 scores (c > 0)
-        far = far || cm[u] > m[u] + kSlack;
-      }
-      if (__any(far)) {
+      auto exponents = [&]() -> bool {
+        u16x2 top = {0, 0};
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
-          const float mn = fmaxf(m[u], group_max(cm[u]));
-          const float alpha = __builtin_amdgcn_exp2f(m[u] - (mn == -INFINITY ? 0.f : mn));
+          const float ref = m[u];
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) {
+            float e4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][t][e], p.c, -ref));
+            const bf16x2 lo = {static_cast<__bf16>(e4[0]), static_cast<__bf16>(e4[1])};
+            const bf16x2 hi = {static_cast<__bf16>(e4[2]), static_cast<__bf16>(e4[3])};
+            pk[u][t][0] = __builtin_bit_cast(uint32_t, lo);
+            pk[u][t][1] = __builtin_bit_cast(uint32_t, hi);
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, lo));
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, hi));
+          }
+        }
+        return max(top[0], top[1]) >= kSlackBits;
+      };
+      bool move = c == 0;
+      if (!move) move = __any(exponents());
+      if (move) {
+#pragma unroll
+        for (int u = 0; u < QT; ++u) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < kNT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x = fmaxf(x, sc[u][t][e]);
+          x = group_max(x);
+          // base-2 scores (c > 0), passed as the exponents above see it
+          const float mn = fmaf(x, p.c, -m[u]) > kSlack ? x * p.c : m[u];
+          const float alpha = __builtin_amdgcn_exp2f(m[u] - mn);
           m[u] = mn;
           l[u] *= alpha;
 #pragma unroll
           for (int j = 0; j < kND; ++j) o[u][j] *= alpha;
         }
-      }
-#pragma unroll
-      for (int u = 0; u < QT; ++u) {
-        const float ref = m[u] == -INFINITY ? 0.f : m[u];
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-          float e4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][t][e], p.c, -ref));
-          const bf16x2 lo = {static_cast<__bf16>(e4[0]), static_cast<__bf16>(e4[1])};
-          const bf16x2 hi = {static_cast<__bf16>(e4[2]), static_cast<__bf16>(e4[3])};
-          pk[u][t][0] = __builtin_bit_cast(uint32_t, lo);
-          pk[u][t][1] = __builtin_bit_cast(uint32_t, hi);
-        }
+        exponents();
       }
       // O^T += V^T P^T: k-slots 8 g .. 8 g + 7 carry keys 32 c + 4 g + (0..3)
       // and 32 c + 16 + 4 g + (0..3) on both sides; a row of ones in the place
       // of V^T gives l, the sum of the probabilities as the product takes them
-      const int vkey = 4 * g + (fr >> 2);
+      constexpr int kGroup = 4, kPer = kND / kGroup, kGroups = KC / 32 * kPer;  // of four 16-dim columns
+      bf16x8 vf[2][kGroup];
+      auto read_v = [&](int n) {
 #pragma unroll
-      for (int cc = 0; cc < KC / 32; ++cc) {
-        const int kr = 32 * cc + vkey;
-        const unsigned char* vrow = sV + kr * D * 2 + (fr & 1) * 8;
+        for (int j = 0; j < kGroup; ++j) {
+          const unsigned char* v = st + vat[(n % kPer) * kGroup + j] + (n / kPer) * 32 * D * 2;
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 16 * D * 2));
+          const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+          vf[n & 1][j] = frag(u32x4{l2[0], l2[1], h2[0], h2[1]});
+        }
+      };
+      read_v(0);
+#pragma unroll
+      for (int n = 0; n < kGroups; ++n) {
+        if (n + 1 < kGroups) read_v(n + 1);
+        const int cc = n / kPer;
         bf16x8 pf[QT];
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
           pf[u] = frag(u32x4{pk[u][2 * cc][0], pk[u][2 * cc][1], pk[u][2 * cc + 1][0], pk[u][2 * cc + 1][1]});
-          l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[u], l[u], 0, 0, 0);
+          if (n % kPer == 0) l[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, pf[u], l[u], 0, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < kND; ++j) {
-          const int pc = 2 * j + ((fr & 3) >> 1);
-          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4*)(vrow + ((pc ^ (kr & (kPieces - 1))) << 4)));
-          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_s16x4*)(vrow + 16 * D * 2 + ((pc ^ ((kr + 16) & (kPieces - 1))) << 4)));
-          const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
-          const bf16x8 vf = frag(u32x4{l2[0], l2[1], h2[0], h2[1]});
+        for (int j = 0; j < kGroup; ++j)
 #pragma unroll
-          for (int u = 0; u < QT; ++u)
-            o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u], o[u][j], 0, 0, 0);
-        }
+          for (int u = 0; u < QT; ++u) {
+            f32x4& acc = o[u][(n % kPer) * kGroup + j];
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[n & 1][j], pf[u], acc, 0, 0, 0);
+          }
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    if (nc > 0) load(0, 0);
+    for (int c = 0; c < nc; c += 2) {
+      step(c, std::integral_constant<int, 0>{});
+      if (c + 1 < nc) step(c + 1, std::integral_constant<int, 1>{});
     }
 
     // o[u][j][e] = O^T[dim 16 j + 4 g + e][row]
@@ -608,17 +667,16 @@ __device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, 
   const int hk = item % p.Hk;
   const int rest = item / p.Hk;
   const int tile = rest % tiles, part = rest / tiles;
-  long long row0, row_end;
+  int row0, row_end;
   int b = -1;
   if (seq) {
     const int per = tiles / p.B;
     b = tile / per;
-    row0 = (long long)b * p.RS + (long long)(tile - b * per) * T::kRows;
-    row_end = (long long)(b + 1) * p.RS;
-    if (p.q_len) row_end = min(row_end, (long long)b * p.RS + (long long)min(max(p.q_len[b], 0), p.Tq) * p.G);
+    row0 = b * p.RS + (tile - b * per) * T::kRows;
+    row_end = b * p.RS + (p.q_len ? min(max(p.q_len[b], 0), p.Tq) * p.G : p.RS);
     if (row0 >= row_end) return;
   } else {
-    row0 = (long long)tile * T::kRows;
+    row0 = tile * T::kRows;
     row_end = p.RT;
   }
   int p0 = 0, p1 = 0, s0 = 0, s1 = 0;
@@ -639,11 +697,13 @@ __device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, 
   T::run(p, lds, hk, own == 0 ? -1 : b, row0, row_end, p0, p1, s0, s1, slot0 + part);
 }
 
-template <int D>
+// KIND: 1 wide items, 2 thin items, 3 both lists in one launch (the thin ones,
+// which wait for memory, beside the wide ones, which compute).
+template <int D, int KIND>
 __global__ __launch_bounds__(256, 2) void prefix_attn_kernel(PaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int bid = blockIdx.x;
-  if (bid < p.n_wide)
+  if (KIND == 1 || (KIND == 3 && bid < p.n_wide))
     run_item<Wide<D>>(p, lds, bid, p.wide_seq, p.wide_tiles, p.wide_parts, p.wide_own, 0);
   else
     run_item<Thin<D>>(p, lds, bid - p.n_wide, p.thin_seq, p.thin_tiles, p.thin_parts, p.thin_own, p.thin_slot);
@@ -739,8 +799,14 @@ size_t al256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 template <int D>
 hipError_t run(const PaParams& p, const Plan& pl, hipStream_t st) {
-  constexpr int lds = Wide<D>::kLds > Thin<D>::kLds ? Wide<D>::kLds : Thin<D>::kLds;
-  hipLaunchKernelGGL((prefix_attn_kernel<D>), dim3((unsigned)(pl.n_wide + pl.n_thin)), dim3(256), lds, st, p);
+  const dim3 grid((unsigned)(pl.n_wide + pl.n_thin));
+  constexpr int both = Wide<D>::kLds > Thin<D>::kLds ? Wide<D>::kLds : Thin<D>::kLds;
+  if (pl.n_thin == 0)
+    hipLaunchKernelGGL((prefix_attn_kernel<D, 1>), grid, dim3(256), Wide<D>::kLds, st, p);
+  else if (pl.n_wide == 0)
+    hipLaunchKernelGGL((prefix_attn_kernel<D, 2>), grid, dim3(256), Thin<D>::kLds, st, p);
+  else
+    hipLaunchKernelGGL((prefix_attn_kernel<D, 3>), grid, dim3(256), both, st, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slots == 1) return e;
   const long long rows = (long long)p.Hk * p.RT;
