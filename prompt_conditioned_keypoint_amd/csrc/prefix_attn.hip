@@ -11,10 +11,11 @@
 // (their keys pass through LDS once per tile of rows, not once per
 // sequence), own keys sequence by sequence, and long ranges in parts.
 //
-// Two tiles, of 256 threads each:
+// Two tiles:
 //   wide   128 rows, four waves of 32 rows, key chunks of 64 shared by them;
-//   thin   16 rows, four waves that take every fourth 32-key chunk and join
-//          at the end: for few rows, where reading the keys is all there is.
+//   thin   16 rows, four or eight waves that take every fourth or eighth
+//          32-key chunk and join at the end: for few rows, where reading the
+//          keys is all there is.
 #include "gkd_device.hpp"
 #include "tokens_launch.hpp"
 
@@ -50,286 +51,102 @@ struct PaParams {
 
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-template <int D, int WR, int WK, int QT, int KC>
-struct ThinTile {
-  static constexpr int kRows = 16 * QT * WR;
-  static constexpr int kPieces = D / 8;                       // 16-byte pieces of a key row
-  static constexpr int kNP = KC * kPieces / (64 * WR);        // pieces a thread stages, K and V each
-  static constexpr int kMat = KC * D * 2;                     // bytes of a chunk's K (or V)
-  static constexpr int kStage = WK * 2 * kMat;
-  static constexpr int kLds = 2 * kStage;
-  static constexpr int kNT = KC / 16, kDK = D / 32, kND = D / 16;
-
-  static __device__ __forceinline__ void run(const PaParams& p, unsigned char* lds, int hk, int b_own,
-                                             int row0, int row_end, int p0, int p1, int s0, int s1,
-                                             int slot) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = wave % WR, wk = wave / WR;
-    const int fr = lane & 15, g = lane >> 4;
-    const int tidc = wr * 64 + lane;  // thread within its key column
-
-    // this lane's rows (query fr of each of its 16-row groups)
-    bf16x8 qf[QT][kDK];
-    int R[QT];
-    bool live[QT];
-    int lim[QT];      // own keys below this are visible
-    long long oaddr[QT];
-    int own_end = s1;
-#pragma unroll
-    for (int u = 0; u < QT; ++u) {
-      live[u] = (wr * QT + u) * 16 + fr < row_end - row0;
-      R[u] = live[u] ? row0 + (wr * QT + u) * 16 + fr : row_end - 1;
-      const int b = (int)((unsigned)R[u] / (unsigned)p.RS), rr = R[u] - b * p.RS;
-      const int t = (int)((unsigned)rr / (unsigned)p.G), h = hk * p.G + (rr - t * p.G);
-      const int ql = p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
-      live[u] = live[u] && t < ql;
-      lim[u] = 0x7fffffff;
-      if (p.causal && b_own >= 0) {
-        const int len = p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
-        lim[u] = len - ql + t + 1;
-      }
-      const uint16_t* src = static_cast<const uint16_t*>(p.q.p) + b * p.q.b + t * p.q.t + h * p.q.h;
-#pragma unroll
-      for (int k = 0; k < kDK; ++k)
-        qf[u][k] = frag(*reinterpret_cast<const u32x4*>(src + 32 * k + 8 * g));
-      oaddr[u] = b * p.out.b + t * p.out.t + h * p.out.h;
-    }
-    if (b_own >= 0) {
-      own_end = min(s1, p.own_len ? min(max(p.own_len[b_own], 0), p.S) : p.S);
-      if (p.causal) {  // no row of the tile sees past its last one's limit
-        const int first = row0 - b_own * p.RS, last = min(first + kRows, row_end - b_own * p.RS) - 1;
-        const int t = (int)((unsigned)last / (unsigned)p.G);
-        const int ql = p.q_len ? min(max(p.q_len[b_own], 0), p.Tq) : p.Tq;
-        const int len = p.own_len ? min(max(p.own_len[b_own], 0), p.S) : p.S;
-        own_end = min(own_end, len - ql + t + 1);
-      }
-    }
-    const int nprefix = p1 > p0 ? (p1 - p0 + KC - 1) / KC : 0;
-    const int nown = own_end > s0 ? (own_end - s0 + KC - 1) / KC : 0;
-    const int nc = nprefix + nown;
-    const int nit = (nc + WK - 1) / WK;
-
-    f32x4 o[QT][kND];
-    float m[QT], l[QT];
-#pragma unroll
-    for (int u = 0; u < QT; ++u) {
-      m[u] = -INFINITY;
-      l[u] = 0.f;
-#pragma unroll
-      for (int j = 0; j < kND; ++j) o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-
-    u32x4 kreg[kNP], vreg[kNP];
-    // chunk c of this column: where its keys are
-    auto load = [&](int it) {
-      const int c = it * WK + wk;
-      const u32x4 z = {0u, 0u, 0u, 0u};
-      const bool pre = c < nprefix;
-      const int base = pre ? p0 + c * KC : s0 + (c - nprefix) * KC;
-      const int end = c >= nc ? base : pre ? p1 : own_end;
-      const Heads& hk_ = pre ? p.kp : p.ko;
-      const Heads& hv_ = pre ? p.vp : p.vo;
-      const long long ob = pre ? 0 : (long long)b_own;
-      const uint16_t* ks = static_cast<const uint16_t*>(hk_.p) + ob * hk_.b + hk * hk_.h;
-      const uint16_t* vs = static_cast<const uint16_t*>(hv_.p) + ob * hv_.b + hk * hv_.h;
-#pragma unroll
-      for (int i = 0; i < kNP; ++i) {
-        const int s = tidc + 64 * WR * i, r = s / kPieces, pc = s % kPieces;
-        const long long key = base + r;
-        bool in = key < end;
-        kreg[i] = vreg[i] = z;
-        if (in) {
-          kreg[i] = *reinterpret_cast<const u32x4*>(ks + key * hk_.t + 8 * pc);
-          // masked values may hold anything: they enter the product as zeros
-          if (!pre && p.mask) in = p.mask[ob * p.S + key] != 0;
-          if (in) vreg[i] = *reinterpret_cast<const u32x4*>(vs + key * hv_.t + 8 * pc);
-        }
-      }
-    };
-    auto store = [&](int buf) {
-      unsigned char* st = lds + buf * kStage + wk * 2 * kMat;
-#pragma unroll
-      for (int i = 0; i < kNP; ++i) {
-        const int s = tidc + 64 * WR * i, r = s / kPieces, pc = s % kPieces;
-        const int at = (r * kPieces + (pc ^ (r & (kPieces - 1)))) * 16;
-        *reinterpret_cast<u32x4*>(st + at) = kreg[i];
-        *reinterpret_cast<u32x4*>(st + kMat + at) = vreg[i];
-      }
-    };
-
-    if (nit > 0) {
-      load(0);
-      store(0);
-    }
-    __syncthreads();
-    for (int it = 0; it < nit; ++it) {
-      if (it + 1 < nit) load(it + 1);
-      const int c = it * WK + wk;
-      if (c < nc) {
-        const unsigned char* sK = lds + (it & 1) * kStage + wk * 2 * kMat;
-        const unsigned char* sV = sK + kMat;
-        const bool pre = c < nprefix;
-        const int base = pre ? p0 + c * KC : s0 + (c - nprefix) * KC;
-        const int end = pre ? p1 : own_end;
-        f32x4 sc[QT][kNT];
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-#pragma unroll
-          for (int u = 0; u < QT; ++u) sc[u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-          const int kr = 16 * t + fr;
-#pragma unroll
-          for (int k = 0; k < kDK; ++k) {
-            const bf16x8 kf = frag(*reinterpret_cast<const u32x4*>(
-                sK + (kr * kPieces + ((4 * k + g) ^ (kr & (kPieces - 1)))) * 16));
-#pragma unroll
-            for (int u = 0; u < QT; ++u)
-              sc[u][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[u][k], sc[u][t], 0, 0, 0);
-          }
-        }
-        // keys that no row or not every row sees
-        if (base + KC > end || (!pre && (p.causal || p.mask))) {
-          unsigned long long bits = ~0ull;
-          if (!pre && p.mask) {
-            const bool on = base + lane < end && lane < KC && p.mask[(long long)b_own * p.S + base + lane] != 0;
-            bits = __ballot(on);
-          }
-#pragma unroll
-          for (int u = 0; u < QT; ++u) {
-            const int stop = pre ? end : min(end, lim[u]);
-#pragma unroll
-            for (int t = 0; t < kNT; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int kk = 16 * t + 4 * g + e;
-                if (base + kk >= stop || !((bits >> kk) & 1)) sc[u][t][e] = -INFINITY;
-              }
-          }
-        }
-        uint32_t pk[QT][kNT][2];
-#pragma unroll
-        for (int u = 0; u < QT; ++u) {
-          float cm = -INFINITY;
-#pragma unroll
-          for (int t = 0; t < kNT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cm = fmaxf(cm, sc[u][t][e]);
-          cm = fmaxf(cm, __shfl_xor(cm, 16));
-          cm = fmaxf(cm, __shfl_xor(cm, 32));
-          cm *= p.c;  // base-2 scores (c > 0)
-          const float mn = fmaxf(m[u], cm);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          const float alpha = __builtin_amdgcn_exp2f(m[u] - ref);
-          m[u] = mn;
-          float ps = 0.f;
-#pragma unroll
-          for (int t = 0; t < kNT; ++t) {
-            float e4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][t][e], p.c, -ref));
-              ps += e4[e];
-            }
-            const bf16x2 lo = {static_cast<__bf16>(e4[0]), static_cast<__bf16>(e4[1])};
-            const bf16x2 hi = {static_cast<__bf16>(e4[2]), static_cast<__bf16>(e4[3])};
-            pk[u][t][0] = __builtin_bit_cast(uint32_t, lo);
-            pk[u][t][1] = __builtin_bit_cast(uint32_t, hi);
-          }
-          l[u] = l[u] * alpha + ps;
-#pragma unroll
-          for (int j = 0; j < kND; ++j) o[u][j] *= alpha;
-        }
-        // O^T += V^T P^T: k-slots 8 g .. 8 g + 7 carry keys 32 c + 4 g + (0..3)
-        // and 32 c + 16 + 4 g + (0..3) on both sides
-        const int vkey = 4 * g + (fr >> 2);
-#pragma unroll
-        for (int cc = 0; cc < KC / 32; ++cc) {
-          const int kr = 32 * cc + vkey;
-          const unsigned char* vrow = sV + kr * D * 2 + (fr & 1) * 8;
-#pragma unroll
-          for (int j = 0; j < kND; ++j) {
-            const int pc = 2 * j + ((fr & 3) >> 1);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4*)(vrow + ((pc ^ (kr & (kPieces - 1))) << 4)));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4*)(vrow + 16 * D * 2 + ((pc ^ ((kr + 16) & (kPieces - 1))) << 4)));
-            const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
-            const bf16x8 vf = frag(u32x4{l2[0], l2[1], h2[0], h2[1]});
-#pragma unroll
-            for (int u = 0; u < QT; ++u)
-              o[u][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  vf, frag(u32x4{pk[u][2 * cc][0], pk[u][2 * cc][1], pk[u][2 * cc + 1][0], pk[u][2 * cc + 1][1]}),
-                  o[u][j], 0, 0, 0);
-          }
-        }
-      }
-      if (it + 1 < nit) store((it + 1) & 1);
-      __syncthreads();
-    }
-#pragma unroll
-    for (int u = 0; u < QT; ++u) {
-      l[u] += __shfl_xor(l[u], 16);
-      l[u] += __shfl_xor(l[u], 32);
-    }
-
-    if constexpr (WK > 1) {
-      // the columns join in LDS, in order
-      constexpr int kPer = QT * kND * 64;  // f32x4 a wave
-      static_assert((WK - 1) * WR * (kPer * 16 + QT * 64 * 8) <= kLds, "the joined results fit");
-      f32x4* so = reinterpret_cast<f32x4*>(lds);
-      f32x2* sm = reinterpret_cast<f32x2*>(lds + (WK - 1) * WR * kPer * 16);
-      if (wk > 0) {
-        const int w = (wk - 1) * WR + wr;
-#pragma unroll
-        for (int u = 0; u < QT; ++u) {
-#pragma unroll
-          for (int j = 0; j < kND; ++j) so[w * kPer + (u * kND + j) * 64 + lane] = o[u][j];
-          sm[(w * QT + u) * 64 + lane] = f32x2{m[u], l[u]};
-        }
-      }
-      __syncthreads();
-      if (wk > 0) return;
-#pragma unroll
-      for (int v = 0; v < WK - 1; ++v) {
-        const int w = v * WR + wr;
-#pragma unroll
-        for (int u = 0; u < QT; ++u) {
-          const f32x2 x = sm[(w * QT + u) * 64 + lane];
-          const float mn = fmaxf(m[u], x[0]);
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          const float a = __builtin_amdgcn_exp2f(m[u] - ref), bsc = __builtin_amdgcn_exp2f(x[0] - ref);
-          m[u] = mn;
-          l[u] = l[u] * a + x[1] * bsc;
-#pragma unroll
-          for (int j = 0; j < kND; ++j) o[u][j] = o[u][j] * a + so[w * kPer + (u * kND + j) * 64 + lane] * bsc;
-        }
-      }
-    }
-
-    // o[u][j][e] = O^T[dim 16 j + 4 g + e][row]
-#pragma unroll
-    for (int u = 0; u < QT; ++u) {
-      if (!live[u]) continue;
-      if (p.slots == 1) {
-        const float inv = l[u] > 0.f ? 1.f / l[u] : 0.f;
-        uint16_t* dst = static_cast<uint16_t*>(p.out.p) + oaddr[u] + 4 * g;
-#pragma unroll
-        for (int j = 0; j < kND; ++j) {
-          const bf16x2 lo = {static_cast<__bf16>(o[u][j][0] * inv), static_cast<__bf16>(o[u][j][1] * inv)};
-          const bf16x2 hi = {static_cast<__bf16>(o[u][j][2] * inv), static_cast<__bf16>(o[u][j][3] * inv)};
-          *reinterpret_cast<u32x2*>(dst + 16 * j) =
-              u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-        }
-      } else {
-        const long long at = ((long long)slot * p.Hk + hk) * p.RT + R[u];
-        if (g == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m[u], l[u]};
-        if (nc == 0) continue;  // the statistics say that there is nothing
-#pragma unroll
-        for (int j = 0; j < kND; ++j) *reinterpret_cast<f32x4*>(p.po + at * D + 16 * j + 4 * g) = o[u][j];
-      }
-    }
-  }
+// A tile's rows and keys, the same for both kinds of tile.
+struct TileWork {
+  int hk;            // key head
+  int b;             // sequence of the own keys, -1: prefix keys only
+  int row0, n;       // packed tiles: first packed row; others: first row R, rows
+  bool packed;       // rows are those in use of all sequences, one after another
+  int p0, p1;        // prefix keys
+  int s0, s1;        // own keys
+  int slot;
 };
+
+// Query rows of a lane: their places, and how far they see.
+struct RowPlace {
+  int R;             // row of the key head
+  bool live;
+  int lim;           // own keys below this are visible
+  long long q, out;  // element offsets
+};
+
+__device__ __forceinline__ int own_length(const PaParams& p, int b) {
+  return p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
+}
+__device__ __forceinline__ int query_length(const PaParams& p, int b) {
+  return p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
+}
+
+// Row i of the tile. `cum`: for packed tiles, the packed rows before each
+// sequence (B + 1 of them, in LDS).
+__device__ __forceinline__ RowPlace place_row(const PaParams& p, const TileWork& w, const int* cum, int i) {
+  RowPlace r;
+  r.live = i < w.n;
+  unsigned b, rr;
+  if (w.packed && p.q_len) {
+    const int at = w.row0 + (r.live ? i : w.n - 1);
+    int lo = 0, hi = p.B;  // cum[lo] <= at < cum[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    rr = at - cum[lo];
+  } else {
+    const unsigned at = w.row0 + (r.live ? i : w.n - 1);
+    b = at / (unsigned)p.RS;
+    rr = at - b * p.RS;
+  }
+  const unsigned t = rr / (unsigned)p.G;
+  const int h = w.hk * p.G + (int)(rr - t * p.G);
+  r.R = (int)(b * p.RS + rr);
+  r.lim = 0x7fffffff;
+  if (p.causal && w.b >= 0) r.lim = own_length(p, w.b) - query_length(p, w.b) + (int)t + 1;
+  r.q = b * p.q.b + t * p.q.t + h * p.q.h;
+  r.out = b * p.out.b + t * p.out.t + h * p.out.h;
+  return r;
+}
+
+// The own keys that the tile's last row sees, and those that every row sees.
+__device__ __forceinline__ void own_ends(const PaParams& p, const TileWork& w, int& last, int& all) {
+  last = all = w.s1;
+  if (w.b < 0) return;
+  const int len = own_length(p, w.b);
+  last = all = min(w.s1, len);
+  if (p.causal) {
+    const int first = w.row0 - w.b * p.RS, before = len - query_length(p, w.b) + 1;
+    last = min(last, before + (int)((unsigned)(first + w.n - 1) / (unsigned)p.G));
+    all = min(all, before + (int)((unsigned)first / (unsigned)p.G));
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// A row's result: O^T[dim 16 j + 4 g + e] in o[j][e], l and m the same in all
+// its lanes.
+template <int D>
+__device__ __forceinline__ void write_row(const PaParams& p, const TileWork& w, const RowPlace& r, int g,
+                                          float m, float l, const f32x4 (&o)[D / 16], bool any_keys) {
+  if (!r.live) return;
+  if (p.slots == 1) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t* dst = static_cast<uint16_t*>(p.out.p) + r.out + 4 * g;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+      *reinterpret_cast<u32x2*>(dst + 16 * j) =
+          u32x2{bf16_pair(o[j][0] * inv, o[j][1] * inv), bf16_pair(o[j][2] * inv, o[j][3] * inv)};
+    return;
+  }
+  const long long at = ((long long)w.slot * p.Hk + w.hk) * p.RT + r.R;
+  if (g == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m, l};
+  if (!any_keys) return;  // the statistics say that there is nothing
+#pragma unroll
+  for (int j = 0; j < D / 16; ++j) *reinterpret_cast<f32x4*>(p.po + at * D + 16 * j + 4 * g) = o[j];
+}
 
 // max over the four 16-lane groups of a wave
 __device__ __forceinline__ float group_max(float x) {
@@ -338,6 +155,178 @@ __device__ __forceinline__ float group_max(float x) {
   const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+
+// ---------------------------------------------------------------------------
+// 16 rows, WK waves that take every WK-th 32-key chunk and join at the end. A
+// wave's K rows go straight into registers as the product's operand and its V
+// rows into its own 32 rows of LDS (the product takes them transposed), with
+// nothing in flight beside them: what hides a chunk's latency are the other
+// waves of the CU, 16 KB of keys each (D = 128).
+// ---------------------------------------------------------------------------
+template <int D, int WK>
+struct ThinTile {
+  static constexpr int KC = 32, kRows = 16;
+  static constexpr int kPieces = D / 8, kDK = D / 32, kND = D / 16;
+  static constexpr int kMat = KC * D * 2;
+  static constexpr int kJoin = (WK - 1) * (kND * 1024 + 512);  // the waves' results at the end
+  static constexpr int kLds = WK * kMat > kJoin ? WK * kMat : kJoin;
+  static constexpr int kLoads = kMat / 1024, kBlkRows = 64 / kPieces;
+
+  static __device__ __forceinline__ void run(const PaParams& p, const TileWork& w, unsigned char* lds, const int* cum) {
+    const int lane = threadIdx.x & 63;
+    const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int fr = lane & 15, g = lane >> 4;
+    const RowPlace row = place_row(p, w, cum, fr);
+    if (cum) __syncthreads();  // looked up by all before keys come into its place
+    bf16x8 qf[kDK];
+#pragma unroll
+    for (int k = 0; k < kDK; ++k)
+      qf[k] = frag(row.live ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.q.p) + row.q + 32 * k + 8 * g)
+                            : u32x4{0u, 0u, 0u, 0u});
+    int own_end, all_see;
+    own_ends(p, w, own_end, all_see);
+    const int nprefix = w.p1 > w.p0 ? (w.p1 - w.p0 + KC - 1) / KC : 0;
+    const int nown = own_end > w.s0 ? (own_end - w.s0 + KC - 1) / KC : 0;
+    const int nc = nprefix + nown;
+
+    f32x4 o[kND];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kND; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    unsigned char* sV = lds + wk * kMat;
+    const int lr = lane / kPieces, vkey = 4 * g + (fr >> 2);
+    for (int c = wk; c < nc; c += WK) {
+      const bool pre = c < nprefix;
+      const int base = pre ? w.p0 + c * KC : w.s0 + (c - nprefix) * KC;
+      const int end = pre ? w.p1 : own_end;
+      const int keys = min(end - base, KC);
+      const Heads& hk = pre ? p.kp : p.ko;
+      const Heads& hv = pre ? p.vp : p.vo;
+      const long long ob = pre ? 0 : (long long)w.b;
+      uint16_t* ks = static_cast<uint16_t*>(hk.p) + ob * hk.b + w.hk * hk.h + (long long)base * hk.t;
+      uint16_t* vs = static_cast<uint16_t*>(hv.p) + ob * hv.b + w.hk * hv.h + (long long)base * hv.t;
+      const uint32_t kt = (uint32_t)hk.t * 2u, vt = (uint32_t)hv.t * 2u;
+      // rows past the last key are past the buffer's end and come out as zeros
+      const auto kb = __builtin_amdgcn_make_buffer_rsrc(ks, 0, (int)((uint32_t)(keys - 1) * kt + D * 2), 0x00020000);
+      const auto vb = __builtin_amdgcn_make_buffer_rsrc(vs, 0, (int)((uint32_t)(keys - 1) * vt + D * 2), 0x00020000);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the last chunk's V is out of LDS
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = i * kBlkRows + lr;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(vb, (lds_void*)(sV + i * 1024), 16,
+                                                 (int)(r * vt + 16 * ((lane % kPieces) ^ (r & (kPieces - 1)))), 0, 0, 0);
+      }
+      bf16x8 kf[2][kDK];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < kDK; ++k)
+          kf[t][k] = frag(__builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+              kb, (int)((16 * t + fr) * kt + 64 * k + 16 * g), 0, 0)));
+      uint32_t bits = ~0u;  // keys in use
+      if (!pre && p.mask) {
+        const bool on = lane < keys && p.mask[(long long)w.b * p.S + base + lane] != 0;
+        bits = (uint32_t)__ballot(on);
+      }
+      f32x4 sc[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        sc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kDK; ++k) sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[t][k], qf[k], sc[t], 0, 0, 0);
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): V is in LDS
+      asm volatile("" ::: "memory");
+      if (~bits != 0u) {
+        // masked values may hold anything: they enter the product as zeros
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (!((bits >> (i * kBlkRows + lr)) & 1))
+            *reinterpret_cast<u32x4*>(sV + i * 1024 + lane * 16) = u32x4{0u, 0u, 0u, 0u};
+      }
+      if (base + KC > (pre ? end : all_see) || ~bits != 0u) {
+        const int seen = min(max((pre ? end : min(end, row.lim)) - base, 0), KC);
+        const uint32_t mine = (seen < KC ? bits & ((1u << seen) - 1u) : bits) >> (4 * g);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)mine, 16 * t + e, 1);
+            sc[t][e] = __uint_as_float((__float_as_uint(sc[t][e]) & keep) | (0xff800000u & ~keep));
+          }
+      }
+      float x = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x = fmaxf(x, sc[t][e]);
+      const float mn = fmaxf(m, group_max(x) * p.c);  // base-2 scores (c > 0)
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float alpha = __builtin_amdgcn_exp2f(m - ref);
+      m = mn;
+      l *= alpha;
+#pragma unroll
+      for (int j = 0; j < kND; ++j) o[j] *= alpha;
+      uint32_t pk[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float e4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[t][e], p.c, -ref));
+          l += e4[e];
+        }
+        pk[t][0] = bf16_pair(e4[0], e4[1]);
+        pk[t][1] = bf16_pair(e4[2], e4[3]);
+      }
+      // O^T += V^T P^T: k-slots 8 g .. 8 g + 7 carry keys 4 g + (0..3) and
+      // 16 + 4 g + (0..3) on both sides
+      const bf16x8 pf = frag(u32x4{pk[0][0], pk[0][1], pk[1][0], pk[1][1]});
+#pragma unroll
+      for (int j = 0; j < kND; ++j) {
+        const unsigned char* v = sV + vkey * D * 2 + (((2 * j + ((fr & 3) >> 1)) ^ (vkey & (kPieces - 1))) << 4) + (fr & 1) * 8;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 16 * D * 2));
+        const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
+        o[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(u32x4{l2[0], l2[1], h2[0], h2[1]}), pf, o[j], 0, 0, 0);
+      }
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+
+    // the waves join in LDS, in order
+    f32x4* so = reinterpret_cast<f32x4*>(lds);
+    f32x2* sm = reinterpret_cast<f32x2*>(lds + (WK - 1) * kND * 1024);
+    __syncthreads();  // V is read
+    if (wk > 0) {
+#pragma unroll
+      for (int j = 0; j < kND; ++j) so[((wk - 1) * kND + j) * 64 + lane] = o[j];
+      sm[(wk - 1) * 64 + lane] = f32x2{m, l};
+    }
+    __syncthreads();
+    if (wk > 0) return;
+    float top = m;
+#pragma unroll
+    for (int v = 0; v < WK - 1; ++v) top = fmaxf(top, sm[v * 64 + lane][0]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float a = __builtin_amdgcn_exp2f(m - ref);
+    m = top;
+    l *= a;
+#pragma unroll
+    for (int j = 0; j < kND; ++j) o[j] *= a;
+    for (int v = 0; v < WK - 1; ++v) {
+      const f32x2 x = sm[v * 64 + lane];
+      const float wgt = __builtin_amdgcn_exp2f(x[0] - ref);
+      l = fmaf(x[1], wgt, l);
+#pragma unroll
+      for (int j = 0; j < kND; ++j) o[j] += so[(v * kND + j) * 64 + lane] * wgt;
+    }
+    write_row<D>(p, w, row, g, m, l, o, nc > 0);
+  }
+};
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
@@ -372,48 +361,26 @@ struct WideTile {
   static constexpr int kLoads = kMat / (WR * 1024);     // 1-KB loads a wave and matrix
   static constexpr int kBlkRows = 64 / kPieces;         // key rows of one load
 
-  static __device__ __forceinline__ void run(const PaParams& p, unsigned char* lds, int hk, int b_own,
-                                             int row0, int row_end, int p0, int p1, int s0, int s1,
-                                             int slot) {
+  static __device__ __forceinline__ void run(const PaParams& p, const TileWork& w, unsigned char* lds, const int* cum) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wr = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fr = lane & 15, g = lane >> 4;
+    const int hk = w.hk, b_own = w.b, p0 = w.p0, p1 = w.p1, s0 = w.s0;
 
     bf16x8 qf[QT][kDK];
-    int lim[QT];      // own keys below this are visible
-    bool live[QT];
-    long long oaddr[QT];
+    RowPlace row[QT];
 #pragma unroll
     for (int u = 0; u < QT; ++u) {
-      const int n = (wr * QT + u) * 16 + fr;
-      live[u] = n < row_end - row0;
-      const unsigned r = live[u] ? row0 + n : row_end - 1;
-      const unsigned b = r / (unsigned)p.RS, rr = r - b * p.RS, t = rr / (unsigned)p.G;
-      const int h = hk * p.G + (int)(rr - t * p.G);
-      const int ql = p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
-      live[u] = live[u] && (int)t < ql;
-      lim[u] = 0x7fffffff;
-      if (p.causal && b_own >= 0) {
-        const int len = p.own_len ? min(max(p.own_len[b], 0), p.S) : p.S;
-        lim[u] = len - ql + (int)t + 1;
-      }
-      const uint16_t* src = static_cast<const uint16_t*>(p.q.p) + b * p.q.b + t * p.q.t + h * p.q.h;
+      row[u] = place_row(p, w, cum, (wr * QT + u) * 16 + fr);
+      const uint16_t* src = static_cast<const uint16_t*>(p.q.p) + row[u].q;
 #pragma unroll
       for (int k = 0; k < kDK; ++k)
-        qf[u][k] = frag(live[u] ? *reinterpret_cast<const u32x4*>(src + 32 * k + 8 * g) : u32x4{0u, 0u, 0u, 0u});
-      oaddr[u] = b * p.out.b + t * p.out.t + h * p.out.h;
+        qf[u][k] = frag(row[u].live ? *reinterpret_cast<const u32x4*>(src + 32 * k + 8 * g) : u32x4{0u, 0u, 0u, 0u});
     }
-    int own_end = s1, all_see = s1;  // own keys of the tile; those that every row sees
-    if (b_own >= 0) {
-      const int len = p.own_len ? min(max(p.own_len[b_own], 0), p.S) : p.S;
-      own_end = all_see = min(s1, len);
-      if (p.causal) {
-        const int ql = p.q_len ? min(max(p.q_len[b_own], 0), p.Tq) : p.Tq;
-        const int first = row0 - b_own * p.RS, last = min(first + kRows, row_end - b_own * p.RS) - 1;
-        own_end = min(own_end, len - ql + (int)((unsigned)last / (unsigned)p.G) + 1);
-        all_see = min(all_see, len - ql + (int)((unsigned)first / (unsigned)p.G) + 1);
-      }
-    }
+    if (cum) __syncthreads();  // looked up by all before keys come into its place
+    const bool idle = wr * QT * 16 >= w.n;  // a wave without rows: it loads, and leaves the pipes to others
+    int own_end, all_see;
+    own_ends(p, w, own_end, all_see);
     const int nprefix = p1 > p0 ? (p1 - p0 + KC - 1) / KC : 0;
     const int nown = own_end > s0 ? (own_end - s0 + KC - 1) / KC : 0;
     const int nc = nprefix + nown;
@@ -502,6 +469,7 @@ struct WideTile {
           if (!((bits >> (i / kPieces)) & 1)) *reinterpret_cast<u32x4*>(z + i * 16) = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
       }
+      if (idle) return;
       // S^T = K Q^T, the next 16 keys' operands read ahead of their products
       f32x4 sc[QT][kNT];
       bf16x8 kf[2][kDK];
@@ -528,7 +496,7 @@ struct WideTile {
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
           // bits of this lane's keys 16 t + 4 g + e, from the first one on
-          const int seen = min(max((pre ? end : min(end, lim[u])) - base, 0), KC);
+          const int seen = min(max((pre ? end : min(end, row[u].lim)) - base, 0), KC);
           const unsigned long long mine = (seen < KC ? bits & ((1ull << seen) - 1ull) : bits) >> (4 * g);
 #pragma unroll
           for (int t = 0; t < kNT; ++t)
@@ -550,12 +518,10 @@ struct WideTile {
             float e4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][t][e], p.c, -ref));
-            const bf16x2 lo = {static_cast<__bf16>(e4[0]), static_cast<__bf16>(e4[1])};
-            const bf16x2 hi = {static_cast<__bf16>(e4[2]), static_cast<__bf16>(e4[3])};
-            pk[u][t][0] = __builtin_bit_cast(uint32_t, lo);
-            pk[u][t][1] = __builtin_bit_cast(uint32_t, hi);
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, lo));
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, hi));
+            pk[u][t][0] = bf16_pair(e4[0], e4[1]);
+            pk[u][t][1] = bf16_pair(e4[2], e4[3]);
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, pk[u][t][0]));
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, pk[u][t][1]));
           }
         }
         return max(top[0], top[1]) >= kSlackBits;
@@ -623,28 +589,8 @@ struct WideTile {
       if (c + 1 < nc) step(c + 1, std::integral_constant<int, 1>{});
     }
 
-    // o[u][j][e] = O^T[dim 16 j + 4 g + e][row]
 #pragma unroll
-    for (int u = 0; u < QT; ++u) {
-      if (!live[u]) continue;
-      if (p.slots == 1) {
-        const float inv = l[u][0] > 0.f ? 1.f / l[u][0] : 0.f;
-        uint16_t* dst = static_cast<uint16_t*>(p.out.p) + oaddr[u] + 4 * g;
-#pragma unroll
-        for (int j = 0; j < kND; ++j) {
-          const bf16x2 lo = {static_cast<__bf16>(o[u][j][0] * inv), static_cast<__bf16>(o[u][j][1] * inv)};
-          const bf16x2 hi = {static_cast<__bf16>(o[u][j][2] * inv), static_cast<__bf16>(o[u][j][3] * inv)};
-          *reinterpret_cast<u32x2*>(dst + 16 * j) =
-              u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
-        }
-      } else {
-        const long long at = ((long long)slot * p.Hk + hk) * p.RT + row0 + (wr * QT + u) * 16 + fr;
-        if (g == 0) *reinterpret_cast<f32x2*>(p.ml + 2 * at) = f32x2{m[u], l[u][0]};
-        if (nc == 0) continue;  // the statistics say that there is nothing
-#pragma unroll
-        for (int j = 0; j < kND; ++j) *reinterpret_cast<f32x4*>(p.po + at * D + 16 * j + 4 * g) = o[u][j];
-      }
-    }
+    for (int u = 0; u < QT; ++u) write_row<D>(p, w, row[u], g, m[u], l[u][0], o[u], nc > 0);
   }
 };
 
@@ -657,89 +603,146 @@ __device__ __forceinline__ void part_range(int n, int parts, int part, int unit,
 
 template <int D>
 using Wide = WideTile<D, 4, 2>;
-template <int D>
-using Thin = ThinTile<D, 1, 4, 1, 32>;
 
+constexpr int kMostPacked = 1024;  // sequences whose packed rows a workgroup looks up
+
+// Item `item` of a list: key heads innermost, so that neighbours in the list
+// (dealt round-robin over the XCDs) read different heads, and the tiles of one
+// head and part, which read the same keys, meet in one L2.
 template <class T>
 __device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, int item, int seq, int tiles,
                                          int parts, int own, int slot0) {
-  // key heads innermost: neighbours in the list read neighbouring heads of the same keys
-  const int hk = item % p.Hk;
+  TileWork w;
+  w.hk = item % p.Hk;
   const int rest = item / p.Hk;
   const int tile = rest % tiles, part = rest / tiles;
-  int row0, row_end;
-  int b = -1;
+  w.b = -1;
+  w.packed = !seq;
+  const int* cum = nullptr;
   if (seq) {
-    const int per = tiles / p.B;
-    b = tile / per;
-    row0 = b * p.RS + (tile - b * per) * T::kRows;
-    row_end = b * p.RS + (p.q_len ? min(max(p.q_len[b], 0), p.Tq) * p.G : p.RS);
-    if (row0 >= row_end) return;
+    const int per = tiles / p.B, b = tile / per, first = (tile - b * per) * T::kRows;
+    w.row0 = b * p.RS + first;
+    w.n = min(query_length(p, b) * p.G - first, T::kRows);
+    if (own != 0) w.b = b;
   } else {
-    row0 = tile * T::kRows;
-    row_end = p.RT;
+    int rows = p.RT;
+    if (p.q_len) {
+      // packed rows before each sequence: a running sum, 256 sequences at a time
+      int* c = reinterpret_cast<int*>(lds);
+      int* part_sum = c + kMostPacked + 1;
+      const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+      int carry = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 256) {
+        const int b = b0 + tid;
+        int n = tid < 256 && b < p.B ? query_length(p, b) * p.G : 0, x = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const int y = __shfl_up(x, d);
+          if (lane >= d) x += y;
+        }
+        if (lane == 63 && wave < 4) part_sum[wave] = x;
+        __syncthreads();
+        int before = carry;
+        for (int v = 0; v < 4; ++v) {
+          if (v < wave) before += part_sum[v];
+          carry += part_sum[v];
+        }
+        if (tid < 256 && b < p.B) c[b] = before + x - n;
+        __syncthreads();
+      }
+      if (tid == 0) c[p.B] = carry;
+      __syncthreads();
+      rows = carry;
+      cum = c;
+    }
+    w.row0 = tile * T::kRows;
+    w.n = min(rows - w.row0, T::kRows);
   }
-  int p0 = 0, p1 = 0, s0 = 0, s1 = 0;
+  if (w.n <= 0) return;
+  w.p0 = w.p1 = w.s0 = w.s1 = 0;
+  w.slot = slot0 + part;
   if (own == 0) {
-    part_range(p.P, parts, part, 64, p0, p1);
+    part_range(p.P, parts, part, 64, w.p0, w.p1);
   } else if (own == 1) {
-    part_range(p.S, parts, part, 64, s0, s1);
+    part_range(p.S, parts, part, 64, w.s0, w.s1);
   } else {
     // prefix (rounded up to whole chunks) and own keys as one list
     const int pp = (p.P + 63) & ~63;
     int lo, hi;
     part_range(pp + p.S, parts, part, 64, lo, hi);
-    p0 = min(lo, p.P);
-    p1 = min(hi, p.P);
-    s0 = max(lo - pp, 0);
-    s1 = max(hi - pp, 0);
+    w.p0 = min(lo, p.P);
+    w.p1 = min(hi, p.P);
+    w.s0 = max(lo - pp, 0);
+    w.s1 = max(hi - pp, 0);
   }
-  T::run(p, lds, hk, own == 0 ? -1 : b, row0, row_end, p0, p1, s0, s1, slot0 + part);
+  T::run(p, w, lds, cum);
 }
 
-// KIND: 1 wide items, 2 thin items, 3 both lists in one launch (the thin ones,
-// which wait for memory, beside the wide ones, which compute).
-template <int D, int KIND>
+// Both lists in one launch: the thin items, which wait for memory, run beside
+// the wide ones, which compute.
+template <int D>
 __global__ __launch_bounds__(256, 2) void prefix_attn_kernel(PaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int bid = blockIdx.x;
-  if (KIND == 1 || (KIND == 3 && bid < p.n_wide))
+  if (bid < p.n_wide)
     run_item<Wide<D>>(p, lds, bid, p.wide_seq, p.wide_tiles, p.wide_parts, p.wide_own, 0);
   else
-    run_item<Thin<D>>(p, lds, bid - p.n_wide, p.thin_seq, p.thin_tiles, p.thin_parts, p.thin_own, p.thin_slot);
+    run_item<ThinTile<D, 4>>(p, lds, bid - p.n_wide, p.thin_seq, p.thin_tiles, p.thin_parts, p.thin_own, p.thin_slot);
 }
 
-// Joins a row's partial results; D / 4 lanes a row.
+template <int D>
+__global__ __launch_bounds__(256, 2) void prefix_wide_kernel(PaParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  run_item<Wide<D>>(p, lds, blockIdx.x, p.wide_seq, p.wide_tiles, p.wide_parts, p.wide_own, 0);
+}
+
+template <int D>
+__global__ __launch_bounds__(512, 4) void prefix_thin_kernel(PaParams p) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  run_item<ThinTile<D, 8>>(p, lds, blockIdx.x, p.thin_seq, p.thin_tiles, p.thin_parts, p.thin_own, p.thin_slot);
+}
+
+// Joins a row's partial results, D / 4 lanes a row: four groups of slots side
+// by side (their loads in flight together), then the groups in order.
 template <int D>
 __global__ __launch_bounds__(256) void prefix_join_kernel(PaParams p) {
-  constexpr int LPR = D / 4;
-  const long long row = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;  // hk * RT + R
-  const int d = (threadIdx.x % LPR) * 4;
+  constexpr int LPR = D / 4, kGroups = 4, kRowsWg = 256 / (LPR * kGroups);
+  __shared__ f32x4 so[kGroups][kRowsWg][LPR];
+  __shared__ float sl[kGroups][kRowsWg];
+  const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR % kGroups, rw = threadIdx.x / (LPR * kGroups);
   const long long rows = (long long)p.Hk * p.RT;
-  if (row >= rows) return;
-  const int hk = (int)(row / p.RT);
-  const int R = (int)(row - (long long)hk * p.RT);
-  const int b = R / p.RS, rr = R - b * p.RS, t = rr / p.G;
-  if (p.q_len && t >= p.q_len[b]) return;
-  float m = -INFINITY;
-  for (int s = 0; s < p.slots; ++s) m = fmaxf(m, p.ml[2 * (s * rows + row)]);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  const long long row = min((long long)blockIdx.x * kRowsWg + rw, rows - 1);  // hk * RT + R
+  const int hk = (int)(row / p.RT), R = (int)(row - (long long)hk * p.RT);
+  const int b = (int)((unsigned)R / (unsigned)p.RS), rr = R - b * p.RS, t = (int)((unsigned)rr / (unsigned)p.G);
+  const bool used = (long long)blockIdx.x * kRowsWg + rw < rows && t < query_length(p, b);
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.slots; ++s) {
-    const f32x2 x = *reinterpret_cast<const f32x2*>(p.ml + 2 * (s * rows + row));
-    if (!(x[1] > 0.f)) continue;  // nothing there, O not written
-    const float w = __builtin_amdgcn_exp2f(x[0] - ref);
-    l += x[1] * w;
-    o += *reinterpret_cast<const f32x4*>(p.po + (s * rows + row) * D + d) * w;
+  float l = 0.f;
+  if (used) {
+    float m = -INFINITY;
+    for (int s = 0; s < p.slots; ++s) m = fmaxf(m, p.ml[2 * (s * rows + row)]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int s = grp; s < p.slots; s += kGroups) {
+      const f32x2 x = *reinterpret_cast<const f32x2*>(p.ml + 2 * (s * rows + row));
+      if (!(x[1] > 0.f)) continue;  // nothing there, O not written
+      const float wgt = __builtin_amdgcn_exp2f(x[0] - ref);
+      l = fmaf(x[1], wgt, l);
+      o += *reinterpret_cast<const f32x4*>(p.po + (s * rows + row) * D + 4 * lane) * wgt;
+    }
+  }
+  so[grp][rw][lane] = o;
+  if (lane == 0) sl[grp][rw] = l;
+  __syncthreads();
+  if (grp > 0 || !used) return;
+#pragma unroll
+  for (int v = 1; v < kGroups; ++v) {
+    o += so[v][rw][lane];
+    l += sl[v][rw];
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int h = hk * p.G + (rr - t * p.G);
   uint16_t* dst = static_cast<uint16_t*>(p.out.p) + (long long)b * p.out.b + (long long)t * p.out.t +
-                  (long long)h * p.out.h + d;
-  const bf16x2 lo = {static_cast<__bf16>(o[0] * inv), static_cast<__bf16>(o[1] * inv)};
-  const bf16x2 hi = {static_cast<__bf16>(o[2] * inv), static_cast<__bf16>(o[3] * inv)};
-  *reinterpret_cast<u32x2*>(dst) = u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+                  (long long)h * p.out.h + 4 * lane;
+  *reinterpret_cast<u32x2*>(dst) = u32x2{bf16_pair(o[0] * inv, o[1] * inv), bf16_pair(o[2] * inv, o[3] * inv)};
 }
 
 // How the rows and keys are dealt to workgroups: from the sizes alone, so
@@ -765,13 +768,14 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   Plan pl{};
   const int G = Hq / Hk;
   const long long RS = (long long)Tq * G, RT = (long long)B * RS;
-  const bool both = RS >= 64 || B == 1 || S == 0 || P == 0;
+  const bool both = RS >= 64 || B == 1 || S == 0 || P == 0 || B > kMostPacked;
   if (both) {
     // every tile stays in its sequence and takes prefix and own keys
     const bool thin = RS <= 16;
     const int rows = thin ? 16 : 128;
     const int tiles = B * cdiv(RS, rows);
-    const int parts = parts_for((long long)P + S, (long long)tiles * Hk, 512, 256);
+    const int parts = thin ? parts_for((long long)P + S, (long long)tiles * Hk, 256, 1024)
+                           : parts_for((long long)P + S, (long long)tiles * Hk, 512, 256);
     if (thin) {
       pl.thin_seq = 1, pl.thin_tiles = tiles, pl.thin_parts = parts, pl.thin_own = 2;
       pl.n_thin = (long long)tiles * Hk * parts;
@@ -800,17 +804,17 @@ size_t al256(size_t n) { return (n + 255) & ~(size_t)255; }
 template <int D>
 hipError_t run(const PaParams& p, const Plan& pl, hipStream_t st) {
   const dim3 grid((unsigned)(pl.n_wide + pl.n_thin));
-  constexpr int both = Wide<D>::kLds > Thin<D>::kLds ? Wide<D>::kLds : Thin<D>::kLds;
+  constexpr int wide = Wide<D>::kLds, thin4 = ThinTile<D, 4>::kLds, thin8 = ThinTile<D, 8>::kLds;
   if (pl.n_thin == 0)
-    hipLaunchKernelGGL((prefix_attn_kernel<D, 1>), grid, dim3(256), Wide<D>::kLds, st, p);
+    hipLaunchKernelGGL((prefix_wide_kernel<D>), grid, dim3(256), wide, st, p);
   else if (pl.n_wide == 0)
-    hipLaunchKernelGGL((prefix_attn_kernel<D, 2>), grid, dim3(256), Thin<D>::kLds, st, p);
+    hipLaunchKernelGGL((prefix_thin_kernel<D>), grid, dim3(512), thin8, st, p);
   else
-    hipLaunchKernelGGL((prefix_attn_kernel<D, 3>), grid, dim3(256), both, st, p);
+    hipLaunchKernelGGL((prefix_attn_kernel<D>), grid, dim3(256), wide > thin4 ? wide : thin4, st, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slots == 1) return e;
   const long long rows = (long long)p.Hk * p.RT;
-  hipLaunchKernelGGL((prefix_join_kernel<D>), dim3((unsigned)cdiv(rows, 1024 / D)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((prefix_join_kernel<D>), dim3((unsigned)cdiv(rows, 256 / D)), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
