@@ -83,7 +83,7 @@ def load():
     lib.gkd_kg_transformer_noalloc.restype = _I
     lib.gkd_kg_transformer_noalloc.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I,
                                                _I, _I, _U32, _P, _P]
-    _L, _Z, _H = ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(GkdHeads)
+    _L, _Z, _H = ctypes.c_int64, ctypes.c_size_t, _P  # _H: gkd_heads *
     lib.gkd_tokens_version.restype = _I
     lib.gkd_linear_workspace_size.restype = _Z
     lib.gkd_linear_workspace_size.argtypes = [_I, _I, _I, _L, _L]
@@ -389,58 +389,75 @@ def kg_transformer(query: torch.Tensor, weights: torch.Tensor, kern_vis=None, ma
     return out
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _on_current(dev):
-    # kernels are launched on the current device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-
-
-def _heads(t, name, dtype=None, ndim=4):
-    """A [B,T,H,D] (ndim 3: [T,H,D]) operand with any strides but adjacent
-    head elements, as gkd_heads."""
+def _place(t, name):
+    """Device index of a GPU tensor, which must be the current device (where
+    kernels are launched)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if dtype is not None and t.dtype != dtype:
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
+                         f"cuda:{_current_device()}")
+    return dev
+
+
+def _beside(dev, t, name):
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _heads(dev, t, name, dtype, ndim=4):
+    """A [B,T,H,D] (ndim 3: [T,H,D]) operand with any strides but adjacent
+    head elements, as the four fields of gkd_heads."""
+    _beside(dev, t, name)
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     st = t.stride()
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a head must be adjacent")
-    return GkdHeads(t.data_ptr(), st[0] if ndim == 4 else 0, st[-3], st[-2])
+    if ndim == 4:
+        return t.data_ptr(), st[0], st[1], st[2]
+    return t.data_ptr(), 0, st[0], st[1]
+
+
+_NO_HEADS = (0, 0, 0, 0)
+_Heads4, _Heads6 = ctypes.c_int64 * 16, ctypes.c_int64 * 24  # four, six gkd_heads
+_HEADS_BYTES = ctypes.sizeof(GkdHeads)
 
 
 def _workspace(workspace, need, dev):
     if need == 0:
         return None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
     _dev(workspace, "workspace", torch.uint8, 1)
-    _same_device(dev, workspace=workspace)
+    _beside(dev, workspace, "workspace")
     return workspace, workspace.numel()
 
 
 def _row_stride(t, name):
     """Row stride of a [..., n] tensor whose rows are evenly spaced."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, st = t.shape, t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
+    if len(shape) == 2:
+        return st[0] if shape[0] != 1 else shape[1]
     ld, span = None, 1
-    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, step in zip(reversed(shape[:-1]), reversed(st[:-1])):
         if size == 1:
             continue
         if ld is None:
-            ld = st
-        elif st != ld * span:
+            ld = step
+        elif step != ld * span:
             raise ValueError(f"{name}: its rows must be evenly spaced")
         span *= size
-    return t.shape[-1] if ld is None else ld
+    return shape[-1] if ld is None else ld
 
 
 def linear_workspace_size(M: int, N: int, K: int, ldx: int | None = None,
@@ -459,43 +476,54 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
     `residual` itself. workspace: a uint8 GPU tensor of at least
     linear_workspace_size() bytes (allocated here when None)."""
     lib = _lib or load()
-    if not (x.is_cuda and weight.is_cuda):
-        raise ValueError("x and weight must be GPU tensors")
-    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+    dev = _place(x, "x")
+    _beside(dev, weight, "weight")
+    bf16 = torch.bfloat16
+    if x.dtype != bf16 or weight.dtype != bf16:
         raise TypeError(f"x and weight must be bfloat16, got {x.dtype} and {weight.dtype}")
-    if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
-        raise ValueError(f"x must be [..., K] and weight [N, K], got {tuple(x.shape)} and "
-                         f"{tuple(weight.shape)}")
-    if act not in GKD_ACTS:
+    lead, wshape = x.shape, weight.shape
+    if len(lead) < 1 or len(wshape) != 2 or lead[-1] != wshape[1]:
+        raise ValueError(f"x must be [..., K] and weight [N, K], got {tuple(lead)} and "
+                         f"{tuple(wshape)}")
+    code = GKD_ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(GKD_ACTS)}")
-    N, K = weight.shape
-    shape = (*x.shape[:-1], N)
-    M = x.numel() // K if K else 0
+    N, K = wshape
+    lead = lead[:-1]
+    M = lead.numel()
+    shape = lead + (N,)
     if out_dtype is None:
         out_dtype = (out.dtype if out is not None else
-                     residual.dtype if residual is not None else torch.bfloat16)
-    if out_dtype not in (torch.bfloat16, torch.float32):
+                     residual.dtype if residual is not None else bf16)
+    if out_dtype != bf16 and out_dtype != torch.float32:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     if out is None:
         out = torch.empty(shape, dtype=out_dtype, device=x.device)
-    dev = x.device
-    _on_current(dev)
-    _same_device(dev, weight=weight, bias=bias, residual=residual, out=out)
-    if out.shape != shape or out.dtype != out_dtype:
-        raise ValueError(f"out must be {shape} of {out_dtype}")
-    if residual is not None and (residual.shape != shape or residual.dtype != out_dtype):
-        raise ValueError(f"residual must be {shape} of {out_dtype}")
-    if bias is not None and (bias.shape != (N,) or bias.dtype != torch.bfloat16 or
-                             not bias.is_contiguous()):
-        raise ValueError("bias must be [N] bfloat16, contiguous")
-    ldx, ldw, ldo = _row_stride(x, "x"), _row_stride(weight, "weight"), _row_stride(out, "out")
-    ldr = _row_stride(residual, "residual") if residual is not None else 0
-    ws, ws_bytes = None, 0
-    if K % 8 or ldx % 8 or ldw % 8:
-        ws, ws_bytes = _workspace(workspace, lib.gkd_linear_workspace_size(M, N, K, ldx, ldw), dev)
-    _check(lib.gkd_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, _ptr(bias), _ptr(residual),
-                          ldr, M, N, K, GKD_ACTS[act], 1, 1 if out_dtype == torch.bfloat16 else 0,
-                          0, out.data_ptr(), ldo, _ptr(ws), ws_bytes, _stream(dev)))
+        ldo = N
+    else:
+        _beside(dev, out, "out")
+        if out.shape != shape or out.dtype != out_dtype:
+            raise ValueError(f"out must be {tuple(shape)} of {out_dtype}")
+        ldo = _row_stride(out, "out")
+    rp = bp = None
+    ldr = 0
+    if residual is not None:
+        _beside(dev, residual, "residual")
+        if residual.shape != shape or residual.dtype != out_dtype:
+            raise ValueError(f"residual must be {tuple(shape)} of {out_dtype}")
+        rp, ldr = residual.data_ptr(), _row_stride(residual, "residual")
+    if bias is not None:
+        _beside(dev, bias, "bias")
+        if bias.shape != (N,) or bias.dtype != bf16 or not bias.is_contiguous():
+            raise ValueError("bias must be [N] bfloat16, contiguous")
+        bp = bias.data_ptr()
+    ldx, ldw = _row_stride(x, "x"), _row_stride(weight, "weight")
+    ws, ws_bytes = _workspace(workspace, lib.gkd_linear_workspace_size(M, N, K, ldx, ldw), dev)
+    status = lib.gkd_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, bp, rp, ldr, M, N, K, code,
+                            1, 1 if out_dtype == bf16 else 0, 0, out.data_ptr(), ldo,
+                            None if ws is None else ws.data_ptr(), ws_bytes, _raw_stream(dev))
+    if status:
+        _check(status)
     return out
 
 
@@ -509,14 +537,13 @@ def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_w
     None (no norm). Returns (q_out, k_out), new and dense unless given; an
     output may be its input (in place)."""
     lib = _lib or load()
-    dev, dtype = q.device, q.dtype
+    dev, dtype = _place(q, "q"), q.dtype
     code = _dtype_code(q)
-    hq = _heads(q, "q")
+    hq = _heads(dev, q, "q", dtype)
     B, T, Hq, D = q.shape
-    Hk = 0
-    hk = hko = None
+    Hk, hk, hko = 0, _NO_HEADS, _NO_HEADS
     if k is not None:
-        hk = _heads(k, "k", dtype)
+        hk = _heads(dev, k, "k", dtype)
         Hk = k.shape[2]
         if k.shape != (B, T, Hk, D) or Hk < 1:
             raise ValueError(f"k must be [B,T,Hk,D], got {tuple(k.shape)}")
@@ -524,33 +551,38 @@ def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_w
         raise ValueError("k_out without k")
     _dev(pos, "pos", torch.float32)
     _dev(freqs, "freqs", torch.float32, 2)
+    _beside(dev, pos, "pos")
+    _beside(dev, freqs, "freqs")
     A, half = freqs.shape
-    if tuple(pos.shape) not in ((T, A), (B, T, A)):
+    if pos.shape != (B, T, A) and pos.shape != (T, A):
         raise ValueError(f"pos must be [T,n_axes] or [B,T,n_axes], got {tuple(pos.shape)}")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _dev(w, name, dtype, 1)
+            _beside(dev, w, name)
             if w.shape[0] != D:
                 raise ValueError(f"{name} must be [D]")
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, D), dtype=dtype, device=dev)
-    hqo = _heads(q_out, "q_out", dtype)
+        q_out = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device)
+    hqo = _heads(dev, q_out, "q_out", dtype)
     if q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((B, T, Hk, D), dtype=dtype, device=dev)
-        hko = _heads(k_out, "k_out", dtype)
+            k_out = torch.empty((B, T, Hk, D), dtype=dtype, device=q.device)
+        hko = _heads(dev, k_out, "k_out", dtype)
         if k_out.shape != k.shape:
             raise ValueError("k_out must have k's shape")
-    _on_current(dev)
-    _same_device(dev, k=k, pos=pos, freqs=freqs, q_weight=q_weight, k_weight=k_weight, q_out=q_out,
-                 k_out=k_out)
-    _check(lib.gkd_qk_norm_rope(hq, Hq, hk, Hk, B, T, D, pos.data_ptr(),
-                                T * A if pos.dim() == 3 else 0, A, freqs.data_ptr(), 2 * half,
-                                _ptr(q_weight), _ptr(k_weight), eps, code,
-                                GKD_ROPE_INTERLEAVED if interleaved else 0, hqo, hko,
-                                _stream(dev)))
+    heads = _Heads4(*hq, *hk, *hqo, *hko)
+    at = ctypes.addressof(heads)
+    status = lib.gkd_qk_norm_rope(at, Hq, at + _HEADS_BYTES if Hk else None, Hk, B, T, D,
+                                  pos.data_ptr(), T * A if pos.dim() == 3 else 0, A,
+                                  freqs.data_ptr(), 2 * half, _ptr(q_weight), _ptr(k_weight), eps,
+                                  code, GKD_ROPE_INTERLEAVED if interleaved else 0,
+                                  at + 2 * _HEADS_BYTES, at + 3 * _HEADS_BYTES if Hk else None,
+                                  _raw_stream(dev))
+    if status:
+        _check(status)
     return q_out, k_out
 
 
@@ -573,49 +605,55 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
     without keys gives zeros."""
     lib = _lib or load()
     bf16 = torch.bfloat16
-    hq = _heads(q, "q", bf16)
+    dev = _place(q, "q")
+    hq = _heads(dev, q, "q", bf16)
     B, Tq, Hq, D = q.shape
-    dev = q.device
     if (k_prefix is None) != (v_prefix is None) or (k_own is None) != (v_own is None):
         raise ValueError("keys and values go together")
     P = S = 0
     Hk = None
-    kp = vp = ko = vo = None
+    kp = vp = ko = vo = _NO_HEADS
     if k_prefix is not None:
-        kp, vp = _heads(k_prefix, "k_prefix", bf16, 3), _heads(v_prefix, "v_prefix", bf16, 3)
-        P, Hk = k_prefix.shape[:2]
-        if k_prefix.shape[2] != D or v_prefix.shape != k_prefix.shape:
+        kp = _heads(dev, k_prefix, "k_prefix", bf16, 3)
+        vp = _heads(dev, v_prefix, "v_prefix", bf16, 3)
+        P, Hk, d = k_prefix.shape
+        if d != D or v_prefix.shape != k_prefix.shape:
             raise ValueError("k_prefix and v_prefix must be [P,Hk,D]")
     if k_own is not None:
-        ko, vo = _heads(k_own, "k_own", bf16), _heads(v_own, "v_own", bf16)
-        S = k_own.shape[1]
-        Hk = k_own.shape[2] if Hk is None else Hk
-        if k_own.shape != (B, S, Hk, D) or v_own.shape != k_own.shape:
+        ko, vo = _heads(dev, k_own, "k_own", bf16), _heads(dev, v_own, "v_own", bf16)
+        b, S, h, d = k_own.shape
+        Hk = h if Hk is None else Hk
+        if b != B or h != Hk or d != D or v_own.shape != k_own.shape:
             raise ValueError("k_own and v_own must be [B,S,Hk,D]")
     if Hk is None:
         raise ValueError("give prefix keys, own keys or both")
     for t, name in ((own_len, "own_len"), (q_len, "q_len")):
         if t is not None:
             _dev(t, name, torch.int32, 1)
+            _beside(dev, t, name)
             if t.shape[0] != B:
                 raise ValueError(f"{name} must be [B]")
     if own_mask is not None:
         _dev(own_mask, "own_mask", torch.uint8, 2)
+        _beside(dev, own_mask, "own_mask")
         if own_mask.shape != (B, S):
             raise ValueError("own_mask must be [B,S]")
     if out is None:
-        out = torch.empty((B, Tq, Hq, D), dtype=bf16, device=dev)
-    ho = _heads(out, "out", bf16)
+        out = torch.empty((B, Tq, Hq, D), dtype=bf16, device=q.device)
+    ho = _heads(dev, out, "out", bf16)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _on_current(dev)
-    _same_device(dev, k_prefix=k_prefix, v_prefix=v_prefix, k_own=k_own, v_own=v_own,
-                 own_len=own_len, q_len=q_len, own_mask=own_mask, out=out)
     ws, ws_bytes = _workspace(workspace, lib.gkd_prefix_attention_workspace_size(
         B, Tq, Hq, Hk, D, P, S), dev)
-    _check(lib.gkd_prefix_attention(hq, kp, vp, P, ko, vo, S, _ptr(own_len), _ptr(q_len),
-                                    _ptr(own_mask), B, Tq, Hq, Hk, D,
-                                    D ** -0.5 if scale is None else float(scale), 1,
-                                    GKD_ATTN_CAUSAL if causal else 0, ho, _ptr(ws), ws_bytes,
-                                    _stream(dev)))
+    heads = _Heads6(*hq, *kp, *vp, *ko, *vo, *ho)
+    at = ctypes.addressof(heads)
+    n = _HEADS_BYTES
+    status = lib.gkd_prefix_attention(at, at + n, at + 2 * n, P, at + 3 * n, at + 4 * n, S,
+                                      _ptr(own_len), _ptr(q_len), _ptr(own_mask), B, Tq, Hq, Hk, D,
+                                      D ** -0.5 if scale is None else scale, 1,
+                                      GKD_ATTN_CAUSAL if causal else 0, at + 5 * n,
+                                      None if ws is None else ws.data_ptr(), ws_bytes,
+                                      _raw_stream(dev))
+    if status:
+        _check(status)
     return out

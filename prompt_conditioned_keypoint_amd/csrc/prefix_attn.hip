@@ -28,6 +28,17 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) void lds_void;
 
+// A list of work items, [part of the keys][tile of rows][key head].
+struct List {
+  int wide;    // its tiles are wide ones, else thin ones
+  int seq;     // they stay within a sequence, else the rows of all sequences are packed
+  int keys;    // 0: the prefix, 1: own keys, 2: both, prefix first
+  int tiles;   // tiles of rows per key head
+  int parts;
+  int slot;    // the first part's slot among a row's partial results
+  int n;       // items
+};
+
 struct PaParams {
   Heads q, kp, vp, ko, vo, out;
   int P, S;
@@ -37,14 +48,8 @@ struct PaParams {
   int RS, RT;          // rows of a sequence, of all sequences (per key head)
   float c;             // scale * log2(e)
   int causal;
-  // the plan: wide items first, then thin ones; an item list is [part][tile][key head]
-  int wide_seq, thin_seq;      // its tiles stay within a sequence
-  int wide_tiles, thin_tiles;  // tiles of rows per key head
-  int wide_parts, thin_parts;
-  int wide_own, thin_own;      // 0: prefix keys, 1: own keys, 2: both, prefix first
-  int n_wide;                  // workgroups of the wide list
-  int slots;                   // partial results a row has; 1: written as they are
-  int thin_slot;               // first slot of the thin list
+  List first, second;  // the plan: the workgroups of both lists, one after the other
+  int slots;           // partial results a row has; 1: written as they are
   float* po;                   // [slots][Hk][RT][D]
   float* ml;                   // [slots][Hk][RT][2]
 };
@@ -610,20 +615,20 @@ constexpr int kMostPacked = 1024;  // sequences whose packed rows a workgroup lo
 // (dealt round-robin over the XCDs) read different heads, and the tiles of one
 // head and part, which read the same keys, meet in one L2.
 template <class T>
-__device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, int item, int seq, int tiles,
-                                         int parts, int own, int slot0) {
+__device__ __forceinline__ void run_item(const PaParams& p, const List& list, unsigned char* lds, int item) {
+  const int tiles = list.tiles, parts = list.parts;
   TileWork w;
   w.hk = item % p.Hk;
   const int rest = item / p.Hk;
   const int tile = rest % tiles, part = rest / tiles;
   w.b = -1;
-  w.packed = !seq;
+  w.packed = !list.seq;
   const int* cum = nullptr;
-  if (seq) {
+  if (list.seq) {
     const int per = tiles / p.B, b = tile / per, first = (tile - b * per) * T::kRows;
     w.row0 = b * p.RS + first;
     w.n = min(query_length(p, b) * p.G - first, T::kRows);
-    if (own != 0) w.b = b;
+    if (list.keys != 0) w.b = b;
   } else {
     int rows = p.RT;
     if (p.q_len) {
@@ -660,10 +665,10 @@ __device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, 
   }
   if (w.n <= 0) return;
   w.p0 = w.p1 = w.s0 = w.s1 = 0;
-  w.slot = slot0 + part;
-  if (own == 0) {
+  w.slot = list.slot + part;
+  if (list.keys == 0) {
     part_range(p.P, parts, part, 64, w.p0, w.p1);
-  } else if (own == 1) {
+  } else if (list.keys == 1) {
     part_range(p.S, parts, part, 64, w.s0, w.s1);
   } else {
     // prefix (rounded up to whole chunks) and own keys as one list
@@ -678,28 +683,28 @@ __device__ __forceinline__ void run_item(const PaParams& p, unsigned char* lds, 
   T::run(p, w, lds, cum);
 }
 
-// Both lists in one launch: the thin items, which wait for memory, run beside
-// the wide ones, which compute.
+// Both lists in one launch: thin items, which wait for memory, run beside wide
+// ones, which compute, and short ones fill in behind long ones.
 template <int D>
-__global__ __launch_bounds__(256, 2) void prefix_attn_kernel(PaParams p) {
+__global__ __launch_bounds__(256, 2) void prefix_mixed_kernel(PaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int bid = blockIdx.x;
-  if (bid < p.n_wide)
-    run_item<Wide<D>>(p, lds, bid, p.wide_seq, p.wide_tiles, p.wide_parts, p.wide_own, 0);
-  else
-    run_item<ThinTile<D, 4>>(p, lds, bid - p.n_wide, p.thin_seq, p.thin_tiles, p.thin_parts, p.thin_own, p.thin_slot);
+  if (bid < p.first.n) run_item<Wide<D>>(p, p.first, lds, bid);
+  else run_item<ThinTile<D, 4>>(p, p.second, lds, bid - p.first.n);
 }
 
 template <int D>
 __global__ __launch_bounds__(256, 2) void prefix_wide_kernel(PaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  run_item<Wide<D>>(p, lds, blockIdx.x, p.wide_seq, p.wide_tiles, p.wide_parts, p.wide_own, 0);
+  const int bid = blockIdx.x;
+  const bool second = bid >= p.first.n;
+  run_item<Wide<D>>(p, second ? p.second : p.first, lds, second ? bid - p.first.n : bid);
 }
 
 template <int D>
 __global__ __launch_bounds__(512, 4) void prefix_thin_kernel(PaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  run_item<ThinTile<D, 8>>(p, lds, blockIdx.x, p.thin_seq, p.thin_tiles, p.thin_parts, p.thin_own, p.thin_slot);
+  run_item<ThinTile<D, 8>>(p, p.first, lds, blockIdx.x);
 }
 
 // Joins a row's partial results, D / 4 lanes a row: four groups of slots side
@@ -748,10 +753,8 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PaParams p) {
 // How the rows and keys are dealt to workgroups: from the sizes alone, so
 // the workspace's size follows from them too.
 struct Plan {
-  int wide_seq, wide_tiles, wide_parts, wide_own;
-  int thin_seq, thin_tiles, thin_parts, thin_own;
-  int slots, thin_slot;
-  long long n_wide, n_thin;
+  List first, second;
+  int slots;
 };
 
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -768,34 +771,37 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   Plan pl{};
   const int G = Hq / Hk;
   const long long RS = (long long)Tq * G, RT = (long long)B * RS;
-  const bool both = RS >= 64 || B == 1 || S == 0 || P == 0 || B > kMostPacked;
-  if (both) {
+  auto list = [&](int wide, int seq, int keys, int tiles, int parts, int slot) {
+    return List{wide, seq, keys, tiles, parts, slot, (int)((long long)tiles * Hk * parts)};
+  };
+  // Packing the rows of all sequences reads the prefix once for 128 of them
+  // and costs a second list of items, partial results and a join. Measured
+  // (us, packed / in sequence): 64 x 1 rows of 16 heads of 64 behind 4096 keys
+  // 21 / 77, behind 256 keys 20 / 16; 64 x 48 rows of 8 heads of 128 behind
+  // 4096 keys 100 / 122, behind 1024 keys 52 / 36; two sequences behind 16384
+  // keys 29 / 21; 37 x 80 rows behind 2304 keys with 80 own ones 63 / 71, but
+  // 16 x 96 rows behind 8192 with 512 own ones 98 / 80. Tiles of 128 rows or
+  // more are full as they are.
+  const bool packed = B >= 4 && B <= kMostPacked && S > 0 && RS < 128 && P >= (RS <= 16 ? 1024 : 2048) &&
+                      (RS < 64 || P / 24 >= S);
+  if (!packed) {
     // every tile stays in its sequence and takes prefix and own keys
-    const bool thin = RS <= 16;
-    const int rows = thin ? 16 : 128;
-    const int tiles = B * cdiv(RS, rows);
-    const int parts = thin ? parts_for((long long)P + S, (long long)tiles * Hk, 256, 1024)
-                           : parts_for((long long)P + S, (long long)tiles * Hk, 512, 256);
-    if (thin) {
-      pl.thin_seq = 1, pl.thin_tiles = tiles, pl.thin_parts = parts, pl.thin_own = 2;
-      pl.n_thin = (long long)tiles * Hk * parts;
-    } else {
-      pl.wide_seq = 1, pl.wide_tiles = tiles, pl.wide_parts = parts, pl.wide_own = 2;
-      pl.n_wide = (long long)tiles * Hk * parts;
-    }
+    const int wide = RS > 16, tiles = B * cdiv(RS, wide ? 128 : 16);
+    const int parts = wide ? parts_for((long long)P + S, (long long)tiles * Hk, 512, 256)
+                           : parts_for((long long)P + S, (long long)tiles * Hk, 256, 1024);
+    pl.first = list(wide, 1, 2, tiles, parts, 0);
     pl.slots = parts;
     return pl;
   }
   // the prefix for the rows of all sequences together, own keys apart
-  pl.wide_tiles = cdiv(RT, 128);
-  pl.wide_parts = parts_for(P, (long long)pl.wide_tiles * Hk, 256, 256);
-  pl.n_wide = (long long)pl.wide_tiles * Hk * pl.wide_parts;
-  pl.thin_seq = 1, pl.thin_own = 1;
-  pl.thin_tiles = B * cdiv(RS, 16);
-  pl.thin_parts = parts_for(S, (long long)pl.thin_tiles * Hk, 256, 256);
-  pl.n_thin = (long long)pl.thin_tiles * Hk * pl.thin_parts;
-  pl.thin_slot = pl.wide_parts;
-  pl.slots = pl.wide_parts + pl.thin_parts;
+  // (beside thin items 256 wide ones, one a CU: with 512 the 48 sequences
+  // behind 32768 keys take 102 instead of 89 us; beside wide ones 512)
+  const int wide = RS > 16, tiles = cdiv(RT, 128);
+  const int parts = parts_for(P, (long long)tiles * Hk, wide ? 512 : 256, 256);
+  pl.first = list(1, 0, 0, tiles, parts, 0);
+  const int own_tiles = B * cdiv(RS, wide ? 128 : 16);
+  pl.second = list(wide, 1, 1, own_tiles, parts_for(S, (long long)own_tiles * Hk, 256, 256), parts);
+  pl.slots = parts + pl.second.parts;
   return pl;
 }
 
@@ -803,14 +809,14 @@ size_t al256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 template <int D>
 hipError_t run(const PaParams& p, const Plan& pl, hipStream_t st) {
-  const dim3 grid((unsigned)(pl.n_wide + pl.n_thin));
+  const dim3 grid((unsigned)(pl.first.n + pl.second.n));
   constexpr int wide = Wide<D>::kLds, thin4 = ThinTile<D, 4>::kLds, thin8 = ThinTile<D, 8>::kLds;
-  if (pl.n_thin == 0)
-    hipLaunchKernelGGL((prefix_wide_kernel<D>), grid, dim3(256), wide, st, p);
-  else if (pl.n_wide == 0)
+  if (!pl.first.wide)
     hipLaunchKernelGGL((prefix_thin_kernel<D>), grid, dim3(512), thin8, st, p);
+  else if (pl.second.n == 0 || pl.second.wide)
+    hipLaunchKernelGGL((prefix_wide_kernel<D>), grid, dim3(256), wide, st, p);
   else
-    hipLaunchKernelGGL((prefix_attn_kernel<D>), grid, dim3(256), wide > thin4 ? wide : thin4, st, p);
+    hipLaunchKernelGGL((prefix_mixed_kernel<D>), grid, dim3(256), wide > thin4 ? wide : thin4, st, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slots == 1) return e;
   const long long rows = (long long)p.Hk * p.RT;
@@ -849,17 +855,9 @@ hipError_t launch_prefix_attn(const PrefixAttnArgs& a, hipStream_t st) {
   p.RT = a.B * p.RS;
   p.c = a.scale * 1.4426950408889634f;
   p.causal = a.causal;
-  p.wide_seq = pl.wide_seq;
-  p.thin_seq = pl.thin_seq;
-  p.wide_tiles = pl.wide_tiles;
-  p.thin_tiles = pl.thin_tiles;
-  p.wide_parts = pl.wide_parts;
-  p.thin_parts = pl.thin_parts;
-  p.wide_own = pl.wide_own;
-  p.thin_own = pl.thin_own;
-  p.n_wide = (int)pl.n_wide;
+  p.first = pl.first;
+  p.second = pl.second;
   p.slots = pl.slots;
-  p.thin_slot = pl.thin_slot;
   if (pl.slots > 1) {
     const size_t rows = (size_t)pl.slots * a.B * a.Tq * a.Hq;
     p.po = static_cast<float*>(a.ws);
