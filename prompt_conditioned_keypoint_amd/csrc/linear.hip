@@ -1,9 +1,11 @@
 // linear.hip - matrix product with bias, activation and residual in its
 // epilogue (gkd_linear): out = act(x w^T + bias) + residual.
 //
-// Two kernels, chosen by the row count:
-//   linear_tile_kernel   a tile of rows x columns a workgroup, both operands
-//                        through LDS: bound by the matrix pipes;
+// Three kernels, chosen by the sizes:
+//   linear_turn_kernel   256 x 256 tiles, both operands through LDS, waves that
+//                        take turns on the matrix pipe: bound by it;
+//   linear_ring_kernel   smaller tiles with a ring of stages in LDS, where there
+//                        are too few large ones: bound by the loads' latency;
 //   linear_few_kernel    up to 64 rows: 16 columns a workgroup, whose waves
 //                        share the K axis, operands straight to registers:
 //                        bound by reading w once.
@@ -29,7 +31,6 @@ struct LinParams {
   int M, N, K;         // K a multiple of 8
   int act;
   int out_f32;
-  int vec;             // finish() may move whole pieces
 };
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -97,6 +98,11 @@ __device__ __forceinline__ void load_bias(const LinParams& p, int n, float (&b)[
   for (int e = 0; e < W; ++e) b[e] = p.bias && n + e < p.N ? bf16_bits_to_f32(p.bias[n + e]) : 0.f;
 }
 
+// Rows may start anywhere: pieces are moved with their elements' alignment
+// (the hardware takes such accesses; aligned ones cost the same as before).
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
 // The residual and the store of W columns in whole pieces, at elements o
 // (out) and r (residual).
 template <int W>
@@ -105,11 +111,11 @@ __device__ __forceinline__ void finish_pieces(const LinParams& p, long long o, l
 #pragma unroll
     for (int q = 0; q < W / 4; ++q) {
       f32x4 t = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-      if (p.res) t += *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.res) + r + 4 * q);
-      *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o + 4 * q) = t;
+      if (p.res) t += *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p.res) + r + 4 * q);
+      *reinterpret_cast<f32x4_any*>(static_cast<float*>(p.out) + o + 4 * q) = t;
     }
   } else {
-    typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+    typedef uint32_t words __attribute__((ext_vector_type(W / 2), aligned(2)));
     if (p.res) {
       const words q = *reinterpret_cast<const words*>(static_cast<const uint16_t*>(p.res) + r);
 #pragma unroll
@@ -126,16 +132,14 @@ __device__ __forceinline__ void finish_pieces(const LinParams& p, long long o, l
 }
 
 // Bias, activation, residual and the store of the W (4 or 8) columns from n
-// of row m < M; columns past N are left out. Whole pieces where the rows
-// allow it (p.vec: W adjacent columns are aligned in out and residual), else
-// one by one.
+// of row m < M: whole pieces, and one by one where the matrix ends.
 template <int ACT, int W>
 __device__ __forceinline__ void finish(const LinParams& p, int m, int n, float (&v)[W], const float (&b)[W]) {
   if (n >= p.N) return;
   const long long o = (long long)m * p.ldo + n, r = (long long)m * p.ldr + n;
 #pragma unroll
   for (int e = 0; e < W; ++e) v[e] = activate<ACT>(v[e] + b[e]);
-  if (n + W <= p.N && p.vec) {
+  if (n + W <= p.N) {
     finish_pieces<W>(p, o, r, v);
     return;
   }
@@ -152,108 +156,168 @@ __device__ __forceinline__ void finish(const LinParams& p, int m, int n, float (
   }
 }
 
-// ---------------------------------------------------------------------------
-// Tiles of BM x BN, K in steps of 64 through a ring of two LDS stages, WM x
-// WN waves of (BM / WM) x (BN / WN). Both tiles stream straight into LDS
-// (16 bytes a lane); 16-byte piece c of tile row r sits at place c ^ (r & 7),
-// so the 16 rows of one operand read fall in different banks. Rows past M
-// or N repeat the last one and are not stored; pieces past K repeat the
-// row's last and enter the product as zeros.
-// ---------------------------------------------------------------------------
 constexpr int kBK = 64;
 
-template <int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinParams p) {
-  constexpr int NW = WM * WN;                  // waves
-  constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
-  constexpr int NA = BM * 8 / (64 * NW), NB = BN * 8 / (64 * NW);  // loads a wave and step
-  constexpr int A_BYTES = BM * kBK * 2, STAGE = (BM + BN) * kBK * 2;
+template <int N>
+__device__ __forceinline__ void wait_vm_here() {
+  asm volatile("" ::: "memory");
+  wait_vm<N>();
+  asm volatile("" ::: "memory");
+}
+
+// s_waitcnt lgkmcnt(0), the other counters left alone
+__device__ __forceinline__ void wait_lds_here() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
+}
+
+// Rows `row` .. rows - 1 of a matrix as a buffer: rows past the last one are
+// past its end and come out as zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const uint16_t* base, int row, int rows, int ld) {
+  const long long bytes = (long long)(rows - row) * ld * 2;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (long long)row * ld), 0,
+                                           (int)(uint32_t)min(bytes, 0xffffffffLL), 0x00020000);
+}
+
+// This workgroup's place in the order of the tiles: workgroups are dealt
+// round-robin over the XCDs, and each XCD takes a contiguous run.
+__device__ __forceinline__ int xcd_run(int total) {
+  const int xcd = blockIdx.x % kXcds, rem = total % kXcds;
+  return xcd * (total / kXcds) + min(xcd, rem) + blockIdx.x / kXcds;
+}
+
+// ---------------------------------------------------------------------------
+// Tiles of BM x BN for products too small to fill the card with 256 x 256
+// ones: WM x WN waves of (BM / WM) x 32, times WK groups of such waves that
+// take every WK-th 64-wide step of K and join at the end, through a ring of
+// NS stages in LDS. What bounds these is how long a step's loads take, so
+// NS - 1 stages are always under way. Places of the pieces in LDS and the
+// lanes' columns are those of the 256 x 256 kernel below.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WM, int WN, int WK, int NS>
+__global__ __launch_bounds__(64 * WM * WN * WK) void linear_ring_kernel(LinParams p) {
+  constexpr int GW = WM * WN;                               // waves of a group
+  constexpr int MT = BM / WM / 16, PT = BN / WN / 32;       // row tiles and column pairs of a wave
+  constexpr int NA = BM / 8 / GW, NB = BN / 8 / GW;         // loads a wave and step
+  constexpr int A_BYTES = BM * kBK * 2, STEP = (BM + BN) * kBK * 2, STAGE = WK * STEP;
+  static_assert(NA >= 1 && NB >= 1 && GW % 2 == 0 && (NS - 2) * (NA + NB) < 64, "ring shape");
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tiles_n = (p.N + BN - 1) / BN;
-  const int total = gridDim.x;
-  // Workgroups are dealt round-robin over the XCDs: each takes a contiguous
-  // run of the tiles, so the column tiles of one row band share an L2.
-  const int bid = blockIdx.x, xcd = bid % kXcds, q = total / kXcds, rem = total % kXcds;
-  const int lin = xcd * q + min(xcd, rem) + bid / kXcds;
-  const int m0 = (lin / tiles_n) * BM, n0 = (lin % tiles_n) * BN;
-  const uint16_t* xb = p.x + (long long)m0 * p.ldx;
-  const uint16_t* wb = p.w + (long long)n0 * p.ldw;
+  const int gw = wave % GW, kg = wave / GW;
+  const int fr = lane & 15, g = lane >> 4, lr = lane >> 3;
+  const int tiles_n = (p.N + BN - 1) / BN, tiles_m = (p.M + BM - 1) / BM;
+  const int l = xcd_run(gridDim.x), per = 8 * tiles_n;      // bands of 8 rows of tiles
+  const int band = l / per, rr = l - band * per, rows = min(8, tiles_m - band * 8);
+  const int m0 = (band * 8 + rr % rows) * BM, n0 = (rr / rows) * BN;
+  const auto xb = rows_from(p.x, m0, p.M, p.ldx), wb = rows_from(p.w, n0, p.N, p.ldw);
 
-  uint32_t aoff[NA], woff[NB];
-  int acol, wcol;  // this lane's piece of a step is the same for all its rows
+  const int acol = (lane & 7) ^ lr, bcol = (lane & 7) ^ ((lr & 3) | ((gw & 1) << 2));
+  uint32_t aoff[NA], boff[NB];
 #pragma unroll
-  for (int i = 0; i < NA; ++i) {
-    const int s = (wave + NW * i) * 64 + lane, r = s >> 3;
-    acol = (s & 7) ^ (r & 7);
-    aoff[i] = (uint32_t)(min(r, p.M - 1 - m0) * p.ldx);
-  }
+  for (int i = 0; i < NA; ++i) aoff[i] = (uint32_t)((gw + GW * i) * 8 + lr) * (uint32_t)p.ldx * 2u;
 #pragma unroll
-  for (int i = 0; i < NB; ++i) {
-    const int s = (wave + NW * i) * 64 + lane, r = s >> 3;
-    wcol = (s & 7) ^ (r & 7);
-    woff[i] = (uint32_t)(min(r, p.N - 1 - n0) * p.ldw);
-  }
-  auto issue = [&](int stage, int k0) {
-    unsigned char* base = lds + stage * STAGE;
-    const int ka = min(k0 + 8 * acol, p.K - 8), kw = min(k0 + 8 * wcol, p.K - 8);
+  for (int i = 0; i < NB; ++i) boff[i] = (uint32_t)((gw + GW * i) * 8 + lr) * (uint32_t)p.ldw * 2u;
+  const int nk = (p.K + kBK - 1) / kBK, nit = (nk + WK - 1) / WK;
+  auto load = [&](int it) {
+    const int k0 = (it * WK + kg) * kBK;
+    // pieces past K repeat the row's last one and enter the product as zeros
+    const int ka = min(k0 + 8 * acol, p.K - 8) * 2, kw = min(k0 + 8 * bcol, p.K - 8) * 2;
+    unsigned char* dst = lds + (it % NS) * STAGE + kg * STEP + gw * 1024;
 #pragma unroll
     for (int i = 0; i < NA; ++i)
-      __builtin_amdgcn_global_load_lds((glb_void*)(xb + aoff[i] + ka),
-                                       (lds_void*)(base + (wave + NW * i) * 1024), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void*)(dst + i * GW * 1024), 16, (int)(aoff[i] + ka), 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
-      __builtin_amdgcn_global_load_lds((glb_void*)(wb + woff[i] + kw),
-                                       (lds_void*)(base + A_BYTES + (wave + NW * i) * 1024), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lds_void*)(dst + A_BYTES + i * GW * 1024), 16, (int)(boff[i] + kw), 0, 0, 0);
   };
 
-  const int wm0 = (wave / WN) * (BM / WM), wn0 = (wave % WN) * (BN / WN);
-  const int fr = lane & 15, g = lane >> 4;
-  f32x4 acc[MT][NT];
+  f32x4 acc[MT][PT][2];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  const int nk = (p.K + kBK - 1) / kBK;
-  issue(0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    wait_vm<0>();
-    __syncthreads();
-    if (kt + 1 < nk) issue((kt + 1) & 1, (kt + 1) * kBK);
-    const unsigned char* sa = lds + (kt & 1) * STAGE;
-    const unsigned char* sb = sa + A_BYTES;
-    const int left = p.K - kt * kBK;  // of this step, in elements
-    auto piece = [&](const unsigned char* t, int r, int c) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(t + (r * 8 + (c ^ (r & 7))) * 16);
-      return frag(8 * c < left ? v : u32x4{0u, 0u, 0u, 0u});
+    for (int j = 0; j < PT; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[i][j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int wm0 = (gw / WN) * (BM / WM), wn0 = (gw % WN) * (BN / WN);
+  const int ar = wm0 + fr, br = wn0 + 8 * (fr >> 2) + (fr & 3);
+  const int aaddr = ar * 128 + ((g ^ (ar & 7)) << 4);
+  const int baddr = A_BYTES + br * 128 + ((g ^ ((br & 3) | ((br & 8) >> 1))) << 4);
+  auto step = [&](int it, bool last) {
+    const int at = (it % NS) * STAGE + kg * STEP, left = p.K - (it * WK + kg) * kBK;
+    auto piece = [&](int a, int c) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + a);
+      return frag(!last || 8 * c < left ? v : u32x4{0u, 0u, 0u, 0u});
     };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      bf16x8 a[MT], b[NT];
+      bf16x8 a[MT], b[PT][2];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) b[j] = piece(sb, wn0 + 16 * j + fr, 4 * h + g);
+      for (int j = 0; j < PT; ++j)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) a[i] = piece(sa, wm0 + 16 * i + fr, 4 * h + g);
+        for (int t = 0; t < 2; ++t) b[j][t] = piece(at + (baddr ^ (h << 6)) + j * 4096 + t * 512, 4 * h + g);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) a[i] = piece(at + (aaddr ^ (h << 6)) + i * 2048, 4 * h + g);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < PT; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            acc[i][j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j][t], a[i], acc[i][j][t], 0, 0, 0);
     }
+  };
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (i < nit) load(i);
+  for (int it = 0; it < nit; ++it) {
+    // this iteration's loads landed; NS - 2 younger ones may fly
+    if (it + NS - 1 <= nit) wait_vm_here<(NS - 2) * (NA + NB)>();
+    else wait_vm_here<0>();
+    wait_lds_here();
+    __builtin_amdgcn_s_barrier();  // everyone's, and stage it - 1 is out of LDS
+    asm volatile("" ::: "memory");
+    if (it + NS - 1 < nit) load(it + NS - 1);
+    if (it + 1 < nit) step(it, false);
+    else step(it, true);
+  }
+
+  if constexpr (WK > 1) {
+    f32x4* part = reinterpret_cast<f32x4*>(lds);
+    __syncthreads();
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < PT; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) part[((((kg - 1) * GW + gw) * MT + i) * PT + j) * 128 + t * 64 + lane] = acc[i][j][t];
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int v = 0; v < WK - 1; ++v)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < PT; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) acc[i][j][t] += part[(((v * GW + gw) * MT + i) * PT + j) * 128 + t * 64 + lane];
   }
   with_act(p.act, [&](auto act) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int n = n0 + wn0 + 16 * j + 4 * g;
-      float b[4];
+    for (int j = 0; j < PT; ++j) {
+      const int n = n0 + wn0 + 32 * j + 8 * g;
+      float b[8];
       load_bias(p, n, b);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int m = m0 + wm0 + 16 * i + fr;
-        float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        if (m < p.M) finish<act, 4>(p, m, n, v, b);
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = acc[i][j][e >> 2][e & 3];
+        if (m < p.M) finish<act, 8>(p, m, n, v, b);
       }
     }
   });
@@ -303,20 +367,6 @@ __device__ __forceinline__ void phase_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void wait_vm_here() {
-  asm volatile("" ::: "memory");
-  wait_vm<N>();
-  asm volatile("" ::: "memory");
-}
-
-// s_waitcnt lgkmcnt(0), the other counters left alone
-__device__ __forceinline__ void wait_lds_here() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xc07f);
-  asm volatile("" ::: "memory");
-}
-
 __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x & 63;
@@ -341,14 +391,7 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
 
   // of the tile whose loads are being issued
   int m0, n0;
-  // the matrices from the tile's first row on; rows past the last one are past
-  // the end of the buffer (they come out as zeros, and are not stored)
   __amdgpu_buffer_rsrc_t xb, wb;
-  auto rows_from = [&](const uint16_t* base, int row, int rows, int ld) {
-    const long long bytes = (long long)(rows - row) * ld * 2;
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (long long)row * ld), 0,
-                                             (int)(uint32_t)min(bytes, 0xffffffffLL), 0x00020000);
-  };
   auto turn_to = [&](int i) {
     const int l = first + i, per = kTurnBand * tiles_n;
     const int band = l / per, r = l - band * per, rows = min(kTurnBand, tiles_m - band * kTurnBand);
@@ -466,11 +509,11 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
     read_b(0, 0, false);
     // lane (fr, g) will hold columns 8 g .. 8 g + 7 of row fr of each 16 x 32 pair
     const int me = m0 + wm * 64 + fr, ne = n0 + wn * 32 + 8 * g;
-    const bool inside = m0 + 256 <= p.M && n0 + 256 <= p.N && p.vec;
+    const bool inside = m0 + 256 <= p.M && n0 + 256 <= p.N;
     u32x4 bias[2] = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
     if (inside && p.bias) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) bias[b] = *reinterpret_cast<const u32x4*>(p.bias + ne + b * 128);
+      for (int b = 0; b < 2; ++b) bias[b] = *reinterpret_cast<const u32x4_any*>(p.bias + ne + b * 128);
     }
     if (wm == 1) phase_barrier();
 #pragma unroll
@@ -578,14 +621,13 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// Up to 16 MT rows: a workgroup takes 16 columns (rows of w), its waves take
-// every 8th 64-wide piece of K, and their sums meet in LDS in a fixed order.
+// Up to 16 MT rows: a workgroup takes 16 columns (rows of w), its NW waves take
+// every NW-th 64-wide piece of K with the next piece's operands on their way
+// during a piece's products, and their sums meet in LDS in a fixed order.
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8;
-
-template <int MT>
-__global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinParams p) {
-  __shared__ f32x4 part[kFewWaves][MT][64];
+template <int MT, int NW>
+__global__ __launch_bounds__(64 * NW) void linear_few_kernel(LinParams p) {
+  __shared__ f32x4 part[NW][MT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int fr = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * 16;
@@ -596,29 +638,45 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinParams p)
   f32x4 acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave * 64; k0 < p.K; k0 += 64 * kFewWaves) {
+  u32x4 wv[2][2], xv[2][2][MT];  // [buffer][half of the piece]
+  auto read = [&](int buf, int k0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = k0 + 32 * h + 8 * g;
-      const bool in = k < p.K;
-      const int kc = min(k, p.K - 8);
-      const u32x4 z = {0u, 0u, 0u, 0u};
-      const u32x4 wv = *reinterpret_cast<const u32x4*>(wr + kc);
-      const bf16x8 b = frag(in ? wv : z);
+      const int k = min(k0 + 32 * h + 8 * g, p.K - 8);  // past K: repeated, and taken as zeros
+      wv[buf][h] = *reinterpret_cast<const u32x4*>(wr + k);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const u32x4 xv = *reinterpret_cast<const u32x4*>(xr[i] + kc);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, frag(in ? xv : z), acc[i], 0, 0, 0);
-      }
+      for (int i = 0; i < MT; ++i) xv[buf][h][i] = *reinterpret_cast<const u32x4*>(xr[i] + k);
+    }
+  };
+  auto product = [&](int buf, int k0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = k0 + 32 * h + 8 * g < p.K;
+      const u32x4 z = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(in ? wv[buf][h] : z), frag(in ? xv[buf][h][i] : z),
+                                                         acc[i], 0, 0, 0);
+    }
+  };
+  constexpr int kStep = 64 * NW;
+  int k0 = wave * 64;
+  if (k0 < p.K) read(0, k0);
+  for (; k0 < p.K; k0 += 2 * kStep) {
+    if (k0 + kStep < p.K) read(1, k0 + kStep);
+    product(0, k0);
+    if (k0 + kStep < p.K) {
+      if (k0 + 2 * kStep < p.K) read(0, k0 + 2 * kStep);
+      product(1, k0 + kStep);
     }
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
   __syncthreads();
-  for (int i = wave; i < MT; i += kFewWaves) {
+  for (int i = wave; i < MT; i += NW) {
     f32x4 s = part[0][i][lane];
 #pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) s += part[v][i][lane];
+    for (int v = 1; v < NW; ++v) s += part[v][i][lane];
     const int m = 16 * i + fr, n = n0 + 4 * g;
     float b[4], v[4] = {s[0], s[1], s[2], s[3]};
     load_bias(p, n, b);
@@ -626,21 +684,33 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(LinParams p)
   }
 }
 
-// Rows of n elements, ld apart, into rows of n8 = n rounded up to 8, the
-// rest zero: one 16-byte piece a thread.
-__global__ __launch_bounds__(256) void linear_pack_kernel(const uint16_t* src, long long ld,
-                                                          int rows, int n, int n8, uint16_t* dst) {
-  const int per = n8 / 8;
-  for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; u < (long long)rows * per;
+// Rows of n elements, ld apart, into rows of n8 = n rounded up to 8, the rest
+// zero, one 16-byte piece a thread: x, w or both, x first.
+struct PackParams {
+  const uint16_t* src[2];
+  uint16_t* dst[2];
+  long long ld[2], pieces[2];
+  int n, n8;
+};
+
+__global__ __launch_bounds__(256) void linear_pack_kernel(PackParams p) {
+  const int per = p.n8 / 8;
+  for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; u < p.pieces[0] + p.pieces[1];
        u += (long long)gridDim.x * 256) {
-    const long long r = u / per;
-    const int c = (int)(u - r * per) * 8;
-    uint16_t t[8];
+    const int which = u >= p.pieces[0];
+    const long long v = which ? u - p.pieces[0] : u, r = v / per;
+    const int c = (int)(v - r * per) * 8;
+    const uint16_t* src = (which ? p.src[1] : p.src[0]) + r * (which ? p.ld[1] : p.ld[0]) + c;
+    u32x4 t;
+    if (c + 8 <= p.n) {
+      t = *reinterpret_cast<const u32x4_any*>(src);
+    } else {
+      uint16_t e8[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = c + e < n ? src[r * ld + c + e] : (uint16_t)0;
-    u32x4 v;
-    __builtin_memcpy(&v, t, 16);
-    *reinterpret_cast<u32x4*>(dst + r * n8 + c) = v;
+      for (int e = 0; e < 8; ++e) e8[e] = c + e < p.n ? src[e] : (uint16_t)0;
+      __builtin_memcpy(&t, e8, 16);
+    }
+    *reinterpret_cast<u32x4*>((which ? p.dst[1] : p.dst[0]) + r * p.n8 + c) = t;
   }
 }
 
@@ -648,17 +718,27 @@ size_t al256(size_t n) { return (n + 255) & ~(size_t)255; }
 int up8(int n) { return (n + 7) & ~7; }
 bool packs(int K, long long ld) { return K % 8 != 0 || ld % 8 != 0; }
 
-template <int BM, int BN, int WM, int WN>
-hipError_t run_tiles(const LinParams& p, hipStream_t st) {
+template <int BM, int BN, int WM, int WN, int WK, int NS>
+hipError_t run_ring(const LinParams& p, hipStream_t st) {
   const long long tiles = (long long)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((linear_tile_kernel<BM, BN, WM, WN>), dim3((unsigned)tiles),
-                     dim3(64 * WM * WN), 2 * (BM + BN) * kBK * 2, st, p);
+  hipLaunchKernelGGL((linear_ring_kernel<BM, BN, WM, WN, WK, NS>), dim3((unsigned)tiles), dim3(64 * WM * WN * WK),
+                     NS * WK * (BM + BN) * kBK * 2, st, p);
   return hipGetLastError();
 }
 
 template <int MT>
 hipError_t run_few(const LinParams& p, hipStream_t st) {
-  hipLaunchKernelGGL((linear_few_kernel<MT>), dim3((p.N + 15) / 16), dim3(64 * kFewWaves), 0, st, p);
+  if (p.K > 512)
+    hipLaunchKernelGGL((linear_few_kernel<MT, 16>), dim3((p.N + 15) / 16), dim3(1024), 0, st, p);
+  else
+    hipLaunchKernelGGL((linear_few_kernel<MT, 8>), dim3((p.N + 15) / 16), dim3(512), 0, st, p);
+  return hipGetLastError();
+}
+
+hipError_t run_turn(const LinParams& p, hipStream_t st) {
+  const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
+  hipLaunchKernelGGL(linear_turn_kernel, dim3((unsigned)(tiles < kTurnCus ? tiles : kTurnCus)), dim3(512),
+                     8 * kHalfBytes, st, p);
   return hipGetLastError();
 }
 
@@ -687,36 +767,49 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
   p.K = up8(a.K);
   p.act = a.act;
   p.out_f32 = a.out_f32;
-  // 16-byte pieces: eight bf16 columns (the 4-column kernels need half), four float32 ones
-  const int unit = a.out_f32 ? 4 : 8;
-  p.vec = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.residual) |
-            reinterpret_cast<uintptr_t>(a.bias)) & 15u) == 0 &&
-          a.ldo % unit == 0 && (a.residual == nullptr || a.ldr % unit == 0);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  auto pack = [&](const uint16_t*& src, int& ld, int rows) -> hipError_t {
-    uint16_t* dst = reinterpret_cast<uint16_t*>(ws);
-    const long long pieces = (long long)rows * (p.K / 8);
-    const long long wgs = (pieces + 255) / 256;
-    hipLaunchKernelGGL(linear_pack_kernel, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0,
-                       st, src, (long long)ld, rows, a.K, p.K, dst);
+  PackParams pk{};
+  pk.n = a.K;
+  pk.n8 = p.K;
+  auto pack = [&](int which, const uint16_t*& src, int& ld, int rows) {
+    pk.src[which] = src;
+    pk.ld[which] = ld;
+    pk.dst[which] = reinterpret_cast<uint16_t*>(ws);
+    pk.pieces[which] = (long long)rows * (p.K / 8);
     ws += al256((size_t)rows * p.K * 2);
-    src = dst;
+    src = pk.dst[which];
     ld = p.K;
-    return hipGetLastError();
   };
-  hipError_t e = hipSuccess;
-  if (packs(a.K, a.ldx) && (e = pack(p.x, p.ldx, a.M)) != hipSuccess) return e;
-  if (packs(a.K, a.ldw) && (e = pack(p.w, p.ldw, a.N)) != hipSuccess) return e;
+  if (packs(a.K, a.ldx)) pack(0, p.x, p.ldx, a.M);
+  if (packs(a.K, a.ldw)) pack(1, p.w, p.ldw, a.N);
+  if (const long long n = pk.pieces[0] + pk.pieces[1]; n > 0) {
+    const long long wgs = (n + 255) / 256;
+    hipLaunchKernelGGL(linear_pack_kernel, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, st, pk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // The kernel follows from how many tiles there are for the 256 CUs. Measured
+  // (us, this choice / the next best): 222 x 58 x 4096 19 / 31, 700 x 1209 x
+  // 2384 15 / 22 (64 x 64 tiles); 1425 x 777 x 646 15 / 18 (128 x 64); 3825 x
+  // 610 x 3616 40 / 43, 8049 x 260 x 2952 35 / 38 (128 x 128, four stages);
+  // 28607 x 2031 x 224 72 / 80, 35266 x 476 x 96 17 / 19 (128 x 128, two
+  // stages, two workgroups a CU).
   if (p.M <= 16) return run_few<1>(p, st);
   if (p.M <= 32) return run_few<2>(p, st);
   if (p.M <= 64) return run_few<4>(p, st);
-  if ((long long)p.M * p.N >= 256LL * 256 * 256 && p.K > (kTurnMinSteps - 1) * kBK) {
-    const long long tiles = (long long)((p.M + 255) / 256) * ((p.N + 255) / 256);
-    hipLaunchKernelGGL(linear_turn_kernel, dim3((unsigned)(tiles < kTurnCus ? tiles : kTurnCus)), dim3(512),
-                       8 * kHalfBytes, st, p);
-    return hipGetLastError();
-  }
-  return run_tiles<128, 128, 2, 2>(p, st);
+  auto tiles = [&](int bm, int bn) { return (long long)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
+  if (tiles(64, 64) <= 256) return run_ring<64, 64, 2, 2, 2, 4>(p, st);
+  if (tiles(128, 64) <= 256) return run_ring<128, 64, 4, 2, 1, 3>(p, st);
+  if (tiles(128, 128) <= 256) return run_ring<128, 128, 2, 4, 1, 4>(p, st);
+  // Beyond that the 256 x 256 kernel takes 1.35 us a step and 10 us a tile, all
+  // CUs in step, and the 128 x 128 one 0.95 us and 7 us for each 512 tiles:
+  // 19706 x 1024 x 1024 (float32 with residual) 76 against 68, 15161 x 3143 x
+  // 1512 168 against 198, 4096 x 4096 x 1024 32 against 39.
+  const int nk = (p.K + kBK - 1) / kBK;
+  const double turn = (double)((tiles(256, 256) + kTurnCus - 1) / kTurnCus) * (1.35 * nk + 10.0);
+  const double ring = (double)tiles(128, 128) / 512.0 * (0.95 * nk + 7.0);
+  if (nk >= kTurnMinSteps && turn <= ring) return run_turn(p, st);
+  return run_ring<128, 128, 4, 2, 1, 2>(p, st);
 }
 
 }  // namespace gkd

