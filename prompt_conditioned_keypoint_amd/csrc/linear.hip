@@ -581,6 +581,7 @@ __global__ __launch_bounds__(512, 2) void linear_turn_kernel(LinParams p) {
     if (more) {
       turn_to(at);
       load_first();
+      asm volatile("" ::: "memory");  // the waits count on the epilogue's stores being younger
     }
     with_act(p.act, [&](auto act) {
       if (inside) {
