@@ -722,16 +722,30 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PaParams p) {
   const bool used = (long long)blockIdx.x * kRowsWg + rw < rows && t < query_length(p, b);
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   float l = 0.f;
+  // the lanes look at the slots' maxima side by side
+  float m = -INFINITY;
+  for (int s = lane; s < p.slots; s += LPR) m = fmaxf(m, p.ml[2 * (s * rows + row)]);
+#pragma unroll
+  for (int d = 1; d < LPR; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  const float ref = m == -INFINITY ? 0.f : m;
   if (used) {
-    float m = -INFINITY;
-    for (int s = 0; s < p.slots; ++s) m = fmaxf(m, p.ml[2 * (s * rows + row)]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    for (int s = grp; s < p.slots; s += kGroups) {
-      const f32x2 x = *reinterpret_cast<const f32x2*>(p.ml + 2 * (s * rows + row));
-      if (!(x[1] > 0.f)) continue;  // nothing there, O not written
-      const float wgt = __builtin_amdgcn_exp2f(x[0] - ref);
-      l = fmaf(x[1], wgt, l);
-      o += *reinterpret_cast<const f32x4*>(p.po + (s * rows + row) * D + 4 * lane) * wgt;
+    constexpr int U = 4;  // slots whose loads are in flight together
+    for (int s0 = grp; s0 < p.slots; s0 += U * kGroups) {
+      f32x2 x[U];
+      f32x4 y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const long long at = min(s0 + u * kGroups, p.slots - 1) * rows + row;
+        x[u] = *reinterpret_cast<const f32x2*>(p.ml + 2 * at);
+        y[u] = *reinterpret_cast<const f32x4*>(p.po + at * D + 4 * lane);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (s0 + u * kGroups >= p.slots || !(x[u][1] > 0.f)) continue;  // nothing there, O not written
+        const float wgt = __builtin_amdgcn_exp2f(x[u][0] - ref);
+        l = fmaf(x[u][1], wgt, l);
+        o += y[u] * wgt;
+      }
     }
   }
   so[grp][rw][lane] = o;
@@ -788,7 +802,7 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
     // every tile stays in its sequence and takes prefix and own keys
     const int wide = RS > 16, tiles = B * cdiv(RS, wide ? 128 : 16);
     const int parts = wide ? parts_for((long long)P + S, (long long)tiles * Hk, 512, 256)
-                           : parts_for((long long)P + S, (long long)tiles * Hk, 256, 1024);
+                           : parts_for((long long)P + S, (long long)tiles * Hk, 256, (long long)P + S <= 1024 ? 1024 : 512);
     pl.first = list(wide, 1, 2, tiles, parts, 0);
     pl.slots = parts;
     return pl;
