@@ -114,8 +114,8 @@ GKD_API gkd_status gkd_linear(const void *x, int64_t ldx, const void *w, int64_t
  *   q_weight, k_weight [D] dtype or NULL
  * Limits: D <= 512, rot even, 2 <= rot <= D, 1 <= n_axes <= 8, eps >= 0
  * and finite. dtype: f32 or bf16. Arrays are aligned to their elements.
- * Where data pointers and strides are multiples of 16 bytes and D (and for
- * split pairs rot/2) fills whole 16-byte pieces, 16-byte accesses are used.
+ * Where data pointers and strides are multiples of 16 bytes and D fills
+ * whole 16-byte pieces, 16-byte accesses are used.
  */
 GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads *q, int Hq, const gkd_heads *k, int Hk, int B,
                                     int T, int D, const float *pos, int64_t pos_batch, int n_axes,

@@ -808,10 +808,11 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
     return pl;
   }
   // the prefix for the rows of all sequences together, own keys apart
-  // (beside thin items 256 wide ones, one a CU: with 512 the 48 sequences
-  // behind 32768 keys take 102 instead of 89 us; beside wide ones 512)
+  // (beside thin items one wide one a CU: with 512 the 48 sequences with 1024
+  // own keys behind 32768 take 102 instead of 89 us; but where own keys are
+  // few, 384: 16 sequences with 256 behind 65536 61 instead of 69 us)
   const int wide = RS > 16, tiles = cdiv(RT, 128);
-  const int parts = parts_for(P, (long long)tiles * Hk, wide ? 512 : 256, 256);
+  const int parts = parts_for(P, (long long)tiles * Hk, wide ? 512 : P / 64 >= S ? 384 : 256, 256);
   pl.first = list(1, 0, 0, tiles, parts, 0);
   const int own_tiles = B * cdiv(RS, wide ? 128 : 16);
   pl.second = list(wide, 1, 1, own_tiles, parts_for(S, (long long)own_tiles * Hk, 256, 256), parts);

@@ -87,13 +87,19 @@ struct Piece<uint16_t> {
 // side, pieces 2 j and 2 j + 1; for split pairs (i, i + rot/2), pieces j and
 // rot/2/N + j while they rotate, then the rest of the head two by two. In
 // both orders the lane's pairs are N j .. N j + N - 1, so cosines and sines
-// are read as whole float4s; past rot/2 the table holds (1, 0). Every lane
-// reads its two pieces before it writes them and no lane touches another's,
-// so an output may be its input.
-template <typename T, int LP, bool IL>
+// are read as whole float4s; past rot/2 the table holds (1, 0). Split pairs
+// whose half is no whole number of pieces (kLoose) keep pieces 2 j and 2 j + 1
+// and find each element's partner in LDS, where the head's lanes put their
+// values. Every lane reads its two pieces before it writes them and no lane
+// touches another's, so an output may be its input.
+enum { kSplit = 0, kSide = 1, kLoose = 2 };
+__host__ __device__ constexpr int loose_floats(int npair) { return 2 * npair + 2 * npair / 8; }
+
+template <typename T, int LP, int PAIRS>
 __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   constexpr int N = Piece<T>::N;
-  extern __shared__ __attribute__((aligned(16))) float cs[];  // [tt][2][npair]
+  constexpr bool IL = PAIRS == kSide;
+  extern __shared__ __attribute__((aligned(16))) float cs[];  // [tt][2][npair], kLoose: and the heads' values
   const int tid = threadIdx.x;
   const int np = (p.D + 2 * N - 1) / (2 * N), npair = np * N;
   const long long tok0 = p.first + (long long)blockIdx.x * p.tt;
@@ -112,7 +118,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   // the pair's two pieces (element offsets; b1: the second one exists)
   const int hp = p.half / N;
   int e0, e1;
-  if (IL) {
+  if (PAIRS != kSplit) {
     e0 = 2 * j * N;
     e1 = e0 + N;
   } else if (j < hp) {
@@ -123,7 +129,11 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
     e1 = e0 + N;
   }
   const bool b0 = j < np && e0 < p.D, b1 = j < np && e1 < p.D;
-  const bool turn = IL ? true : j < hp;
+  const bool turn = PAIRS != kSplit || j < hp;
+  // kLoose: this head's values, a gap after every 8 so that lanes 16 apart meet
+  // different banks
+  float* mine = cs + 2 * p.tt * npair + (tid / LP) * loose_floats(npair);
+  auto gap = [](int e) { return e + (e >> 3); };
   const u32x4 z4 = {0u, 0u, 0u, 0u};
   u32x4 wq0 = z4, wq1 = z4, wk0 = z4, wk1 = z4;  // gains, as stored
   auto gain = [&](const void* w, int e, bool in) {
@@ -169,7 +179,33 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
       }
     }
     float y0[N], y1[N];
-    if (turn && b0) {
+    if constexpr (PAIRS == kLoose) {
+      if (b0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          mine[gap(e0 + i)] = x0[i];
+          mine[gap(e1 + i)] = x1[i];
+        }
+      }
+      asm volatile("" ::: "memory");  // the head's lanes are in one wave, whose LDS accesses keep their order
+      __builtin_amdgcn_wave_barrier();
+      const float* c = cs + (2 * t) * npair;
+      const float* s = c + npair;
+      auto turned = [&](int e, float x) {
+        const bool second = e >= p.half;
+        if (e >= 2 * p.half || e >= p.D) return x;
+        const int i = second ? e - p.half : e;
+        const float y = mine[gap(second ? i : e + p.half)];
+        return second ? x * c[i] + y * s[i] : x * c[i] - y * s[i];
+      };
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        y0[i] = turned(e0 + i, x0[i]);
+        y1[i] = turned(e1 + i, x1[i]);
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+    } else if (turn && b0) {
       const float* c = cs + (2 * t) * npair + N * j;
       const float* s = c + npair;
       if (IL) {
@@ -204,7 +240,7 @@ __device__ __forceinline__ float rope_load(const uint16_t* p) { return bf16_bits
 __device__ __forceinline__ void rope_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void rope_store(uint16_t* p, float v) { *p = f32_to_bf16_bits(v); }
 
-// Any alignment, head width and rotated width: one wave a head, elements
+// Any alignment and head width: one wave a head, elements
 // one by one (D <= 512: at most 4 rotated pairs and 8 other elements a
 // lane). A lane reads all its elements before it writes them.
 template <typename T>
@@ -265,7 +301,7 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeParams p, bool interl
 constexpr long long kMostWgs = 1 << 23;
 
 template <typename T, int LP>
-hipError_t run_pieces(RopeParams p, bool il, hipStream_t st) {
+hipError_t run_pieces(RopeParams p, int pairs, hipStream_t st) {
   constexpr int N = Piece<T>::N;
   const int npair = (p.D + 2 * N - 1) / (2 * N) * N;
   // about 1024 pairs of pieces a workgroup (four rounds of its lanes), while
@@ -275,14 +311,16 @@ hipError_t run_pieces(RopeParams p, bool il, hipStream_t st) {
   const long long most = 16384 / (8 * npair);
   if (tt > most) tt = most;
   p.tt = (int)tt;
-  const size_t lds = (size_t)tt * npair * 8;
+  const size_t lds = (size_t)tt * npair * 8 + (pairs == kLoose ? (size_t)(256 / LP) * loose_floats(npair) * 4 : 0);
   for (; p.first < p.n_tok; p.first += kMostWgs * tt) {
     const long long wgs = (p.n_tok - p.first + tt - 1) / tt;
     const dim3 grid((unsigned)(wgs < kMostWgs ? wgs : kMostWgs));
-    if (il)
-      hipLaunchKernelGGL((rope_kernel<T, LP, true>), grid, dim3(256), lds, st, p);
+    if (pairs == kSide)
+      hipLaunchKernelGGL((rope_kernel<T, LP, kSide>), grid, dim3(256), lds, st, p);
+    else if (pairs == kSplit)
+      hipLaunchKernelGGL((rope_kernel<T, LP, kSplit>), grid, dim3(256), lds, st, p);
     else
-      hipLaunchKernelGGL((rope_kernel<T, LP, false>), grid, dim3(256), lds, st, p);
+      hipLaunchKernelGGL((rope_kernel<T, LP, kLoose>), grid, dim3(256), lds, st, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -295,15 +333,16 @@ hipError_t run_typed(const RopeArgs& a, RopeParams p, hipStream_t st) {
   auto whole = [](const Heads& h) {
     return (reinterpret_cast<uintptr_t>(h.p) & 15u) == 0 && h.b % N == 0 && h.t % N == 0 && h.h % N == 0;
   };
-  bool pieces = a.D % N == 0 && (a.interleaved || p.half % N == 0) && whole(a.q) && whole(a.qo);
+  bool pieces = a.D % N == 0 && whole(a.q) && whole(a.qo);
+  const int pairs = a.interleaved ? kSide : p.half % N == 0 ? kSplit : kLoose;
   if (a.Hk > 0) pieces = pieces && whole(a.k) && whole(a.ko);
   if (pieces) {
     const int np = (a.D + 2 * N - 1) / (2 * N);
-    if (np <= 4) return run_pieces<T, 4>(p, a.interleaved, st);
-    if (np <= 8) return run_pieces<T, 8>(p, a.interleaved, st);
-    if (np <= 16) return run_pieces<T, 16>(p, a.interleaved, st);
-    if (np <= 32) return run_pieces<T, 32>(p, a.interleaved, st);
-    return run_pieces<T, 64>(p, a.interleaved, st);
+    if (np <= 4) return run_pieces<T, 4>(p, pairs, st);
+    if (np <= 8) return run_pieces<T, 8>(p, pairs, st);
+    if (np <= 16) return run_pieces<T, 16>(p, pairs, st);
+    if (np <= 32) return run_pieces<T, 32>(p, pairs, st);
+    return run_pieces<T, 64>(p, pairs, st);
   }
   for (; p.first < p.n_tok * p.H; p.first += kMostWgs * 4) {
     const long long wgs = (p.n_tok * p.H - p.first + 3) / 4;

@@ -201,6 +201,14 @@ def test_rope_any_width(gkd, dtype, D, rot):
     check_rope(gkd, 1, 3, 1, 2, D, rot, 3, dtype, False, True, seed=D)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,rot", [(64, 50), (96, 76), (128, 6), (256, 226), (512, 510), (80, 78), (40, 2)])
+def test_rope_halves_of_no_whole_pieces(gkd, dtype, D, rot):
+    """Split pairs whose halves end inside a 16-byte piece."""
+    check_rope(gkd, 2, 37, 3, 2, D, rot, 2, dtype, True, False, seed=D)
+    check_rope(gkd, 1, 5, 1, 1, D, rot, 1, dtype, False, False, seed=D)
+
+
 @pytest.mark.parametrize("B,T,Hq,Hk,A", [(1, 1, 1, 1, 1), (1, 1, 32, 8, 1), (3, 129, 1, 1, 3), (2, 77, 5, 1, 8),
                                          (1, 700, 16, 16, 2)])
 def test_rope_counts(gkd, B, T, Hq, Hk, A):
@@ -233,7 +241,12 @@ def test_rope_in_place_shared_table_queries_alone_and_strided_out(gkd):
     o2, _ = gkd.qk_norm_rope(off, None, pos, freqs, wq)
     err = (o2.float() - want[0].float()).abs()
     assert bool((err <= 2 ** -7 * want[0].float().abs() + 1e-6).all())
-    # in place, both kernels
+    # in place, all kernels
+    f2 = freqs[:, :21].contiguous()
+    loose = gkd.qk_norm_rope(q, k, pos, f2, wq, wk)
+    q2, k2 = q.clone(), k.clone()
+    gkd.qk_norm_rope(q2, k2, pos, f2, wq, wk, q_out=q2, k_out=k2)
+    assert torch.equal(q2, loose[0]) and torch.equal(k2, loose[1])
     gkd.qk_norm_rope(q, k, pos, freqs, wq, wk, q_out=q, k_out=k)
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
     gkd.qk_norm_rope(off, None, pos, freqs, wq, q_out=off)
