@@ -707,11 +707,12 @@ __global__ __launch_bounds__(512, 4) void prefix_thin_kernel(PaParams p) {
   run_item<ThinTile<D, 8>>(p, p.first, lds, blockIdx.x);
 }
 
-// Joins a row's partial results, D / 4 lanes a row: four groups of slots side
-// by side (their loads in flight together), then the groups in order.
-template <int D>
+// Joins a row's partial results, D / 4 lanes a row: kGroups groups of slots
+// side by side (four loads of each in flight together), then the groups in
+// order. Up to four slots take one group.
+template <int D, int kGroups>
 __global__ __launch_bounds__(256) void prefix_join_kernel(PaParams p) {
-  constexpr int LPR = D / 4, kGroups = 4, kRowsWg = 256 / (LPR * kGroups);
+  constexpr int LPR = D / 4, kRowsWg = 256 / (LPR * kGroups);
   __shared__ f32x4 so[kGroups][kRowsWg][LPR];
   __shared__ float sl[kGroups][kRowsWg];
   const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR % kGroups, rw = threadIdx.x / (LPR * kGroups);
@@ -835,7 +836,11 @@ hipError_t run(const PaParams& p, const Plan& pl, hipStream_t st) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || pl.slots == 1) return e;
   const long long rows = (long long)p.Hk * p.RT;
-  hipLaunchKernelGGL((prefix_join_kernel<D>), dim3((unsigned)cdiv(rows, 256 / D)), dim3(256), 0, st, p);
+  constexpr int many = 256 / D, few = 1024 / D;  // rows a workgroup
+  if (pl.slots > 4)
+    hipLaunchKernelGGL((prefix_join_kernel<D, 4>), dim3((unsigned)cdiv(rows, many)), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((prefix_join_kernel<D, 1>), dim3((unsigned)cdiv(rows, few)), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
