@@ -790,15 +790,15 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
     return List{wide, seq, keys, tiles, parts, slot, (int)((long long)tiles * Hk * parts)};
   };
   // Packing the rows of all sequences reads the prefix once for 128 of them
-  // and costs a second list of items, partial results and a join. Measured
-  // (us, packed / in sequence): 64 x 1 rows of 16 heads of 64 behind 4096 keys
-  // 21 / 77, behind 256 keys 20 / 16; 64 x 48 rows of 8 heads of 128 behind
-  // 4096 keys 100 / 122, behind 1024 keys 52 / 36; two sequences behind 16384
-  // keys 29 / 21; 37 x 80 rows behind 2304 keys with 80 own ones 63 / 71, but
-  // 16 x 96 rows behind 8192 with 512 own ones 98 / 80. Tiles of 128 rows or
-  // more are full as they are.
-  const bool packed = B >= 4 && B <= kMostPacked && S > 0 && RS < 128 && P >= (RS <= 16 ? 1024 : 2048) &&
-                      (RS < 64 || P / 24 >= S);
+  // and costs a second list of items, partial results and a join; tiles within
+  // a sequence leave 128 - RS of their rows empty instead. Measured (us, packed
+  // / in sequence): 64 x 1 row of 16 heads of 64 behind 4096 keys 21 / 77,
+  // behind 256 20 / 16; two sequences behind 16384 29 / 21; 37 x 80 rows behind
+  // 2304 54 / 72, behind 1024 38 / 38; 64 x 96 rows of 8 heads of 128 behind
+  // 8192 236 / 246, behind 2304 89 / 77; 8 x 80 rows behind 2304 32 / 29.
+  const bool packed = S > 0 && B <= kMostPacked &&
+                      (RS <= 16 ? B >= 4 && P >= 1024
+                                : B >= 16 && RS < 128 && P >= 2048 && (128 - RS) * P >= 90000);
   if (!packed) {
     // every tile stays in its sequence and takes prefix and own keys
     const int wide = RS > 16, tiles = B * cdiv(RS, wide ? 128 : 16);
