@@ -52,7 +52,9 @@ typedef enum {
 
 /* Heads in memory: element (b, t, h, d) of a [B, T, H, D] operand is
  * data[b*batch + t*token + h*head + d]. Strides are in elements, none
- * negative; a head's D values are adjacent. */
+ * negative; a head's D values are adjacent. An output's elements all have
+ * places of their own: a stride of 0 over a size above one is refused there
+ * (GKD_ERR_SHAPE), and allowed for inputs. */
 typedef struct {
     void *data;
     int64_t batch, token, head;
@@ -75,7 +77,8 @@ typedef struct {
  *            where that is 0). Operands whose rows do not all start on
  *            16-byte boundaries (ldx or ldw % 8 != 0, or K % 8 != 0) are
  *            first copied there; any other layout runs in place.
- * Any M, N >= 0 and K >= 1 (M, N < 2^26, ldx, ldw < 2^22, else GKD_ERR_SHAPE);
+ * Any M, N >= 0 and K >= 1 (M < 2^26, N < 2^25, M N < 2^36, ldx, ldw < 2^22,
+ * else GKD_ERR_SHAPE);
  * dtype must be GKD_DTYPE_BF16. flags must be 0. M == 0 or N == 0: nothing
  * is launched.
  */
@@ -132,7 +135,7 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads *q, int Hq, const gkd_heads 
 /*
  * Attention of a batch with a shared prefix of keys:
  *   out[b,i,h] = softmax_j(scale q[b,i,h] . K_j) V_j
- * over the P prefix keys, the same for every sequence and read once for the
+ * over the P prefix keys, the same for every sequence and held once for the
  * whole batch, and the sequence's own keys j < own_len[b] with own_mask[b,j]
  * set (and, with GKD_ATTN_CAUSAL, visible to query i). Head h reads key
  * head h / (Hq / Hk). A query that sees no key gives zeros.
@@ -148,10 +151,11 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads *q, int Hq, const gkd_heads 
  *   workspace  gkd_prefix_attention_workspace_size() bytes, 256-byte
  *            aligned (NULL where that is 0)
  * Own keys and values past own_len or masked may hold anything, NaN
- * included; every other input must be finite. Scores, softmax statistics
+ * included, and so may queries past q_len; every other input must be
+ * finite, and so must the scores. Scores, softmax statistics
  * and outputs are float32; probabilities are rounded to bfloat16 for the
  * product with V. Limits: D 64 or 128, Hq a multiple of Hk, B Tq Hq below
- * 2^31, P and S below 2^30, scale finite and above 0; dtype must be
+ * 2^31, B Hk ceil(Tq Hq / Hk / 128) below 2^23, P and S below 2^30, scale finite and above 0; dtype must be
  * GKD_DTYPE_BF16. q, k, v and
  * out: 16-byte aligned data, strides multiples of 8 (else GKD_ERR_ALIGN);
  * token strides of keys and values below 2^25 (else GKD_ERR_SHAPE).

@@ -796,7 +796,8 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   // behind 256 20 / 16; two sequences behind 16384 29 / 21; 37 x 80 rows behind
   // 2304 54 / 72, behind 1024 38 / 38; 64 x 96 rows of 8 heads of 128 behind
   // 8192 236 / 246, behind 2304 89 / 77; 8 x 80 rows behind 2304 32 / 29.
-  const bool packed = S > 0 && B <= kMostPacked &&
+  // (The last limit keeps the join's threads below 2^32.)
+  const bool packed = S > 0 && B <= kMostPacked && RT * Hk < (1 << 25) &&
                       (RS <= 16 ? B >= 4 && P >= 1024
                                 : B >= 16 && RS < 128 && P >= 2048 && (128 - RS) * P >= 90000);
   if (!packed) {

@@ -32,6 +32,17 @@ gkd_status check_heads(const char* fn, const char* name, const gkd_heads* h, uns
   return GKD_OK;
 }
 
+// An output, of which no two elements may share a place: no stride of a size
+// above one is 0.
+gkd_status check_out(const char* fn, const char* name, const gkd_heads* h, unsigned size, unsigned n, int B,
+                     int T, int H) {
+  const gkd_status st = check_heads(fn, name, h, size, n);
+  if (st != GKD_OK) return st;
+  if ((B > 1 && h->batch == 0) || (T > 1 && h->token == 0) || (H > 1 && h->head == 0))
+    return fail(GKD_ERR_SHAPE, "%s: a stride of %s is 0", fn, name);
+  return GKD_OK;
+}
+
 // Keys and values of the attention: a chunk of 64 of them is addressed with
 // 32 bits.
 gkd_status check_keys(const char* fn, const char* name, const gkd_heads* h) {
@@ -51,13 +62,18 @@ gkd_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t 
 }
 
 bool linear_sizes_ok(int M, int N, int K, int64_t ldx, int64_t ldw) {
-  return M >= 0 && N >= 0 && K >= 1 && M < (1 << 26) && N < (1 << 26) && ldx >= K && ldw >= K &&
-         ldx < (1 << 22) && ldw < (1 << 22);
+  // (a launch has fewer than 2^32 threads)
+  return M >= 0 && N >= 0 && K >= 1 && M < (1 << 26) && N < (1 << 25) && (int64_t)M * N < (1LL << 36) &&
+         ldx >= K && ldw >= K && ldx < (1 << 22) && ldw < (1 << 22);
 }
 
 bool attn_sizes_ok(int B, int Tq, int Hq, int Hk, int P, int S) {
-  return B >= 0 && Tq >= 0 && Hk >= 1 && Hq >= 1 && P >= 0 && S >= 0 && P < (1 << 30) && S < (1 << 30) &&
-         (B == 0 || Tq == 0 || (long long)B * Tq <= 0x7fffffffLL / Hq);
+  if (B < 0 || Tq < 0 || Hk < 1 || Hq < 1 || P < 0 || S < 0 || P >= (1 << 30) || S >= (1 << 30)) return false;
+  if (B == 0 || Tq == 0) return true;
+  if ((long long)B * Tq > 0x7fffffffLL / Hq) return false;
+  // (a launch has fewer than 2^32 threads)
+  const long long tiles = ((long long)Tq * Hq / Hk + 127) / 128;
+  return (long long)B * Hk < (1 << 23) && (long long)B * Hk * (tiles > 0 ? tiles : 1) < (1 << 23);
 }
 
 }  // namespace
@@ -140,10 +156,10 @@ gkd_status gkd_qk_norm_rope(const gkd_heads* q, int Hq, const gkd_heads* k, int 
     return fail(GKD_ERR_NULL, "%s: k and k_out go with Hk > 0", fn);
   gkd_status st;
   if ((st = check_heads(fn, "q", q, size, size)) != GKD_OK) return st;
-  if ((st = check_heads(fn, "q_out", q_out, size, size)) != GKD_OK) return st;
+  if ((st = check_out(fn, "q_out", q_out, size, size, B, T, Hq)) != GKD_OK) return st;
   if (Hk > 0) {
     if ((st = check_heads(fn, "k", k, size, size)) != GKD_OK) return st;
-    if ((st = check_heads(fn, "k_out", k_out, size, size)) != GKD_OK) return st;
+    if ((st = check_out(fn, "k_out", k_out, size, size, B, T, Hk)) != GKD_OK) return st;
   }
   if (!pos || !freqs) return fail(GKD_ERR_NULL, "%s: NULL pos or freqs", fn);
   if (!aligned(pos, 4) || !aligned(freqs, 4) || !aligned(q_weight, size) || !aligned(k_weight, size))
@@ -199,7 +215,7 @@ gkd_status gkd_prefix_attention(const gkd_heads* q, const gkd_heads* k_prefix,
   if (B == 0 || Tq == 0) return ok();
   gkd_status st;
   if ((st = check_heads(fn, "q", q, 2, 16)) != GKD_OK) return st;
-  if ((st = check_heads(fn, "out", out, 2, 16)) != GKD_OK) return st;
+  if ((st = check_out(fn, "out", out, 2, 16, B, Tq, Hq)) != GKD_OK) return st;
   if (P > 0) {
     if ((st = check_keys(fn, "k_prefix", k_prefix)) != GKD_OK) return st;
     if ((st = check_keys(fn, "v_prefix", v_prefix)) != GKD_OK) return st;

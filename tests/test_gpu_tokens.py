@@ -105,6 +105,55 @@ def test_linear_large(gkd, M, K, N):
     check_linear(gkd, M, K, N, "gelu", seed=N)
 
 
+@pytest.mark.parametrize("M,K,N,act,out,residual", [
+    (5601, 520, 5797, "relu", BF, True),      # 256 x 256 tiles, two a workgroup, no even edge
+    (5601, 250, 5800, "none", F32, True),
+    (4000, 331, 4090, "silu", BF, False),     # one a workgroup, rows copied first
+    (2100, 400, 1100, "gelu", F32, True),     # 128 x 128 tiles, a step or several
+    (2100, 40, 1101, "none", BF, True),
+    (1025, 72, 1023, "relu", F32, True),      # 128 x 64
+    (20000, 24, 300, "none", BF, True),       # 128 x 128, two workgroups a CU
+])
+def test_linear_tile_sizes(gkd, M, K, N, act, out, residual):
+    check_linear(gkd, M, K, N, act, out=out, residual=residual, seed=K)
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (64, 33), (150, 170), (1100, 1000), (2100, 1100), (4097, 4096),
+                                 (20000, 300)])
+@pytest.mark.parametrize("K", [72, 328])
+def test_linear_reads_nothing_beside_its_rows(gkd, M, N, K):
+    """NaN between the rows, before and behind them changes nothing."""
+    g = rng(M + N)
+    x, w, b = randn(g, M, K), randn(g, N, K), randn(g, N)
+    want = gkd.linear(x, w, bias=b)
+
+    def framed(t):
+        buf = torch.full((t.shape[0] + 2, K + 24), float("nan"), dtype=BF, device="cuda")
+        view = buf[1:-1, 8:8 + K]
+        view.copy_(t)
+        return view
+    out = torch.full((M + 2, N + 3), 7.0, dtype=BF, device="cuda")
+    got = gkd.linear(framed(x), framed(w), bias=b, out=out[1:-1, 1:-2])
+    assert torch.equal(got, want)
+    out[1:-1, 1:-2] = 7
+    assert bool((out == 7).all())
+
+
+@pytest.mark.parametrize("M,N", [(40, 600), (600, 600)])
+def test_linear_rows_past_32_bit_offsets(gkd, M, N):
+    """Rows 2^22 - 8 elements apart: the last of 600 lie past 2^31 elements."""
+    g, K, ld = rng(6), 200, (1 << 22) - 8
+    x, w, r = randn(g, M, K), randn(g, N, K), randn(g, M, N)
+    want = gkd.linear(x, w, residual=r)
+
+    def spread(t):
+        far = torch.empty(t.shape[0], ld, dtype=BF, device="cuda")[:, :t.shape[1]]
+        far.copy_(t)
+        return far
+    far = spread(r)
+    assert torch.equal(gkd.linear(spread(x), spread(w), residual=far, out=far), want)
+
+
 def test_linear_extreme_activations(gkd):
     """Activations far out: their limits, and NaN stays where it is."""
     x = torch.tensor([[200.0], [-200.0], [1e30], [-1e30], [0.0], [float("nan")]], device="cuda").to(BF)
@@ -253,6 +302,24 @@ def test_rope_in_place_shared_table_queries_alone_and_strided_out(gkd):
     assert torch.equal(off, o2)
 
 
+def test_rope_past_32_bit_offsets_and_two_streams(gkd):
+    g = rng(15)
+    for D, rot, inter in ((64, 64, False), (64, 42, False), (64, 42, True), (36, 20, False)):
+        q, k, pos, freqs, wq, wk = rope_inputs(g, 2, 70, 3, 2, D, rot, 2, BF)
+        want = gkd.qk_norm_rope(q, k, pos, freqs, wq, wk, interleaved=inter)
+        far = torch.empty(2, 70, 1 << 25, dtype=BF, device="cuda")      # 2^25 elements a token: 9.4 GB
+        fq, fk = far[:, :, :3 * D].unflatten(2, (3, D)), far[:, :, 1024:1024 + 2 * D].unflatten(2, (2, D))
+        fq.copy_(q), fk.copy_(k)
+        torch.cuda.synchronize()
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            gkd.qk_norm_rope(fq, fk, pos, freqs, wq, wk, interleaved=inter, q_out=fq, k_out=fk)
+        again = gkd.qk_norm_rope(q, k, pos, freqs, wq, wk, interleaved=inter)
+        torch.cuda.synchronize()
+        assert torch.equal(fq, want[0]) and torch.equal(fk, want[1])
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
 def test_rope_zero_rows_and_refusals(gkd):
     z = torch.zeros(1, 2, 1, 64, dtype=BF, device="cuda")
     pos, freqs = torch.zeros(2, 1, device="cuda"), torch.ones(1, 32, device="cuda")
@@ -366,6 +433,73 @@ def test_attention_hidden_places_may_hold_anything(gkd, Tq):
                                               (2, 260, 2, 1, 128, 700, 300)])
 def test_attention_split_ranges(gkd, B, Tq, Hq, Hk, D, P, S):
     check_attn(gkd, B, Tq, Hq, Hk, D, P, S, [S - 7 * b for b in range(B)], None, None, True, seed=P)
+
+
+# Batches whose rows are packed over the sequences for the prefix: few and
+# many rows a sequence, more than 256 sequences, and one too many to pack.
+PACKED = [(5, 1, 4, 2, 64, 1050, 70), (6, 3, 8, 2, 128, 1100, 150), (9, 16, 2, 2, 64, 1024, 33),
+          (17, 33, 2, 2, 64, 2050, 40), (17, 20, 4, 1, 128, 2100, 130), (16, 97, 1, 1, 64, 3001, 97),
+          (300, 1, 4, 2, 64, 1030, 33), (1024, 1, 2, 2, 64, 1024, 9), (1025, 1, 2, 2, 64, 1024, 9),
+          (600, 18, 2, 2, 64, 2048, 20)]
+
+
+@pytest.mark.parametrize("B,Tq,Hq,Hk,D,P,S", PACKED)
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_packed_rows(gkd, B, Tq, Hq, Hk, D, P, S, causal):
+    some = [S, Tq, 0, S // 2 + 1, S + 60, -3, 1]
+    less = [Tq, max(Tq - 2, 0), Tq, 1, Tq + 9, 0, Tq]
+    own_len, q_len = [some[b % 7] for b in range(B)], [less[b % 7] for b in range(B)]
+    check_attn(gkd, B, Tq, Hq, Hk, D, P, S, own_len, q_len, masks(1, B, S), causal, seed=P)
+    if B < 100:
+        check_attn(gkd, B, Tq, Hq, Hk, D, P, S, own_len, None, None, causal, seed=P)
+        check_attn(gkd, B, Tq, Hq, Hk, D, P, S, None, [0] * B, None, causal, seed=P)
+        check_attn(gkd, B, Tq, Hq, Hk, D, P, S, None, [0] * (B - 1) + [Tq], None, causal, seed=P)
+
+
+@pytest.mark.parametrize("Tq", [1, 5, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_packed_rows_beside_hidden_places(gkd, Tq, D):
+    """NaN and infinities past own_len, under the mask and past q_len, with
+    strided caches and an output between other values."""
+    g = rng(12)
+    B, Hq, Hk, P, S = 18, 4, 2, 2100, 60
+    q, kp, vp, ko, vo = attn_inputs(g, B, Tq, Hq, Hk, D, P, S)
+    own_len = torch.tensor([60, 33, 0] * 6, dtype=torch.int32, device="cuda")
+    q_len = torch.tensor([Tq, max(1, Tq - 1), 0, Tq, 1, Tq] * 3, dtype=torch.int32, device="cuda")
+    m = masks(2, B, S)
+    kw = dict(own_len=own_len, q_len=q_len, own_mask=m)
+    want = gkd.prefix_attention(q, kp, vp, ko, vo, out=torch.full_like(q, 7.0), **kw)
+    hidden = (m == 0) | (torch.arange(S, device="cuda") >= own_len[:, None])
+    heads_first = lambda t: t.transpose(-2, -3).contiguous().transpose(-2, -3)
+    ko, vo, kp, vp, q = (heads_first(t) for t in (ko, vo, kp, vp, q))
+    ko[hidden], vo[hidden] = float("nan"), float("inf")
+    vo[..., ::2][hidden] = float("nan")
+    q[torch.arange(Tq, device="cuda") >= q_len[:, None]] = float("nan")
+    buf = torch.full((B, Hq, Tq + 2, D + 8), 7.0, dtype=BF, device="cuda")
+    out = buf[:, :, 1:-1, :D].transpose(1, 2)
+    gkd.prefix_attention(q, kp, vp, ko, vo, out=out, **kw)
+    assert torch.equal(out, want)
+    out.fill_(7)
+    assert bool((buf == 7).all())
+
+
+def test_attention_shared_operands_and_no_keys(gkd):
+    """One query row and one set of own keys for all sequences (strides of
+    0), keys as values, and keys of no tokens."""
+    g = rng(13)
+    for P, Tq in ((70, 3), (1100, 3)):
+        q, kp, vp, ko, vo = attn_inputs(g, 1, Tq, 4, 2, 64, P, 50)
+        wide = [t.expand(6, *t.shape[1:]) for t in (q, ko, vo)]
+        dense = [t.contiguous() for t in wide]
+        assert torch.equal(gkd.prefix_attention(wide[0], kp, vp, wide[1], wide[2]),
+                           gkd.prefix_attention(dense[0], kp, vp, dense[1], dense[2]))
+        assert torch.equal(gkd.prefix_attention(dense[0], kp, kp, dense[1], dense[1]),
+                           gkd.prefix_attention(dense[0], kp, kp.clone(), dense[1], dense[1].clone()))
+        assert not bool(gkd.prefix_attention(q, kp[:0], vp[:0]).any())
+        assert not bool(gkd.prefix_attention(q, kp[:0], vp[:0], ko[:, :0], vo[:, :0]).any())
+        with pytest.raises(gkd.GkdError) as e:
+            gkd.prefix_attention(wide[0], kp, vp, out=wide[0])
+        assert e.value.status == 2
 
 
 def test_attention_large_scores_and_scales(gkd):

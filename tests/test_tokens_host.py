@@ -58,6 +58,8 @@ def lin(lib, x=A, ldx=64, w=A2, ldw=64, bias=None, res=None, ldr=0, M=4, N=32, K
     (dict(N=-1), SHAPE),
     (dict(K=0), SHAPE),
     (dict(M=1 << 26), SHAPE),
+    (dict(N=1 << 25, ldo=1 << 25), SHAPE),
+    (dict(M=1 << 18, N=1 << 18, ldo=1 << 18), SHAPE),      # M N >= 2^36
     (dict(ldx=63), SHAPE),
     (dict(ldw=0), SHAPE),                     # rows that repeat
     (dict(ldx=1 << 22), SHAPE),
@@ -136,6 +138,11 @@ def test_rope_rejects_operands(lib):
     assert rope(lib, k=heads(token=-8)) == SHAPE
     assert rope(lib, qo=heads(data=A + 1)) == ALIGN
     assert rope(lib, q=heads(data=A + 2), dtype=0) == ALIGN
+    # an output's elements have places of their own, an input's need not
+    for kw in (dict(batch=0), dict(token=0), dict(head=0)):
+        assert rope(lib, qo=heads(**kw)) == SHAPE and rope(lib, ko=heads(**kw)) == SHAPE
+        assert rope(lib, q=heads(**kw), freqs=None) == NULL
+    assert rope(lib, qo=heads(batch=0), B=1, freqs=None) == NULL
     assert rope(lib, B=0) == OK and rope(lib, T=0, Hk=0, no_k=True) == OK
 
 
@@ -159,6 +166,8 @@ def attn(lib, q=None, kp=None, vp=None, P=16, ko=None, vo=None, S=8, own_len=Non
     (dict(S=1 << 30), SHAPE),
     (dict(D=0), SHAPE),
     (dict(B=1 << 16, Tq=1 << 14), SHAPE),      # B Tq Hq >= 2^31
+    (dict(B=1 << 22, Tq=1), SHAPE),            # 2^23 groups of heads
+    (dict(B=1 << 14, Tq=16448, Hk=4), SHAPE),  # 129 tiles of each of 2^16
     (dict(D=96), UNSUP),
     (dict(Hk=3), UNSUP),
     (dict(scale=0.0), VALUE),
@@ -180,6 +189,10 @@ def test_attention_rejects_operands(lib):
         assert attn(lib, **{name: heads(head=-64)}) == SHAPE, name
     for name in ("kp", "vp", "ko", "vo"):
         assert attn(lib, **{name: heads(token=1 << 25)}) == SHAPE, name
+    for kw in (dict(batch=0), dict(token=0), dict(head=0)):
+        assert attn(lib, out=heads(**kw)) == SHAPE
+        assert attn(lib, q=heads(**kw), ko=heads(**kw), own_len=A + 2) == ALIGN
+    assert attn(lib, out=heads(head=0, token=64), Hq=1, Hk=1, own_len=A + 2) == ALIGN
     assert attn(lib, B=0) == OK and attn(lib, Tq=0, ws=None) == OK
 
 
