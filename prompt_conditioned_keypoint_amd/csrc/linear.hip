@@ -11,6 +11,14 @@
 //                        bound by reading w once.
 // The products run on v_mfma_f32_16x16x32_bf16 with w as the first operand,
 // so a lane ends with four adjacent columns of one row.
+//
+// Measured (a call, inputs that change from call to call; the card copies at
+// 5.08 TB/s):
+//   turn  36864 x 1024 x 4096, GELU             277 us, 1.12 PFLOP/s
+//   ring  19706 x 1024 x 1024, float32 residual  87 us, 0.48 PFLOP/s, 2.4 TB/s:
+//         2.4 rounds of workgroups in three, and their epilogues, 161 MB of
+//         them, come when no products are left to hide them
+//   few   37 x 1024 x 4096, GELU 6.8 us on the GPU; 1 x 1024 x 1024 4.1 us
 #include "gkd_device.hpp"
 #include "gkdtokens.h"
 #include "tokens_launch.hpp"

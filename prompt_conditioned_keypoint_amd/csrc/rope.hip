@@ -11,6 +11,10 @@
 // a float32 angle of 10^5 would be off by 2^-8 of a radian. It is reduced to
 // one turn there (phi / 2 pi minus the nearest whole number) and only the
 // rest, in [-1/2, 1/2], goes to float32 (2^-25 of a turn).
+//
+// Measured (the card copies at 5.08 TB/s): 2 x 18432 tokens, 40 heads of 128,
+// three axes, norm, bfloat16: 755 MB in 150 us, 5.0 TB/s; 64 x 581 tokens, 32
+// heads of 64: 305 MB in 61 us, 5.0 TB/s; 8 tokens 7.1 us on the GPU.
 #include "gkd_device.hpp"
 #include "tokens_launch.hpp"
 
