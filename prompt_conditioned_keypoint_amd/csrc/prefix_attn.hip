@@ -164,6 +164,17 @@ __device__ __forceinline__ void write_row(const PaParams& p, const TileWork& w, 
   for (int j = 0; j < D / 16; ++j) *reinterpret_cast<f32x4*>(p.po + at * D + 16 * j + 4 * g) = o[j];
 }
 
+// V's rows lie in LDS with piece c of key row r at place c ^ v_turn(r). A
+// transposing read takes 16 bytes' halves of pieces 2 j and 2 j + 1 of eight
+// keys at a time: with rows of 256 bytes (D = 128) these meet in different
+// banks only if keys differ by an even number of pieces (turned by r like K's
+// rows, a third of the LDS cycles were conflicts); rows of 128 bytes alternate
+// between the halves of the banks by themselves.
+template <int D>
+__device__ __forceinline__ int v_turn(int r) {
+  return (D == 128 ? 2 * r : r) & (D / 8 - 1);
+}
+
 // max over the four 16-lane groups of a wave
 __device__ __forceinline__ float group_max(float x) {
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -232,7 +243,7 @@ struct ThinTile {
       for (int i = 0; i < kLoads; ++i) {
         const int r = i * kBlkRows + lr;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(vb, (lds_void*)(sV + i * 1024), 16,
-                                                 (int)(r * vt + 16 * ((lane % kPieces) ^ (r & (kPieces - 1)))), 0, 0, 0);
+                                                 (int)(r * vt + 16 * ((lane % kPieces) ^ v_turn<D>(r))), 0, 0, 0);
       }
       bf16x8 kf[2][kDK];
 #pragma unroll
@@ -303,7 +314,7 @@ struct ThinTile {
       const bf16x8 pf = frag(u32x4{pk[0][0], pk[0][1], pk[1][0], pk[1][1]});
 #pragma unroll
       for (int j = 0; j < kND; ++j) {
-        const unsigned char* v = sV + vkey * D * 2 + (((2 * j + ((fr & 3) >> 1)) ^ (vkey & (kPieces - 1))) << 4) + (fr & 1) * 8;
+        const unsigned char* v = sV + vkey * D * 2 + (((2 * j + ((fr & 3) >> 1)) ^ v_turn<D>(vkey)) << 4) + (fr & 1) * 8;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)v);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(v + 16 * D * 2));
         const u32x2 l2 = __builtin_bit_cast(u32x2, lo), h2 = __builtin_bit_cast(u32x2, hi);
@@ -431,7 +442,7 @@ struct WideTile {
     // this lane's piece of the wave's first load: key row lr, piece (place ^
     // row), so that the 16 rows of an operand read lie in different banks
     const int lr = wr * kBlkRows + lane / kPieces;
-    const int lp = 16 * ((lane % kPieces) ^ (lr & (kPieces - 1)));
+    const int lp = 16 * ((lane % kPieces) ^ (lr & (kPieces - 1))), vp = 16 * ((lane % kPieces) ^ v_turn<D>(lr));
     auto load = [&](int c, int buf) {
       if (c == nprefix) walk = own;
       const int keys = min(walk.left, KC);
@@ -445,7 +456,7 @@ struct WideTile {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i, off += (uint32_t)walk.kt * (WR * kBlkRows * 2))
         __builtin_amdgcn_raw_ptr_buffer_load_lds(kb, (lds_void*)(st + i * WR * 1024), 16, (int)off, 0, 0, 0);
-      off = (uint32_t)lr * (uint32_t)walk.vt * 2u + lp;
+      off = (uint32_t)lr * (uint32_t)walk.vt * 2u + vp;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i, off += (uint32_t)walk.vt * (WR * kBlkRows * 2))
         __builtin_amdgcn_raw_ptr_buffer_load_lds(vb, (lds_void*)(st + kMat + i * WR * 1024), 16, (int)off, 0, 0, 0);
@@ -462,7 +473,7 @@ struct WideTile {
     const int vkey = 4 * g + (fr >> 2);
 #pragma unroll
     for (int j = 0; j < kND; ++j)
-      vat[j] = kMat + vkey * D * 2 + (((2 * j + ((fr & 3) >> 1)) ^ (vkey & (kPieces - 1))) << 4) + (fr & 1) * 8;
+      vat[j] = kMat + vkey * D * 2 + (((2 * j + ((fr & 3) >> 1)) ^ v_turn<D>(vkey)) << 4) + (fr & 1) * 8;
     bf16x8 ones;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ones[e] = static_cast<__bf16>(1.f);
