@@ -731,7 +731,7 @@ __global__ __launch_bounds__(512, 4) void prefix_thin_kernel(PaParams p) {
 
 // Joins a row's partial results, D / 4 lanes a row: kGroups groups of slots
 // side by side (four loads of each in flight together), then the groups in
-// order. Up to four slots take one group.
+// order. Up to eight slots take one group.
 template <int D, int kGroups>
 __global__ __launch_bounds__(256) void prefix_join_kernel(PaParams p) {
   constexpr int LPR = D / 4, kRowsWg = 256 / (LPR * kGroups);
@@ -804,6 +804,15 @@ int parts_for(long long n, long long items, long long want, long long least) {
   return (int)(parts < 1 ? 1 : parts);
 }
 
+// Parts for wide tiles within sequences, 512 of which run at a time: as many
+// as fit into one round, if that is filled to four fifths, else about a round
+// and a half, and never a little over one: 2 x 300 rows of 16 heads of 128
+// behind 9000 keys, 96 tiles, take 71 us in 5 parts and 88 in 6.
+int wide_parts(long long n, long long items) {
+  const long long fit = 512 / (items > 0 ? items : 1);
+  return parts_for(n, items, fit * items * 5 >= 512 * 4 ? fit * items : 768, 256);
+}
+
 Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   Plan pl{};
   const int G = Hq / Hk;
@@ -825,7 +834,7 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   if (!packed) {
     // every tile stays in its sequence and takes prefix and own keys
     const int wide = RS > 16, tiles = B * cdiv(RS, wide ? 128 : 16);
-    const int parts = wide ? parts_for((long long)P + S, (long long)tiles * Hk, 512, 256)
+    const int parts = wide ? wide_parts((long long)P + S, (long long)tiles * Hk)
                            : parts_for((long long)P + S, (long long)tiles * Hk, 256, (long long)P + S <= 1024 ? 1024 : 512);
     pl.first = list(wide, 1, 2, tiles, parts, 0);
     pl.slots = parts;
@@ -834,9 +843,11 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   // the prefix for the rows of all sequences together, own keys apart
   // (beside thin items one wide one a CU: with 512 the 48 sequences with 1024
   // own keys behind 32768 take 102 instead of 89 us; but where own keys are
-  // few, 384: 16 sequences with 256 behind 65536 61 instead of 69 us)
+  // few, 384: 16 sequences with 256 behind 65536 61 instead of 69 us; among
+  // wide ones half as many again as the CUs hold, which fill each other's gaps:
+  // 37 x 80 rows of 8 heads of 128 behind 8192 125 us, with 512 149, with 1024 137)
   const int wide = RS > 16, tiles = cdiv(RT, 128);
-  const int parts = parts_for(P, (long long)tiles * Hk, wide ? 512 : P / 64 >= S ? 384 : 256, 256);
+  const int parts = parts_for(P, (long long)tiles * Hk, wide ? 768 : P / 64 >= S ? 384 : 256, 256);
   pl.first = list(1, 0, 0, tiles, parts, 0);
   const int own_tiles = B * cdiv(RS, wide ? 128 : 16);
   pl.second = list(wide, 1, 1, own_tiles, parts_for(S, (long long)own_tiles * Hk, 256, 256), parts);
@@ -860,7 +871,7 @@ hipError_t run(const PaParams& p, const Plan& pl, hipStream_t st) {
   if (e != hipSuccess || pl.slots == 1) return e;
   const long long rows = (long long)p.Hk * p.RT;
   constexpr int many = 256 / D, few = 1024 / D;  // rows a workgroup
-  if (pl.slots > 4)
+  if (pl.slots > 8)
     hipLaunchKernelGGL((prefix_join_kernel<D, 4>), dim3((unsigned)cdiv(rows, many)), dim3(256), 0, st, p);
   else
     hipLaunchKernelGGL((prefix_join_kernel<D, 1>), dim3((unsigned)cdiv(rows, few)), dim3(256), 0, st, p);
