@@ -396,9 +396,9 @@ _current_device = torch._C._cuda_getDevice
 def _place(t, name):
     """Device index of a GPU tensor, which must be the current device (where
     kernels are launched)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
     dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
     if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is "
                          f"cuda:{_current_device()}")
@@ -406,19 +406,29 @@ def _place(t, name):
 
 
 def _beside(dev, t, name):
-    if not t.is_cuda or t.get_device() != dev:
+    if t.get_device() != dev or not t.is_cuda:
         raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _dense(dev, t, name, dtype, shape):
+    """The address of a contiguous tensor of this type and shape."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _dev(t, name, dtype, len(shape))
+        _beside(dev, t, name)
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _heads(dev, t, name, dtype, ndim=4):
     """A [B,T,H,D] (ndim 3: [T,H,D]) operand with any strides but adjacent
     head elements, as the four fields of gkd_heads."""
-    _beside(dev, t, name)
+    if t.get_device() != dev or not t.is_cuda:
+        _beside(dev, t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     st = t.stride()
+    if len(st) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a head must be adjacent")
     if ndim == 4:
@@ -498,7 +508,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
     if out_dtype != bf16 and out_dtype != torch.float32:
         raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        out = x.new_empty(shape) if out_dtype == bf16 else x.new_empty(shape, dtype=out_dtype)
         ldo = N
     else:
         _beside(dev, out, "out")
@@ -513,10 +523,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
             raise ValueError(f"residual must be {tuple(shape)} of {out_dtype}")
         rp, ldr = residual.data_ptr(), _row_stride(residual, "residual")
     if bias is not None:
-        _beside(dev, bias, "bias")
-        if bias.shape != (N,) or bias.dtype != bf16 or not bias.is_contiguous():
-            raise ValueError("bias must be [N] bfloat16, contiguous")
-        bp = bias.data_ptr()
+        bp = _dense(dev, bias, "bias", bf16, (N,))
     ldx, ldw = _row_stride(x, "x"), _row_stride(weight, "weight")
     ws, ws_bytes = _workspace(workspace, lib.gkd_linear_workspace_size(M, N, K, ldx, ldw), dev)
     status = lib.gkd_linear(x.data_ptr(), ldx, weight.data_ptr(), ldw, bp, rp, ldr, M, N, K, code,
@@ -549,35 +556,33 @@ def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_w
             raise ValueError(f"k must be [B,T,Hk,D], got {tuple(k.shape)}")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _dev(pos, "pos", torch.float32)
-    _dev(freqs, "freqs", torch.float32, 2)
-    _beside(dev, pos, "pos")
-    _beside(dev, freqs, "freqs")
+    if freqs.dim() != 2:
+        raise ValueError(f"freqs must be [n_axes, rot/2], got {tuple(freqs.shape)}")
     A, half = freqs.shape
-    if pos.shape != (B, T, A) and pos.shape != (T, A):
-        raise ValueError(f"pos must be [T,n_axes] or [B,T,n_axes], got {tuple(pos.shape)}")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _dev(w, name, dtype, 1)
-            _beside(dev, w, name)
-            if w.shape[0] != D:
-                raise ValueError(f"{name} must be [D]")
+    pf = _dense(dev, freqs, "freqs", torch.float32, (A, half))
+    own_pos = pos.dim() == 3
+    pp = _dense(dev, pos, "pos", torch.float32, (B, T, A) if own_pos else (T, A))
+    pwq = None if q_weight is None else _dense(dev, q_weight, "q_weight", dtype, (D,))
+    pwk = None if k_weight is None else _dense(dev, k_weight, "k_weight", dtype, (D,))
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, D), dtype=dtype, device=q.device)
-    hqo = _heads(dev, q_out, "q_out", dtype)
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
+        q_out = q.new_empty((B, T, Hq, D))
+        hqo = (q_out.data_ptr(), T * Hq * D, Hq * D, D)
+    else:
+        hqo = _heads(dev, q_out, "q_out", dtype)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
     if k is not None:
         if k_out is None:
-            k_out = torch.empty((B, T, Hk, D), dtype=dtype, device=q.device)
-        hko = _heads(dev, k_out, "k_out", dtype)
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
+            k_out = q.new_empty((B, T, Hk, D))
+            hko = (k_out.data_ptr(), T * Hk * D, Hk * D, D)
+        else:
+            hko = _heads(dev, k_out, "k_out", dtype)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
     heads = _Heads4(*hq, *hk, *hqo, *hko)
     at = ctypes.addressof(heads)
     status = lib.gkd_qk_norm_rope(at, Hq, at + _HEADS_BYTES if Hk else None, Hk, B, T, D,
-                                  pos.data_ptr(), T * A if pos.dim() == 3 else 0, A,
-                                  freqs.data_ptr(), 2 * half, _ptr(q_weight), _ptr(k_weight), eps,
+                                  pp, T * A if own_pos else 0, A, pf, 2 * half, pwq, pwk, eps,
                                   code, GKD_ROPE_INTERLEAVED if interleaved else 0,
                                   at + 2 * _HEADS_BYTES, at + 3 * _HEADS_BYTES if Hk else None,
                                   _raw_stream(dev))
@@ -627,19 +632,11 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
             raise ValueError("k_own and v_own must be [B,S,Hk,D]")
     if Hk is None:
         raise ValueError("give prefix keys, own keys or both")
-    for t, name in ((own_len, "own_len"), (q_len, "q_len")):
-        if t is not None:
-            _dev(t, name, torch.int32, 1)
-            _beside(dev, t, name)
-            if t.shape[0] != B:
-                raise ValueError(f"{name} must be [B]")
-    if own_mask is not None:
-        _dev(own_mask, "own_mask", torch.uint8, 2)
-        _beside(dev, own_mask, "own_mask")
-        if own_mask.shape != (B, S):
-            raise ValueError("own_mask must be [B,S]")
+    pol = None if own_len is None else _dense(dev, own_len, "own_len", torch.int32, (B,))
+    pql = None if q_len is None else _dense(dev, q_len, "q_len", torch.int32, (B,))
+    pm = None if own_mask is None else _dense(dev, own_mask, "own_mask", torch.uint8, (B, S))
     if out is None:
-        out = torch.empty((B, Tq, Hq, D), dtype=bf16, device=q.device)
+        out = q.new_empty((B, Tq, Hq, D))
     ho = _heads(dev, out, "out", bf16)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -649,7 +646,7 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
     at = ctypes.addressof(heads)
     n = _HEADS_BYTES
     status = lib.gkd_prefix_attention(at, at + n, at + 2 * n, P, at + 3 * n, at + 4 * n, S,
-                                      _ptr(own_len), _ptr(q_len), _ptr(own_mask), B, Tq, Hq, Hk, D,
+                                      pol, pql, pm, B, Tq, Hq, Hk, D,
                                       D ** -0.5 if scale is None else scale, 1,
                                       GKD_ATTN_CAUSAL if causal else 0, at + 5 * n,
                                       None if ws is None else ws.data_ptr(), ws_bytes,
