@@ -647,7 +647,16 @@ __device__ __forceinline__ void run_item(const PaParams& p, const List& list, un
   w.packed = !list.seq;
   const int* cum = nullptr;
   if (list.seq) {
-    const int per = tiles / p.B, b = tile / per, first = (tile - b * per) * T::kRows;
+    const int per = tiles / p.B;
+    int b = tile / per, first = (tile - b * per) * T::kRows;
+    if (p.causal) {
+      // every sequence's last rows, which see the most keys, come first, and the
+      // short ones fill the gaps at the end (8 x 1024 rows, 16 heads of 128, no
+      // prefix: 66 -> 54 us; behind 8192 1139 -> 1083)
+      const int turned = tiles - 1 - tile;
+      b = turned % p.B;
+      first = turned / p.B * T::kRows;
+    }
     w.row0 = b * p.RS + first;
     w.n = min(query_length(p, b) * p.G - first, T::kRows);
     if (list.keys != 0) w.b = b;
