@@ -15,9 +15,9 @@
 // Measured (a call, inputs that change from call to call; the card copies at
 // 5.08 TB/s):
 //   turn  36864 x 1024 x 4096, GELU             277 us, 1.12 PFLOP/s
-//   ring  19706 x 1024 x 1024, float32 residual  87 us, 0.48 PFLOP/s, 2.4 TB/s:
-//         2.4 rounds of workgroups in three, and their epilogues, 161 MB of
-//         them, come when no products are left to hide them
+//   turn and ring  19706 x 1024 x 1024, float32 residual  74 us, 0.56 PFLOP/s,
+//         2.8 TB/s: one round of 256 x 256 tiles and 3322 rows apart; their
+//         epilogues, 161 MB of them, come when no products are left to hide them
 //   few   37 x 1024 x 4096, GELU 6.8 us on the GPU; 1 x 1024 x 1024 4.1 us
 #include "gkd_device.hpp"
 #include "gkdtokens.h"
@@ -751,6 +751,54 @@ hipError_t run_turn(const LinParams& p, hipStream_t st) {
   return hipGetLastError();
 }
 
+// The kernel follows from how many tiles there are for the 256 CUs. Measured
+// (us, this choice / the next best): 222 x 58 x 4096 19 / 31, 700 x 1209 x
+// 2384 15 / 22 (64 x 64 tiles); 1425 x 777 x 646 15 / 18 (128 x 64); 3825 x
+// 610 x 3616 40 / 43, 8049 x 260 x 2952 35 / 38 (128 x 128, four stages);
+// 28607 x 2031 x 224 72 / 80, 35266 x 476 x 96 17 / 19 (128 x 128, two
+// stages, two workgroups a CU).
+hipError_t run_rows(const LinParams& p, hipStream_t st) {
+  if (p.M <= 16) return run_few<1>(p, st);
+  if (p.M <= 32) return run_few<2>(p, st);
+  if (p.M <= 64) return run_few<4>(p, st);
+  auto tiles = [&](long long m, int bm, int bn) { return ((m + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
+  if (tiles(p.M, 64, 64) <= 256) return run_ring<64, 64, 2, 2, 2, 4>(p, st);
+  if (tiles(p.M, 128, 64) <= 256) return run_ring<128, 64, 4, 2, 1, 3>(p, st);
+  if (tiles(p.M, 128, 128) <= 256) return run_ring<128, 128, 2, 4, 1, 4>(p, st);
+  // Beyond that the 256 x 256 kernel takes 1.35 us a step and 10 us a tile, all
+  // CUs in step, and the 128 x 128 one 0.95 us and 7 us for each 512 tiles, one
+  // round of smaller tiles 1.2 us and 5: 15161 x 3143 x 1512 168 against 198,
+  // 4096 x 4096 x 1024 32 against 39. Rows beyond the 256 x 256 tiles' last
+  // whole round go to a launch of their own where that is the least: 19706 x
+  // 1024 x 1024 78 against 92 us (float32 with residual), 8917 x 3552 x 2079
+  // 135 against 185.
+  const int nk = (p.K + kBK - 1) / kBK;
+  auto ring = [&](long long m) {
+    const long long n = tiles(m, 128, 128);
+    return n <= 256 ? 1.2 * nk + 5.0 : (double)((n + 511) / 512) * (0.95 * nk + 7.0);
+  };
+  if (nk >= kTurnMinSteps) {
+    const double round = 1.35 * nk + 10.0;
+    const long long n = tiles(p.M, 256, 256), whole = n / kTurnCus;
+    const double turn = (double)((n + kTurnCus - 1) / kTurnCus) * round, all = ring(p.M);
+    const long long head = whole * kTurnCus / tiles(1, 256, 256) * 256;  // rows of the whole rounds
+    if (head > 0 && head < p.M && (double)whole * round + ring(p.M - head) < 0.95 * (turn < all ? turn : all)) {
+      LinParams first = p, rest = p;
+      first.M = (int)head;
+      const hipError_t e = run_turn(first, st);
+      if (e != hipSuccess) return e;
+      const long long size = p.out_f32 ? 4 : 2;
+      rest.M = (int)(p.M - head);
+      rest.x = p.x + head * p.ldx;
+      if (p.res) rest.res = static_cast<const uint8_t*>(p.res) + head * p.ldr * size;
+      rest.out = static_cast<uint8_t*>(p.out) + head * p.ldo * size;
+      return run_rows(rest, st);
+    }
+    if (turn <= all) return run_turn(p, st);
+  }
+  return run_ring<128, 128, 4, 2, 1, 2>(p, st);
+}
+
 }  // namespace
 
 size_t linear_workspace_bytes(int M, int N, int K, long long ldx, long long ldw) {
@@ -797,28 +845,7 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  // The kernel follows from how many tiles there are for the 256 CUs. Measured
-  // (us, this choice / the next best): 222 x 58 x 4096 19 / 31, 700 x 1209 x
-  // 2384 15 / 22 (64 x 64 tiles); 1425 x 777 x 646 15 / 18 (128 x 64); 3825 x
-  // 610 x 3616 40 / 43, 8049 x 260 x 2952 35 / 38 (128 x 128, four stages);
-  // 28607 x 2031 x 224 72 / 80, 35266 x 476 x 96 17 / 19 (128 x 128, two
-  // stages, two workgroups a CU).
-  if (p.M <= 16) return run_few<1>(p, st);
-  if (p.M <= 32) return run_few<2>(p, st);
-  if (p.M <= 64) return run_few<4>(p, st);
-  auto tiles = [&](int bm, int bn) { return (long long)((p.M + bm - 1) / bm) * ((p.N + bn - 1) / bn); };
-  if (tiles(64, 64) <= 256) return run_ring<64, 64, 2, 2, 2, 4>(p, st);
-  if (tiles(128, 64) <= 256) return run_ring<128, 64, 4, 2, 1, 3>(p, st);
-  if (tiles(128, 128) <= 256) return run_ring<128, 128, 2, 4, 1, 4>(p, st);
-  // Beyond that the 256 x 256 kernel takes 1.35 us a step and 10 us a tile, all
-  // CUs in step, and the 128 x 128 one 0.95 us and 7 us for each 512 tiles:
-  // 19706 x 1024 x 1024 (float32 with residual) 76 against 68, 15161 x 3143 x
-  // 1512 168 against 198, 4096 x 4096 x 1024 32 against 39.
-  const int nk = (p.K + kBK - 1) / kBK;
-  const double turn = (double)((tiles(256, 256) + kTurnCus - 1) / kTurnCus) * (1.35 * nk + 10.0);
-  const double ring = (double)tiles(128, 128) / 512.0 * (0.95 * nk + 7.0);
-  if (nk >= kTurnMinSteps && turn <= ring) return run_turn(p, st);
-  return run_ring<128, 128, 4, 2, 1, 2>(p, st);
+  return run_rows(p, st);
 }
 
 }  // namespace gkd

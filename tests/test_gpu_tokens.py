@@ -113,6 +113,8 @@ def test_linear_large(gkd, M, K, N):
     (2100, 40, 1101, "none", BF, True),
     (1025, 72, 1023, "relu", F32, True),      # 128 x 64
     (20000, 24, 300, "none", BF, True),       # 128 x 128, two workgroups a CU
+    (4130, 328, 4090, "none", F32, True),     # a whole round of 256 x 256 tiles and 34 rows apart
+    (4470, 520, 4096, "gelu", BF, True),      # and 374 rows apart
 ])
 def test_linear_tile_sizes(gkd, M, K, N, act, out, residual):
     check_linear(gkd, M, K, N, act, out=out, residual=residual, seed=K)
