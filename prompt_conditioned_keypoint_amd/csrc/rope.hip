@@ -13,8 +13,8 @@
 // rest, in [-1/2, 1/2], goes to float32 (2^-25 of a turn).
 //
 // Measured (the card copies at 5.08 TB/s): 2 x 18432 tokens, 40 heads of 128,
-// three axes, norm, bfloat16: 755 MB in 150 us, 5.0 TB/s; 64 x 581 tokens, 32
-// heads of 64: 305 MB in 61 us, 5.0 TB/s; 8 tokens 7.1 us on the GPU.
+// three axes, norm, bfloat16: 755 MB in 142 us, 5.3 TB/s; 64 x 581 tokens, 32
+// heads of 64: 305 MB in 61 us, 5.0 TB/s; 8 tokens 5.7 us on the GPU.
 #include "gkd_device.hpp"
 #include "tokens_launch.hpp"
 
@@ -108,15 +108,14 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   const int np = (p.D + 2 * N - 1) / (2 * N), npair = np * N;
   const long long tok0 = p.first + (long long)blockIdx.x * p.tt;
   const int nt = (int)min((long long)p.tt, p.n_tok - tok0);
-
-  for (int i = tid; i < nt * npair; i += 256) {
-    const int t = i / npair, pr = i - t * npair;
-    const long long tok = tok0 + t, b = tok / p.T, tb = tok - b * p.T;
-    float c = 1.f, s = 0.f;
-    if (pr < p.half) rope_angle(p, p.pos + b * p.pos_batch + tb * p.n_axes, pr, c, s);
-    cs[(2 * t) * npair + pr] = c;
-    cs[(2 * t + 1) * npair + pr] = s;
-  }
+  const long long seq0 = tok0 / p.T;
+  const uint32_t at0 = (uint32_t)(tok0 - seq0 * p.T);
+  // sequence of the workgroup's token t, and its place there
+  auto place = [&](int t, long long& b, uint32_t& tb) {
+    const uint32_t at = at0 + (uint32_t)t, over = at / (uint32_t)p.T;
+    b = seq0 + over;
+    tb = at - over * (uint32_t)p.T;
+  };
 
   const int j = tid & (LP - 1);
   // the pair's two pieces (element offsets; b1: the second one exists)
@@ -141,6 +140,8 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   const u32x4 z4 = {0u, 0u, 0u, 0u};
   u32x4 wq0 = z4, wq1 = z4, wk0 = z4, wk1 = z4;  // gains, as stored
   auto gain = [&](const void* w, int e, bool in) {
+    if ((reinterpret_cast<uintptr_t>(w) & 15u) == 0)
+      return in ? *reinterpret_cast<const u32x4*>(static_cast<const T*>(w) + e) : z4;
     T t[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) t[i] = in ? static_cast<const T*>(w)[e + i] : T(0);
@@ -150,22 +151,51 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   };
   if (p.wq) wq0 = gain(p.wq, e0, b0), wq1 = gain(p.wq, e1, b1);
   if (p.wk) wk0 = gain(p.wk, e0, b0), wk1 = gain(p.wk, e1, b1);
-  __syncthreads();
 
+  // A head is on its way while the one before is worked on, the first one
+  // while the table is made (kLoose: 54 instead of 51 us at 9 x 2193 tokens of
+  // 16 heads of 96, so there each head is loaded when it is due).
   constexpr int kStep = 256 / LP;  // heads a round
   const int units = nt * p.H;
-  for (int u = tid / LP; u < units; u += kStep) {
-    const int t = u / p.H, hh = u - t * p.H;
+  u32x4 next0 = z4, next1 = z4;
+  T* next_dst = nullptr;
+  auto fetch = [&](int u) {
+    const int t = (int)((uint32_t)u / (uint32_t)p.H), hh = u - t * p.H;
     const bool isk = hh >= p.Hq;
     const int h = isk ? hh - p.Hq : hh;
-    const long long tok = tok0 + t, b = tok / p.T, tb = tok - b * p.T;
+    long long b;
+    uint32_t tb;
+    place(t, b, tb);
     const Heads& in = isk ? p.k : p.q;
     const Heads& out = isk ? p.ko : p.qo;
     const T* src = static_cast<const T*>(in.p) + b * in.b + tb * in.t + h * in.h;
-    T* dst = static_cast<T*>(out.p) + b * out.b + tb * out.t + h * out.h;
+    next_dst = static_cast<T*>(out.p) + b * out.b + tb * out.t + h * out.h;
+    next0 = b0 ? *reinterpret_cast<const u32x4*>(src + e0) : z4;
+    next1 = b1 ? *reinterpret_cast<const u32x4*>(src + e1) : z4;
+  };
+  if (PAIRS != kLoose && tid / LP < units) fetch(tid / LP);
+
+  for (int i = tid; i < nt * npair; i += 256) {
+    const int t = (int)((uint32_t)i / (uint32_t)npair), pr = i - t * npair;
+    long long b;
+    uint32_t tb;
+    place(t, b, tb);
+    float c = 1.f, s = 0.f;
+    if (pr < p.half) rope_angle(p, p.pos + b * p.pos_batch + (long long)tb * p.n_axes, pr, c, s);
+    cs[(2 * t) * npair + pr] = c;
+    cs[(2 * t + 1) * npair + pr] = s;
+  }
+  __syncthreads();
+
+  for (int u = tid / LP; u < units; u += kStep) {
+    const int t = (int)((uint32_t)u / (uint32_t)p.H);
+    const bool isk = u - t * p.H >= p.Hq;
+    if (PAIRS == kLoose) fetch(u);
+    T* dst = next_dst;
     float x0[N], x1[N];
-    Piece<T>::unpack(b0 ? *reinterpret_cast<const u32x4*>(src + e0) : z4, x0);
-    Piece<T>::unpack(b1 ? *reinterpret_cast<const u32x4*>(src + e1) : z4, x1);
+    Piece<T>::unpack(next0, x0);
+    Piece<T>::unpack(next1, x1);
+    if (PAIRS != kLoose && u + kStep < units) fetch(u + kStep);
     if ((isk ? p.wk : p.wq) != nullptr) {
       float ss = 0.f;
 #pragma unroll
@@ -308,9 +338,13 @@ template <typename T, int LP>
 hipError_t run_pieces(RopeParams p, int pairs, hipStream_t st) {
   constexpr int N = Piece<T>::N;
   const int npair = (p.D + 2 * N - 1) / (2 * N) * N;
-  // about 1024 pairs of pieces a workgroup (four rounds of its lanes), while
-  // its table stays within 16 KB of LDS
+  // about 1024 pairs of pieces a workgroup (four rounds of its lanes), fewer
+  // where that leaves less than four workgroups a CU (3 x 1001 tokens of 8
+  // heads of 96 in float32 9.0 us, with 1024 10.5; 4 x 300 of 5 heads of 128
+  // 5.6, 10.2), while its table stays within 16 KB of LDS
+  const long long round = 256 / ((long long)p.H * LP);
   long long tt = 1024 / ((long long)p.H * LP);
+  if (tt > p.n_tok / 1024) tt = p.n_tok / 1024 > round ? p.n_tok / 1024 : round;
   tt = tt < 1 ? 1 : tt;
   const long long most = 16384 / (8 * npair);
   if (tt > most) tt = most;
