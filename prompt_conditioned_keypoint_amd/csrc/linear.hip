@@ -14,7 +14,7 @@
 //
 // Measured (a call, inputs that change from call to call; the card copies at
 // 5.08 TB/s):
-//   turn  36864 x 1024 x 4096, GELU             277 us, 1.12 PFLOP/s
+//   turn  36864 x 1024 x 4096, GELU             280 us, 1.10 PFLOP/s
 //   turn and ring  19706 x 1024 x 1024, float32 residual  74 us, 0.56 PFLOP/s,
 //         2.8 TB/s: one round of 256 x 256 tiles and 3322 rows apart; their
 //         epilogues, 161 MB of them, come when no products are left to hide them

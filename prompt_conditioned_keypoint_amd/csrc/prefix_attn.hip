@@ -19,13 +19,13 @@
 //
 // Measured (bfloat16, a call, inputs that change from call to call):
 //   8 x 1024 queries, 32 heads of 128 (8 of keys), causal, behind 8192 keys:
-//     1.12 ms, 1.04 PFLOP/s. A wave's chunk is 68 matrix instructions and the
+//     1.09 ms, 1.07 PFLOP/s. A wave's chunk is 68 matrix instructions and the
 //     exponents between them; two waves a SIMD take turns with both.
 //   48 x 1 query, the same heads, 1024 own keys at most, behind 32768: 82 us,
 //     287 MB at 3.5 TB/s. Up to 128 rows it is the reading (32 sequences: 52 us,
 //     4.5 TB/s); these 192 are two tiles, which read the prefix through L2 and
 //     take its products twice.
-//   37 x 80 queries at most, 16 heads of 64, behind 2304: 39 us, 35 of them the
+//   37 x 80 queries at most, 16 heads of 64, behind 2304: 40 us, 35 of them the
 //     products' kernel; a lone query behind 576 keys 8 us on the GPU.
 #include "gkd_device.hpp"
 #include "tokens_launch.hpp"
