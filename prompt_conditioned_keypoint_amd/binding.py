@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 
 import torch
 
@@ -396,8 +398,8 @@ _current_device = torch._C._cuda_getDevice
 def _place(t, name):
     """Device index of a GPU tensor, which must be the current device (where
     kernels are launched)."""
-    dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
+    dev = t.get_device()  # -1 without a GPU's memory
+    if dev < 0:
         raise ValueError(f"{name} must be a GPU tensor")
     if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is "
@@ -406,7 +408,7 @@ def _place(t, name):
 
 
 def _beside(dev, t, name):
-    if t.get_device() != dev or not t.is_cuda:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
@@ -422,7 +424,7 @@ def _dense(dev, t, name, dtype, shape):
 def _heads(dev, t, name, dtype, ndim=4):
     """A [B,T,H,D] (ndim 3: [T,H,D]) operand with any strides but adjacent
     head elements, as the four fields of gkd_heads."""
-    if t.get_device() != dev or not t.is_cuda:
+    if t.get_device() != dev:
         _beside(dev, t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -437,8 +439,20 @@ def _heads(dev, t, name, dtype, ndim=4):
 
 
 _NO_HEADS = (0, 0, 0, 0)
-_Heads4, _Heads6 = ctypes.c_int64 * 16, ctypes.c_int64 * 24  # four, six gkd_heads
 _HEADS_BYTES = ctypes.sizeof(GkdHeads)
+_pack4, _pack6 = struct.Struct("16q").pack_into, struct.Struct("24q").pack_into  # gkd_heads
+
+
+class _Records(threading.local):
+    """Each thread's place for a call's gkd_heads, which are read before the
+    call returns."""
+
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(6 * _HEADS_BYTES)
+        self.at = ctypes.addressof(self.buf)
+
+
+_records = _Records()
 
 
 def _workspace(workspace, need, dev):
@@ -453,7 +467,10 @@ def _workspace(workspace, need, dev):
 
 def _row_stride(t, name):
     """Row stride of a [..., n] tensor whose rows are evenly spaced."""
-    shape, st = t.shape, t.stride()
+    shape = t.shape
+    if t.is_contiguous():
+        return shape[-1]
+    st = t.stride()
     if shape[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name}: the elements of a row must be adjacent")
     if len(shape) == 2:
@@ -487,7 +504,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
     linear_workspace_size() bytes (allocated here when None)."""
     lib = _lib or load()
     dev = _place(x, "x")
-    _beside(dev, weight, "weight")
+    if weight.get_device() != dev:
+        _beside(dev, weight, "weight")
     bf16 = torch.bfloat16
     if x.dtype != bf16 or weight.dtype != bf16:
         raise TypeError(f"x and weight must be bfloat16, got {x.dtype} and {weight.dtype}")
@@ -511,14 +529,16 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
         out = x.new_empty(shape) if out_dtype == bf16 else x.new_empty(shape, dtype=out_dtype)
         ldo = N
     else:
-        _beside(dev, out, "out")
+        if out.get_device() != dev:
+            _beside(dev, out, "out")
         if out.shape != shape or out.dtype != out_dtype:
             raise ValueError(f"out must be {tuple(shape)} of {out_dtype}")
         ldo = _row_stride(out, "out")
     rp = bp = None
     ldr = 0
     if residual is not None:
-        _beside(dev, residual, "residual")
+        if residual.get_device() != dev:
+            _beside(dev, residual, "residual")
         if residual.shape != shape or residual.dtype != out_dtype:
             raise ValueError(f"residual must be {tuple(shape)} of {out_dtype}")
         rp, ldr = residual.data_ptr(), _row_stride(residual, "residual")
@@ -579,8 +599,9 @@ def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_w
             hko = _heads(dev, k_out, "k_out", dtype)
             if k_out.shape != k.shape:
                 raise ValueError("k_out must have k's shape")
-    heads = _Heads4(*hq, *hk, *hqo, *hko)
-    at = ctypes.addressof(heads)
+    rec = _records
+    at = rec.at
+    _pack4(rec.buf, 0, *hq, *hk, *hqo, *hko)
     status = lib.gkd_qk_norm_rope(at, Hq, at + _HEADS_BYTES if Hk else None, Hk, B, T, D,
                                   pp, T * A if own_pos else 0, A, pf, 2 * half, pwq, pwk, eps,
                                   code, GKD_ROPE_INTERLEAVED if interleaved else 0,
@@ -642,8 +663,9 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
         raise ValueError("out must have q's shape")
     ws, ws_bytes = _workspace(workspace, lib.gkd_prefix_attention_workspace_size(
         B, Tq, Hq, Hk, D, P, S), dev)
-    heads = _Heads6(*hq, *kp, *vp, *ko, *vo, *ho)
-    at = ctypes.addressof(heads)
+    rec = _records
+    at = rec.at
+    _pack6(rec.buf, 0, *hq, *kp, *vp, *ko, *vo, *ho)
     n = _HEADS_BYTES
     status = lib.gkd_prefix_attention(at, at + n, at + 2 * n, P, at + 3 * n, at + 4 * n, S,
                                       pol, pql, pm, B, Tq, Hq, Hk, D,

@@ -193,18 +193,18 @@ __device__ __forceinline__ float group_max(float x) {
 template <int D, int WK>
 struct ThinTile {
   static constexpr int KC = 32, kRows = 16;
+  static constexpr bool kPacked = false;  // thin tiles stay within a sequence
   static constexpr int kPieces = D / 8, kDK = D / 32, kND = D / 16;
   static constexpr int kMat = KC * D * 2;
   static constexpr int kJoin = (WK - 1) * (kND * 1024 + 512);  // the waves' results at the end
   static constexpr int kLds = WK * kMat > kJoin ? WK * kMat : kJoin;
   static constexpr int kLoads = kMat / 1024, kBlkRows = 64 / kPieces;
 
-  static __device__ __forceinline__ void run(const PaParams& p, const TileWork& w, unsigned char* lds, const int* cum) {
+  static __device__ __forceinline__ void run(const PaParams& p, const TileWork& w, unsigned char* lds, const int*) {
     const int lane = threadIdx.x & 63;
     const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fr = lane & 15, g = lane >> 4;
-    const RowPlace row = place_row(p, w, cum, fr);
-    if (cum) __syncthreads();  // looked up by all before keys come into its place
+    const RowPlace row = place_row(p, w, nullptr, fr);
     bf16x8 qf[kDK];
 #pragma unroll
     for (int k = 0; k < kDK; ++k)
@@ -380,6 +380,7 @@ template <int D, int WR, int QT>
 struct WideTile {
   static constexpr int KC = 64;
   static constexpr int kRows = 16 * QT * WR;
+  static constexpr bool kPacked = true;
   static constexpr int kPieces = D / 8;                 // 16-byte pieces of a key row
   static constexpr int kMat = KC * D * 2;               // bytes of a chunk's K (or V)
   static constexpr int kStage = 2 * kMat;
@@ -644,9 +645,9 @@ __device__ __forceinline__ void run_item(const PaParams& p, const List& list, un
   const int rest = item / p.Hk;
   const int tile = rest % tiles, part = rest / tiles;
   w.b = -1;
-  w.packed = !list.seq;
+  w.packed = T::kPacked && !list.seq;
   const int* cum = nullptr;
-  if (list.seq) {
+  if (!w.packed) {
     const int per = tiles / p.B;
     int b = tile / per, first = (tile - b * per) * T::kRows;
     if (p.causal) {

@@ -656,3 +656,28 @@ def test_two_captured_graphs_and_eager_calls_do_not_share_a_workspace(gkd):
         torch.cuda.synchronize()
         for o, w in zip(outs, want):
             assert torch.equal(o, w)
+
+
+def test_calls_from_several_threads_at_once(gkd):
+    """Each thread's calls keep their own operands."""
+    import threading
+    sets = [attn_inputs(rng(60 + i), 4, 3, 4, 2, 64, 200 + 30 * i, 50) for i in range(4)]
+    pos, freqs = torch.rand(3, 1, device="cuda"), torch.rand(1, 32, device="cuda")
+    want = [(gkd.prefix_attention(*s), gkd.qk_norm_rope(s[0], s[3][:, :3], pos, freqs)) for s in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = gkd.prefix_attention(*sets[i]), gkd.qk_norm_rope(sets[i][0], sets[i][3][:, :3], pos, freqs)
+                torch.cuda.current_stream().synchronize()
+                if not (torch.equal(got[0], want[i][0]) and torch.equal(got[1][0], want[i][1][0])
+                        and torch.equal(got[1][1], want[i][1][1])):
+                    bad.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
