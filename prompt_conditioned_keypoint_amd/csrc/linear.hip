@@ -15,7 +15,7 @@
 // Measured (a call, inputs that change from call to call; the card copies at
 // 5.08 TB/s):
 //   turn  36864 x 1024 x 4096, GELU             280 us, 1.10 PFLOP/s
-//   turn and ring  19706 x 1024 x 1024, float32 residual  74 us, 0.56 PFLOP/s,
+//   turn and ring  19706 x 1024 x 1024, float32 residual  72 us, 0.57 PFLOP/s,
 //         2.8 TB/s: one round of 256 x 256 tiles and 3322 rows apart; their
 //         epilogues, 161 MB of them, come when no products are left to hide them
 //   few   37 x 1024 x 4096, GELU 6.8 us on the GPU; 1 x 1024 x 1024 4.1 us

@@ -19,7 +19,7 @@
 //
 // Measured (bfloat16, a call, inputs that change from call to call):
 //   8 x 1024 queries, 32 heads of 128 (8 of keys), causal, behind 8192 keys:
-//     1.09 ms, 1.07 PFLOP/s. A wave's chunk is 68 matrix instructions and the
+//     1.06 ms, 1.10 PFLOP/s. A wave's chunk is 68 matrix instructions and the
 //     exponents between them; two waves a SIMD take turns with both.
 //   48 x 1 query, the same heads, 1024 own keys at most, behind 32768: 82 us,
 //     287 MB at 3.5 TB/s. Up to 128 rows it is the reading (32 sequences: 52 us,
