@@ -852,7 +852,7 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   }
   // the prefix for the rows of all sequences together, own keys apart
   // (beside thin items one wide one a CU: with 512 the 48 sequences with 1024
-  // own keys behind 32768 take 102 instead of 89 us; but where own keys are
+  // own keys behind 32768 take 83 instead of 75 us; but where own keys are
   // few, 384: 16 sequences with 256 behind 65536 61 instead of 69 us; among
   // wide ones half as many again as the CUs hold, which fill each other's gaps:
   // 37 x 80 rows of 8 heads of 128 behind 8192 125 us, with 512 149, with 1024 137)
