@@ -91,7 +91,7 @@ struct Piece<uint16_t> {
 // side, pieces 2 j and 2 j + 1; for split pairs (i, i + rot/2), pieces j and
 // rot/2/N + j while they rotate, then the rest of the head two by two. In
 // both orders the lane's pairs are N j .. N j + N - 1, so cosines and sines
-// are read as whole float4s; past rot/2 the table holds (1, 0). Split pairs
+// are read as whole float4s (past rot/2 the table is not used). Split pairs
 // whose half is no whole number of pieces (kLoose) keep pieces 2 j and 2 j + 1
 // and find each element's partner in LDS, where the head's lanes put their
 // values. Every lane reads its two pieces before it writes them and no lane
@@ -243,12 +243,16 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
       const float* c = cs + (2 * t) * npair + N * j;
       const float* s = c + npair;
       if (IL) {
+        // elements past rot are copied, not turned by (1, 0): an infinite or NaN
+        // neighbour times 0 would make them NaN
+        const int left = p.half - N * j;  // pairs that turn, from the lane's first on
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-          y0[2 * i] = x0[2 * i] * c[i] - x0[2 * i + 1] * s[i];
-          y0[2 * i + 1] = x0[2 * i + 1] * c[i] + x0[2 * i] * s[i];
-          y1[2 * i] = x1[2 * i] * c[N / 2 + i] - x1[2 * i + 1] * s[N / 2 + i];
-          y1[2 * i + 1] = x1[2 * i + 1] * c[N / 2 + i] + x1[2 * i] * s[N / 2 + i];
+          const bool t0 = i < left, t1 = N / 2 + i < left;
+          y0[2 * i] = t0 ? x0[2 * i] * c[i] - x0[2 * i + 1] * s[i] : x0[2 * i];
+          y0[2 * i + 1] = t0 ? x0[2 * i + 1] * c[i] + x0[2 * i] * s[i] : x0[2 * i + 1];
+          y1[2 * i] = t1 ? x1[2 * i] * c[N / 2 + i] - x1[2 * i + 1] * s[N / 2 + i] : x1[2 * i];
+          y1[2 * i + 1] = t1 ? x1[2 * i + 1] * c[N / 2 + i] + x1[2 * i] * s[N / 2 + i] : x1[2 * i + 1];
         }
       } else {
 #pragma unroll

@@ -341,6 +341,31 @@ def test_rope_zero_rows_and_refusals(gkd):
         gkd.qk_norm_rope(z, None, pos.int(), freqs)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 32), (64, 30), (96, 62), (80, 2), (40, 18), (128, 126), (65, 62)])
+def test_rope_elements_past_rot_are_copied(gkd, dtype, inter, D, rot):
+    """Infinities, NaN and zeros of both signs past rot come out as they are
+    and stay out of their neighbours, whichever kernel runs."""
+    print(f"[rope] D={D} rot={rot} {dtype} inter={inter}", flush=True)
+    q, _, pos, freqs, wq, _ = rope_inputs(rng(D), 2, 9, 3, 1, D, rot, 2, dtype)
+    q = q.contiguous()
+    special = torch.tensor([float("inf"), 1.5, -float("inf"), -0.0, float("nan"), 2.5, 0.0, -3.0], device="cuda")
+    q[..., rot:] = special.repeat(D // 8 + 1)[:D - rot].to(dtype)
+    y, _ = gkd.qk_norm_rope(q, None, pos, freqs, interleaved=inter)
+    rest, want = y[..., rot:].float(), q[..., rot:].float()
+    assert torch.equal(rest.isnan(), want.isnan()) and torch.equal(rest.nan_to_num(9.0), want.nan_to_num(9.0))
+    assert torch.equal(rest.signbit(), want.signbit())
+    clean = q.clone()
+    clean[..., rot:] = 0
+    assert torch.equal(y[..., :rot], gkd.qk_norm_rope(clean, None, pos, freqs, interleaved=inter)[0][..., :rot])
+    # an infinite square makes the norm infinite: finite elements become 0
+    q[..., rot:] = 1
+    q[..., -1] = float("inf")
+    y, _ = gkd.qk_norm_rope(q, None, pos, freqs, wq, interleaved=inter)
+    assert not bool(y[..., :-1].any()) and bool(y[..., -1].isnan().all())
+
+
 # --------------------------------------------------------------- attention
 def attn_inputs(g, B, Tq, Hq, Hk, D, P, S):
     q = randn(g, B, Tq, Hq, D)
