@@ -142,8 +142,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
-// A row's result: O^T[dim 16 j + 4 g + e] in o[j][e], l and m the same in all
-// its lanes.
+// A row's result: O^T[dim 16 j + 4 g + e] in o[j][e], l and m (base 2) the same
+// in all its lanes.
 template <int D>
 __device__ __forceinline__ void write_row(const PaParams& p, const TileWork& w, const RowPlace& r, int g,
                                           float m, float l, const f32x4 (&o)[D / 16], bool any_keys) {
@@ -290,9 +290,12 @@ struct ThinTile {
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x = fmaxf(x, sc[t][e]);
-      const float mn = fmaxf(m, group_max(x) * p.c);  // base-2 scores (c > 0)
+      // m is a product as it comes: differences of scores are taken first and
+      // scaled then, so the largest one's exponent is 0 at any size (the rounding
+      // of score times c is 2^7 and more from 2^31 on)
+      const float mn = fmaxf(m, group_max(x));
       const float ref = mn == -INFINITY ? 0.f : mn;
-      const float alpha = __builtin_amdgcn_exp2f(m - ref);
+      const float alpha = __builtin_amdgcn_exp2f((m - ref) * p.c);
       m = mn;
       l *= alpha;
 #pragma unroll
@@ -303,7 +306,7 @@ struct ThinTile {
         float e4[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[t][e], p.c, -ref));
+          e4[e] = __builtin_amdgcn_exp2f((sc[t][e] - ref) * p.c);
           l += e4[e];
         }
         pk[t][0] = bf16_pair(e4[0], e4[1]);
@@ -339,19 +342,19 @@ struct ThinTile {
 #pragma unroll
     for (int v = 0; v < WK - 1; ++v) top = fmaxf(top, sm[v * 64 + lane][0]);
     const float ref = top == -INFINITY ? 0.f : top;
-    const float a = __builtin_amdgcn_exp2f(m - ref);
+    const float a = __builtin_amdgcn_exp2f((m - ref) * p.c);
     m = top;
     l *= a;
 #pragma unroll
     for (int j = 0; j < kND; ++j) o[j] *= a;
     for (int v = 0; v < WK - 1; ++v) {
       const f32x2 x = sm[v * 64 + lane];
-      const float wgt = __builtin_amdgcn_exp2f(x[0] - ref);
+      const float wgt = __builtin_amdgcn_exp2f((x[0] - ref) * p.c);
       l = fmaf(x[1], wgt, l);
 #pragma unroll
       for (int j = 0; j < kND; ++j) o[j] += so[(v * kND + j) * 64 + lane] * wgt;
     }
-    write_row<D>(p, w, row, g, m, l, o, nc > 0);
+    write_row<D>(p, w, row, g, m * p.c, l, o, nc > 0);
   }
 };
 
@@ -375,6 +378,19 @@ struct KeyWalk {
 constexpr float kSlack = 8.f;
 constexpr uint32_t kSlackBits = 0x4380u;  // 2^8 in bfloat16
 constexpr float kNowhere = -3e38f;        // m before a row's first key: any score passes it
+
+// How far a score s passes m, base 2. One fused operation, while the rounding of
+// m (a score times c) is at most 1/2; a row that is further out takes the
+// rounded product, of which m is one, so that its largest score is at 0 and not
+// at that rounding (half of 2^9 at scores of 2^32, which leaves the row with
+// nothing or with infinities).
+constexpr float kFar = 16777216.f;
+__device__ __forceinline__ bool far_out(float m) { return fabsf(m) >= kFar && m != kNowhere; }
+__device__ __forceinline__ float passed(float s, float c, float m, bool far) {
+#pragma clang fp contract(off)
+  const float t = s * c;
+  return far ? t - m : fmaf(s, c, -m);
+}
 
 template <int D, int WR, int QT>
 struct WideTile {
@@ -432,6 +448,7 @@ struct WideTile {
 
     f32x4 o[QT][kND], l[QT];
     float m[QT];
+    bool wary = false;  // a row of the wave is far out
 #pragma unroll
     for (int u = 0; u < QT; ++u) {
       m[u] = kNowhere;
@@ -536,16 +553,17 @@ struct WideTile {
         }
       }
       uint32_t pk[QT][kNT][2];
-      auto exponents = [&]() -> bool {
+      auto exponents = [&](auto any_size) -> bool {
         u16x2 top = {0, 0};
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
           const float ref = m[u];
+          const bool far = any_size && far_out(ref);
 #pragma unroll
           for (int t = 0; t < kNT; ++t) {
             float e4[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f(fmaf(sc[u][t][e], p.c, -ref));
+            for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f(passed(sc[u][t][e], p.c, ref, far));
             pk[u][t][0] = bf16_pair(e4[0], e4[1]);
             pk[u][t][1] = bf16_pair(e4[2], e4[3]);
             top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, pk[u][t][0]));
@@ -554,9 +572,10 @@ struct WideTile {
         }
         return max(top[0], top[1]) >= kSlackBits;
       };
-      bool move = c == 0;
-      if (!move) move = __any(exponents());
+      bool move = c == 0 || wary;
+      if (!move) move = __any(exponents(std::false_type{}));
       if (move) {
+        bool far = false;
 #pragma unroll
         for (int u = 0; u < QT; ++u) {
           float x = -INFINITY;
@@ -566,14 +585,16 @@ struct WideTile {
             for (int e = 0; e < 4; ++e) x = fmaxf(x, sc[u][t][e]);
           x = group_max(x);
           // base-2 scores (c > 0), passed as the exponents above see it
-          const float mn = fmaf(x, p.c, -m[u]) > kSlack ? x * p.c : m[u];
+          const float mn = passed(x, p.c, m[u], far_out(m[u])) > kSlack ? x * p.c : m[u];
           const float alpha = __builtin_amdgcn_exp2f(m[u] - mn);
           m[u] = mn;
+          far = far || far_out(mn);
           l[u] *= alpha;
 #pragma unroll
           for (int j = 0; j < kND; ++j) o[u][j] *= alpha;
         }
-        exponents();
+        wary = __any(far);
+        exponents(std::true_type{});
       }
       // O^T += V^T P^T: k-slots 8 g .. 8 g + 7 carry keys 32 c + 4 g + (0..3)
       // and 32 c + 16 + 4 g + (0..3) on both sides; a row of ones in the place

@@ -587,6 +587,65 @@ def test_attention_refusals(gkd):
         gkd.prefix_attention(q.float(), kv, kv)
 
 
+def one_hot_scores(B, Tq, Hq, Hk, D, P, S, dots):
+    """Operands whose dot product with key j is `dots[j]` times a query row's
+    sign (own keys behind the prefix's), exactly: one element of a head does it."""
+    g = rng(P + S)
+    q, kp, vp, ko, vo = (t.contiguous() for t in attn_inputs(g, B, Tq, Hq, Hk, D, P, S))
+    for t in (q, kp, ko):
+        t.zero_()
+    q[..., 5] = 1
+    q[:, 1::2, :, 5] = -1
+    kp[..., 5] = dots[:P, None].to(BF)
+    ko[..., 5] = dots[None, P:, None].to(BF)
+    return q, kp, vp, ko, vo
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Tq,Hq,Hk,P,S", [
+    (1, 2, 2, 1, 300, 70),        # thin tiles
+    (1, 2, 1, 1, 9000, 64),       # and parts
+    (2, 40, 2, 1, 300, 70),       # wide tiles
+    (1, 130, 1, 1, 5000, 90),     # and parts
+    (5, 2, 2, 1, 1100, 40),       # packed rows, thin tiles beside them
+    (17, 20, 2, 1, 2100, 130)])   # packed rows, wide tiles beside them
+@pytest.mark.parametrize("size", [1e5, 1e9, 1e10, 3.3e11, 1e20, 1e36])
+def test_attention_scores_of_any_size(gkd, D, B, Tq, Hq, Hk, P, S, size):
+    """Scores whose float32 steps are large numbers: the largest takes all."""
+    print(f"[attn] B={B} Tq={Tq} {Hq}/{Hk} of {D} P={P} S={S} scores {size}", flush=True)
+    j = torch.arange(P + S, device="cuda")
+    dots = ((j * 7919) % (P + S) / (P + S) - 0.5) * size
+    orders = {"mixed": dots, "rising": dots.sort()[0], "below zero": dots - size}
+    for name, d in orders.items():
+        # bfloat16 keeps 8 bits: one key above the rest and one below
+        d = d.clone()
+        top, low = (P + S // 2, 3) if name != "rising" else (P + S - 1, 0)
+        d[top] = 2 * size if name != "below zero" else -0.25 * size
+        d[low] = -3 * size
+        q, kp, vp, ko, vo = one_hot_scores(B, Tq, Hq, Hk, D, P, S, d)
+        got = gkd.prefix_attention(q, kp, vp, ko, vo, scale=1.0)
+        v = torch.cat([vp.expand(B, -1, -1, -1), vo], 1)
+        want = torch.empty_like(got)
+        want[:, 0::2] = v[:, top, None].repeat_interleave(Hq // Hk, 2)
+        want[:, 1::2] = v[:, low, None].repeat_interleave(Hq // Hk, 2)
+        assert torch.equal(got, want), name
+
+
+def test_attention_rows_with_huge_scores_leave_their_neighbours(gkd):
+    """A row's bits are the same whatever the other rows of its wave see."""
+    for D in (64, 128):
+        for B, Tq, P, S in ((2, 60, 400, 90), (17, 20, 2100, 130)):
+            q, kp, vp, ko, vo = attn_inputs(rng(31), B, Tq, 2, 1, D, P, S)
+            want = gkd.prefix_attention(q, kp, vp, ko, vo)
+            for size in (30.0, 1e8, 1e12):
+                wild = q.clone()
+                wild[:, ::3] *= size
+                got = gkd.prefix_attention(wild, kp, vp, ko, vo)
+                keep = torch.arange(Tq, device="cuda") % 3 != 0
+                assert torch.equal(got[:, keep], want[:, keep]), (D, B, size)
+                assert bool(got.isfinite().all()), (D, B, size)
+
+
 # ------------------------------------------------------------ together
 def test_a_block_over_image_tokens_and_prompt_rows(gkd):
     """A pre-projection block as a user builds it: image tokens give the
