@@ -155,7 +155,7 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads *q, int Hq, const gkd_heads 
  * finite, and the products q . K_j, as they are and scaled, at most 1e38
  * in magnitude. Scores, softmax statistics and outputs are float32; probabilities are rounded to bfloat16 for the
  * product with V. Limits: D 64 or 128, Hq a multiple of Hk, B Tq Hq below
- * 2^31, B Hk ceil(Tq Hq / Hk / 128) below 2^23, P and S below 2^30, scale finite and above 0; dtype must be
+ * 2^31, B Hk ceil(Tq Hq / Hk / 128) below 2^23, P and S below 2^30, 0 < scale <= 2e38; dtype must be
  * GKD_DTYPE_BF16. q, k, v and
  * out: 16-byte aligned data, strides multiples of 8 (else GKD_ERR_ALIGN);
  * token strides of keys and values below 2^25 (else GKD_ERR_SHAPE).

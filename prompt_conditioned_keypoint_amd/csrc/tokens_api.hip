@@ -210,8 +210,9 @@ gkd_status gkd_prefix_attention(const gkd_heads* q, const gkd_heads* k_prefix,
     return fail(GKD_ERR_SHAPE, "%s: bad shape B=%d Tq=%d Hq=%d Hk=%d D=%d P=%d S=%d", fn, B, Tq, Hq, Hk, D, P, S);
   if ((D != 64 && D != 128) || Hq % Hk != 0)
     return fail(GKD_ERR_UNSUPPORTED, "%s: needs D 64 or 128 and Hq %% Hk == 0", fn);
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return fail(GKD_ERR_VALUE, "%s: scale must be finite and above 0", fn);
+  // (the kernels take base-2 scores: scale log2(e) must be finite too)
+  if (!(scale > 0.f) || !(scale <= 2e38f))
+    return fail(GKD_ERR_VALUE, "%s: scale must be above 0 and at most 2e38", fn);
   if (B == 0 || Tq == 0) return ok();
   gkd_status st;
   if ((st = check_heads(fn, "q", q, 2, 16)) != GKD_OK) return st;

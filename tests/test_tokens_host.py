@@ -173,6 +173,7 @@ def attn(lib, q=None, kp=None, vp=None, P=16, ko=None, vo=None, S=8, own_len=Non
     (dict(scale=0.0), VALUE),
     (dict(scale=-1.0), VALUE),
     (dict(scale=float("inf")), VALUE),
+    (dict(scale=3e38, own_len=A + 2), VALUE),  # times log2(e) past float32
     (dict(own_len=A + 2), ALIGN),
     (dict(q_len=A + 1), ALIGN),
 ])
