@@ -643,11 +643,12 @@ struct WideTile {
   }
 };
 
-// One part of a list of keys n, cut at multiples of `unit`.
+// One part of a list of keys n, cut at multiples of `unit` (n rounded up to
+// that may pass 2^31: prefix and own keys have up to 2^30 each).
 __device__ __forceinline__ void part_range(int n, int parts, int part, int unit, int& lo, int& hi) {
-  const int nu = (n + unit - 1) / unit;
-  lo = min((int)((long long)nu * part / parts) * unit, n);
-  hi = min((int)((long long)nu * (part + 1) / parts) * unit, n);
+  const long long nu = ((long long)n + unit - 1) / unit;
+  lo = (int)min(nu * part / parts * unit, (long long)n);
+  hi = (int)min(nu * (part + 1) / parts * unit, (long long)n);
 }
 
 template <int D>

@@ -646,6 +646,24 @@ def test_attention_rows_with_huge_scores_leave_their_neighbours(gkd):
                 assert bool(got.isfinite().all()), (D, B, size)
 
 
+@pytest.mark.parametrize("Tq", [1, 20])
+@pytest.mark.parametrize("P,S,n", [((1 << 30) - 1, (1 << 30) - 1, (1 << 30) - 1),     # 2^31 - 2 keys
+                                   ((1 << 30) - 1, (1 << 30) - 1, 1 << 29), ((1 << 30) - 64, (1 << 30) - 1, 70),
+                                   (5, (1 << 30) - 1, (1 << 30) - 1)])
+def test_attention_longest_lists_of_keys(gkd, Tq, P, S, n):
+    """As many keys as the limits allow, one in memory (token strides of 0):
+    equal scores, so the mean of the prefix's ones and the own keys' threes."""
+    print(f"[attn] Tq={Tq} P={P} S={S} own_len={n}", flush=True)
+    g = rng(4)
+    q, k = randn(g, 1, Tq, 1, 64), randn(g, 1, 1, 64)
+    one = torch.ones(1, 1, 64, dtype=BF, device="cuda")
+    own_len = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = gkd.prefix_attention(q, k.expand(P, 1, 64), one.expand(P, 1, 64), k[None].expand(1, S, 1, 64),
+                               (3 * one)[None].expand(1, S, 1, 64), own_len=own_len)
+    want = torch.tensor((P + 3 * n) / (P + n), device="cuda").to(BF)
+    assert bool((got == want).all()), (got.float().min(), got.float().max(), want)
+
+
 # ------------------------------------------------------------ together
 def test_a_block_over_image_tokens_and_prompt_rows(gkd):
     """A pre-projection block as a user builds it: image tokens give the
