@@ -455,6 +455,12 @@ class _Records(threading.local):
 _records = _Records()
 
 
+def _int_sizes(fn, *sizes):
+    """The C ABI takes sizes as ints, and ctypes would cut larger ones short."""
+    if max(sizes) > 0x7fffffff:
+        raise GkdError(2, f"{fn}: a size does not fit 32 bits: {sizes}")
+
+
 def _workspace(workspace, need, dev):
     if need == 0:
         return None, 0
@@ -490,6 +496,7 @@ def _row_stride(t, name):
 def linear_workspace_size(M: int, N: int, K: int, ldx: int | None = None,
                           ldw: int | None = None) -> int:
     """Bytes of workspace gkd_linear needs for these sizes and row strides."""
+    _int_sizes("gkd_linear_workspace_size", M, N, K)
     return int(load().gkd_linear_workspace_size(M, N, K, K if ldx is None else ldx,
                                                 K if ldw is None else ldw))
 
@@ -519,6 +526,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
     N, K = wshape
     lead = lead[:-1]
     M = lead.numel()
+    _int_sizes("gkd_linear", M, N, K)
     shape = lead + (N,)
     if out_dtype is None:
         out_dtype = (out.dtype if out is not None else
@@ -579,6 +587,7 @@ def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_w
     if freqs.dim() != 2:
         raise ValueError(f"freqs must be [n_axes, rot/2], got {tuple(freqs.shape)}")
     A, half = freqs.shape
+    _int_sizes("gkd_qk_norm_rope", B, T, Hq, Hk, D, A, 2 * half)
     pf = _dense(dev, freqs, "freqs", torch.float32, (A, half))
     own_pos = pos.dim() == 3
     pp = _dense(dev, pos, "pos", torch.float32, (B, T, A) if own_pos else (T, A))
@@ -615,6 +624,7 @@ def qk_norm_rope(q: torch.Tensor, k, pos: torch.Tensor, freqs: torch.Tensor, q_w
 def prefix_attention_workspace_size(B: int, Tq: int, Hq: int, Hk: int, D: int, P: int,
                                     S: int) -> int:
     """Bytes of workspace gkd_prefix_attention needs for these sizes."""
+    _int_sizes("gkd_prefix_attention_workspace_size", B, Tq, Hq, Hk, D, P, S)
     return int(load().gkd_prefix_attention_workspace_size(B, Tq, Hq, Hk, D, P, S))
 
 
@@ -653,6 +663,7 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
             raise ValueError("k_own and v_own must be [B,S,Hk,D]")
     if Hk is None:
         raise ValueError("give prefix keys, own keys or both")
+    _int_sizes("gkd_prefix_attention", B, Tq, Hq, Hk, D, P, S)
     pol = None if own_len is None else _dense(dev, own_len, "own_len", torch.int32, (B,))
     pql = None if q_len is None else _dense(dev, q_len, "q_len", torch.int32, (B,))
     pm = None if own_mask is None else _dense(dev, own_mask, "own_mask", torch.uint8, (B, S))

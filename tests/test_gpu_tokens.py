@@ -664,6 +664,31 @@ def test_attention_longest_lists_of_keys(gkd, Tq, P, S, n):
     assert bool((got == want).all()), (got.float().min(), got.float().max(), want)
 
 
+def test_sizes_past_32_bits_are_refused(gkd):
+    """Sizes that a C int would cut to 5: views of little memory, and rows of
+    one element (8 GB)."""
+    n = 2 ** 32 + 5
+    one = torch.ones(1, 1, 64, dtype=BF, device="cuda")
+    q = torch.ones(1, 1, 1, 64, dtype=BF, device="cuda")
+    out = torch.full_like(q, 7.0)
+    for kw in (dict(k_prefix=one.expand(n, 1, 64), v_prefix=one.expand(n, 1, 64)),
+               dict(k_own=one[None].expand(1, n, 1, 64), v_own=one[None].expand(1, n, 1, 64))):
+        with pytest.raises(gkd.GkdError) as e:
+            gkd.prefix_attention(q, out=out, **kw)
+        assert e.value.status == 2
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.qk_norm_rope(q.expand(1, 1, n, 64), None, torch.zeros(1, 1, device="cuda"),
+                         torch.zeros(1, 32, device="cuda"), q_out=q.expand(1, 1, n, 64))
+    assert e.value.status == 2 and "32 bits" in str(e.value)
+    x = torch.empty(n, 1, dtype=BF, device="cuda")
+    w = torch.ones(1, 1, dtype=BF, device="cuda")
+    y = torch.empty(n, 1, dtype=BF, device="cuda")
+    y[:8] = 7
+    with pytest.raises(gkd.GkdError) as e:
+        gkd.linear(x, w, out=y)
+    assert e.value.status == 2 and bool((y[:8] == 7).all()) and bool((out == 7).all())
+
+
 # ------------------------------------------------------------ together
 def test_a_block_over_image_tokens_and_prompt_rows(gkd):
     """A pre-projection block as a user builds it: image tokens give the

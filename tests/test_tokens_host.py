@@ -221,6 +221,26 @@ def test_python_calls_reject_cpu_tensors_and_bad_shapes():
         gkd.prefix_attention(h, h[0], h[0])
 
 
+def test_python_calls_refuse_sizes_past_32_bits():
+    """The C ABI's sizes are ints; a larger one must not arrive cut short."""
+    import prompt_conditioned_keypoint_amd as gkd
+    from prompt_conditioned_keypoint_amd.binding import _int_sizes
+    _int_sizes("f", 0, 5, 2**31 - 1)
+    for bad in (2**31, 2**32, 2**32 + 5, 2**63):
+        with pytest.raises(gkd.GkdError) as e:
+            _int_sizes("f", 1, bad, 2)
+        assert e.value.status == SHAPE
+        for i in range(3):
+            with pytest.raises(gkd.GkdError) as e:
+                gkd.linear_workspace_size(*(bad if j == i else 8 for j in range(3)))
+            assert e.value.status == SHAPE
+        for i in range(7):
+            with pytest.raises(gkd.GkdError) as e:
+                gkd.prefix_attention_workspace_size(*(bad if j == i else 8 for j in range(7)))
+            assert e.value.status == SHAPE
+    assert gkd.linear_workspace_size(2**31 - 1, 8, 8) == 0      # past the call's own limits: it takes none
+
+
 def test_row_stride_takes_evenly_spaced_rows_only():
     from prompt_conditioned_keypoint_amd.binding import _row_stride
     t = torch.zeros(4, 6, 16)
