@@ -636,9 +636,10 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
     [B,S,Hk,D] (either pair may be None), of which the first own_len[b]
     (int32) with own_mask[b,j] (uint8) set count. causal: the q_len[b]
     (int32, default Tq) queries are the last of the own_len[b] own tokens and
-    see own keys up to their place. Queries past q_len[b] leave their rows of
-    out as they are. scale: default D**-0.5. Returns out [B,Tq,Hq,D]; a query
-    without keys gives zeros."""
+    see own keys up to their place. Queries past q_len[b] are not computed:
+    their rows of a given `out` stay as they are, those of a new one are zeros.
+    scale: default D**-0.5. Returns out [B,Tq,Hq,D]; a query without keys gives
+    zeros."""
     lib = _lib or load()
     bf16 = torch.bfloat16
     dev = _place(q, "q")
@@ -668,7 +669,7 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
     pql = None if q_len is None else _dense(dev, q_len, "q_len", torch.int32, (B,))
     pm = None if own_mask is None else _dense(dev, own_mask, "own_mask", torch.uint8, (B, S))
     if out is None:
-        out = q.new_empty((B, Tq, Hq, D))
+        out = q.new_empty((B, Tq, Hq, D)) if q_len is None else q.new_zeros((B, Tq, Hq, D))
     ho = _heads(dev, out, "out", bf16)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")

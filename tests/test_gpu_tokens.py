@@ -689,6 +689,19 @@ def test_sizes_past_32_bits_are_refused(gkd):
     assert e.value.status == 2 and bool((y[:8] == 7).all()) and bool((out == 7).all())
 
 
+def test_attention_new_outputs_are_zero_past_q_len(gkd):
+    """Without `out`, the rows of queries that are not computed are zeros."""
+    for B, Tq, P in ((3, 5, 40), (17, 20, 2100)):
+        q, kp, vp, ko, vo = attn_inputs(rng(41), B, Tq, 4, 2, 64, P, 30)
+        q_len = torch.arange(B, dtype=torch.int32, device="cuda") % (Tq + 1)
+        want = gkd.prefix_attention(q, kp, vp, ko, vo, q_len=q_len, out=torch.zeros_like(q))
+        for _ in range(3):
+            held = [torch.full_like(q, 7.0) for _ in range(4)]      # what new memory may hold
+            torch.cuda.synchronize()
+            del held
+            assert torch.equal(gkd.prefix_attention(q, kp, vp, ko, vo, q_len=q_len), want)
+
+
 # ------------------------------------------------------------ together
 def test_a_block_over_image_tokens_and_prompt_rows(gkd):
     """A pre-projection block as a user builds it: image tokens give the
