@@ -305,12 +305,12 @@ struct ThinTile {
       for (int t = 0; t < 2; ++t) {
         float e4[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          e4[e] = __builtin_amdgcn_exp2f((sc[t][e] - ref) * p.c);
-          l += e4[e];
-        }
+        for (int e = 0; e < 4; ++e) e4[e] = __builtin_amdgcn_exp2f((sc[t][e] - ref) * p.c);
         pk[t][0] = bf16_pair(e4[0], e4[1]);
         pk[t][1] = bf16_pair(e4[2], e4[3]);
+        // the sum takes the probabilities as the product does, so weights add to one
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l += __uint_as_float(pk[t][e] << 16) + __uint_as_float(pk[t][e] & 0xffff0000u);
       }
       // O^T += V^T P^T: k-slots 8 g .. 8 g + 7 carry keys 4 g + (0..3) and
       // 16 + 4 g + (0..3) on both sides

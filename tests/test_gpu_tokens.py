@@ -702,6 +702,27 @@ def test_attention_new_outputs_are_zero_past_q_len(gkd):
             assert torch.equal(gkd.prefix_attention(q, kp, vp, ko, vo, q_len=q_len), want)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Tq,P,S", [(1, 1, 400, 0), (1, 1, 9000, 64), (3, 4, 0, 300), (2, 30, 300, 100),
+                                      (5, 1, 1100, 40), (17, 20, 2100, 130)])
+def test_attention_weights_add_to_one(gkd, D, B, Tq, P, S):
+    """Where all probabilities but a few round down by almost half a step, the
+    mean of ones is still 1: the sum takes what the product takes."""
+    s = float(np.log(0.5 + 0.9 * 2.0 ** -9))
+    hi = float(torch.tensor(s).to(BF))
+    q, kp, vp, ko, vo = (t.contiguous() for t in attn_inputs(rng(1), B, Tq, 2, 1, D, P, S))
+    for t in (q, kp, ko):
+        t.zero_()
+    q[..., :2] = 1
+    for t in (kp, ko):
+        t[..., 0], t[..., 1] = hi, s - hi
+    kp[::32, :, :2] = 0         # every chunk of keys holds one that is not rounded
+    ko[:, ::32, :, :2] = 0
+    vp.fill_(1), vo.fill_(1)
+    got = gkd.prefix_attention(q, kp, vp, ko, vo, scale=1.0)
+    assert bool((got == 1).all()), got.float().min()
+
+
 # ------------------------------------------------------------ together
 def test_a_block_over_image_tokens_and_prompt_rows(gkd):
     """A pre-projection block as a user builds it: image tokens give the
