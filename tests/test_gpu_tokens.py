@@ -212,6 +212,36 @@ def test_linear_empty_and_refusals(gkd):
         gkd.linear(x.float(), w)
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "quick_gelu", "silu"])
+@pytest.mark.parametrize("M", [40, 257])
+def test_linear_activations_by_themselves(gkd, act, M):
+    """Exact sums (one product each), so that the activation's own error is
+    what there is: GELU to 2^-20 |z|, and relative to itself to 2^-12 in the
+    tail down to -6; the quotients' exponent is rounded by 2^-22 of itself, its
+    exponential, the sum, the reciprocal and the product by a step or two each."""
+    x = torch.zeros(M, 8, dtype=BF, device="cuda")
+    w = torch.zeros(300, 8, dtype=BF, device="cuda")
+    x[:, 2] = torch.tensor(np.geomspace(1e-6, 4, M) * (-1.0) ** np.arange(M), device="cuda").to(BF)
+    w[:, 2] = torch.linspace(1, 2, 300, device="cuda").to(BF)
+    z = torch.outer(x[:, 2].double(), w[:, 2].double())
+    got = gkd.linear(x, w, act=act, out_dtype=F32).double()
+    if act == "relu":
+        assert torch.equal(got, z.clamp(min=0))
+        return
+    if act == "gelu":
+        want = z * torch.special.ndtr(z)
+        err = (got - want).abs()
+        assert bool((err <= 2.0 ** -20 * z.abs()).all()), (err / z.abs()).max()
+        tail = (z < -1) & (z > -6)
+        assert bool((err <= 2.0 ** -12 * want.abs())[tail].all()), (err / want.abs())[tail].max()
+        return
+    c = 1.702 if act == "quick_gelu" else 1.0
+    gate = torch.sigmoid(c * z)
+    want = z * gate
+    tol = want.abs() * ((1 - gate) * (c * z.abs() * 2.0 ** -22 + 2.0 ** -23) + 2.0 ** -21)
+    assert bool(((got - want).abs() <= tol).all()), ((got - want).abs() / want.abs()).max()
+
+
 # -------------------------------------------------------------------- rope
 def rope_inputs(g, B, T, Hq, Hk, D, rot, A, dtype, far=1000):
     rows = randn(g, B, T, (Hq + Hk) * D, dtype=dtype)
