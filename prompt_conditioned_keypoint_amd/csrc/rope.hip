@@ -8,9 +8,11 @@
 // float operations an element, far below what the memory leaves room for).
 //
 // phi in float64: pos and freqs are float32, so their product is exact, and
-// a float32 angle of 10^5 would be off by 2^-8 of a radian. It is reduced to
-// one turn there (phi / 2 pi minus the nearest whole number) and only the
-// rest, in [-1/2, 1/2], goes to float32 (2^-25 of a turn).
+// a float32 angle of 10^5 would be off by 2^-8 of a radian. For bfloat16 heads
+// it is reduced to one turn there (phi / 2 pi minus the nearest whole number)
+// and the rest, in [-1/2, 1/2], goes to float32 (2^-26 of a turn) and to the
+// hardware's functions; for float32 heads it stays in float64 up to the cosine
+// and sine, which are rounded once.
 //
 // Measured (the card copies at 5.08 TB/s): 2 x 18432 tokens, 40 heads of 128,
 // three axes, norm, bfloat16: 755 MB in 142 us, 5.3 TB/s; 64 x 581 tokens, 32
@@ -36,17 +38,41 @@ struct RopeParams {
   long long first;          // first token (head, rope_any_kernel) of this launch
 };
 
+// T: the heads' type.
+template <typename T>
 __device__ __forceinline__ void rope_angle(const RopeParams& p, const float* pos, int i, float& c,
                                            float& s) {
   double phi = 0.0;
   for (int a = 0; a < p.n_axes; ++a)
     phi = fma((double)pos[a], (double)p.freqs[(long long)a * p.half + i], phi);
-  const double turns = phi * 0.15915494309189533576888;  // 1 / (2 pi)
-  const float r = (float)(turns - rint(turns));
-  // the hardware's functions take turns; within half a turn they are right to
-  // 1.3e-7 (measured), two float32 steps of a value near 1
-  s = __builtin_amdgcn_sinf(r);
-  c = __builtin_amdgcn_cosf(r);
+  if constexpr (sizeof(T) == 2) {
+    const double turns = phi * 0.15915494309189533576888;  // 1 / (2 pi)
+    const float r = (float)(turns - rint(turns));
+    // the hardware's functions take turns; with the angle's rounding they are
+    // right to 1.8e-7 (measured), three float32 steps of a value near 1 and
+    // nothing beside the output's rounding to bfloat16 (2^-8)
+    s = __builtin_amdgcn_sinf(r);
+    c = __builtin_amdgcn_cosf(r);
+  } else {
+    // the nearest whole number k of quarter turns, and Taylor series of the rest,
+    // |h| <= pi / 4, whose first terms left out are h^13 / 13! and h^12 / 12! (1.2e-10)
+    const double quarters = phi * 0.63661977236758134308;  // 2 / pi
+    const double q = rint(quarters), h = (quarters - q) * 1.57079632679489661923, u = h * h;
+    const int k = (int)fma(-4.0, rint(0.25 * q), q) & 3;
+    double x = fma(u, -1.0 / 39916800, 1.0 / 362880);
+    x = fma(u, x, -1.0 / 5040);
+    x = fma(u, x, 1.0 / 120);
+    x = fma(u, x, -1.0 / 6);
+    const float sh = (float)fma(h * u, x, h);
+    double y = fma(u, -1.0 / 3628800, 1.0 / 40320);
+    y = fma(u, y, -1.0 / 720);
+    y = fma(u, y, 1.0 / 24);
+    y = fma(u, y, -0.5);
+    const float ch = (float)fma(u, y, 1.0);
+    const float sk = k & 1 ? ch : sh, ck = k & 1 ? sh : ch;
+    s = k & 2 ? -sk : sk;
+    c = (k + 1) & 2 ? -ck : ck;
+  }
 }
 
 // 16 bytes of T as floats and back (one rounding to nearest even).
@@ -181,7 +207,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
     uint32_t tb;
     place(t, b, tb);
     float c = 1.f, s = 0.f;
-    if (pr < p.half) rope_angle(p, p.pos + b * p.pos_batch + (long long)tb * p.n_axes, pr, c, s);
+    if (pr < p.half) rope_angle<T>(p, p.pos + b * p.pos_batch + (long long)tb * p.n_axes, pr, c, s);
     cs[(2 * t) * npair + pr] = c;
     cs[(2 * t + 1) * npair + pr] = s;
   }
@@ -322,7 +348,7 @@ __global__ __launch_bounds__(256) void rope_any_kernel(RopeParams p, bool interl
     if (pr >= p.half) continue;
     const int e0 = interleaved ? 2 * pr : pr, e1 = interleaved ? 2 * pr + 1 : pr + p.half;
     float c, s;
-    rope_angle(p, pos, pr, c, s);
+    rope_angle<T>(p, pos, pr, c, s);
     const float u0 = w ? a0[i] * rs * rope_load(w + e0) : a0[i];
     const float u1 = w ? a1[i] * rs * rope_load(w + e1) : a1[i];
     rope_store(dst + e0, u0 * c - u1 * s);

@@ -396,6 +396,26 @@ def test_rope_elements_past_rot_are_copied(gkd, dtype, inter, D, rot):
     assert not bool(y[..., :-1].any()) and bool(y[..., -1].isnan().all())
 
 
+@pytest.mark.parametrize("D,rot,inter", [(64, 64, False), (64, 64, True), (96, 76, False), (66, 62, True)])
+def test_rope_float32_angles(gkd, D, rot, inter):
+    """The pair (1, 0) comes out as (cos, sin): half a float32 step of 1
+    (2^-25) for the rounding and 2^-30 for the angle and the functions."""
+    q = torch.zeros(1, 3000, 1, D, device="cuda")
+    i = torch.arange(rot // 2, device="cuda")
+    p0, p1 = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    q[..., p0] = 1
+    g = rng(D)
+    pos = (torch.rand(3000, 2, generator=g, device="cuda") * 4000).floor()
+    pos[:8, 0] = torch.arange(8, device="cuda")
+    pos[:8, 1] = 0
+    freqs = torch.rand(2, rot // 2, generator=g, device="cuda")
+    freqs[0, :4] = torch.tensor([np.pi / 2, np.pi / 4, np.pi, 1e-4])
+    y = gkd.qk_norm_rope(q, None, pos, freqs, interleaved=inter)[0].double()[0, :, 0]
+    phi = (pos.double()[:, :, None] * freqs.double()).sum(1)
+    err = max(float((y[:, p0] - phi.cos()).abs().max()), float((y[:, p1] - phi.sin()).abs().max()))
+    assert err <= 2.0 ** -25 + 2.0 ** -30, err
+
+
 # --------------------------------------------------------------- attention
 def attn_inputs(g, B, Tq, Hq, Hk, D, P, S):
     q = randn(g, B, Tq, Hq, D)
