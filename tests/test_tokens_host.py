@@ -7,6 +7,8 @@ read.
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -254,3 +256,21 @@ def test_row_stride_takes_evenly_spaced_rows_only():
     for bad in (t[:, :3], t.transpose(1, 2)):
         with pytest.raises(ValueError):
             _row_stride(bad, "t")
+
+
+@pytest.mark.parametrize("gone", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_package_needs_no_private_part_of_torch(gone):
+    """Imported on a torch without its private stream and device calls, it
+    takes the public ones."""
+    code = ("import torch\n"
+            f"del torch._C.{gone}\n"
+            "import prompt_conditioned_keypoint_amd as gkd\n"
+            "from prompt_conditioned_keypoint_amd import binding\n"
+            "class S: cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda dev=None: S\n"
+            f"gone = {gone!r}\n"
+            "assert gone != '_cuda_getCurrentRawStream' or binding._raw_stream(0) == 77\n"
+            "assert gone != '_cuda_getDevice' or binding._current_device is torch.cuda.current_device\n"
+            "print('fine')\n")
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert res.stdout.strip() == "fine", res.stderr
