@@ -773,6 +773,51 @@ def test_attention_weights_add_to_one(gkd, D, B, Tq, P, S):
     assert bool((got == 1).all()), got.float().min()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Tq,P,S", [(2, 20, 300, 100), (2, 70, 700, 60), (17, 20, 2100, 130)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_growing_scores_in_wide_tiles(gkd, D, B, Tq, P, S, causal):
+    """Scores that grow from chunk to chunk, so that the reference point moves
+    by finite amounts while sums and outputs stand behind it."""
+    q, kp, vp, ko, vo = attn_inputs(rng(9), B, Tq, 4, 2, D, P, S)
+    q[:, ::4] *= 0.25                                   # rows that hardly move
+    kp = kp * torch.linspace(0.1, 12, P, device="cuda").to(BF)[:, None, None]
+    ko = ko * torch.linspace(12, 20, S, device="cuda").to(BF)[:, None, None]
+    for scale in (1.0, 0.05, 1e-6):
+        got = np64(gkd.prefix_attention(q, kp, vp, ko, vo, scale=scale, causal=causal))
+        want, mean_abs, worst = ot.prefix_attention(*(np64(t) for t in (q, kp, vp, ko, vo)), causal=causal,
+                                                    scale=scale)
+        err = np.abs(got - want)
+        assert np.all(err <= attn_tol(want, mean_abs, worst, D)), (scale, err.max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Tq,P,S", [(2, 40, 640, 64), (17, 20, 2112, 128), (1, 130, 5000, 64)])
+@pytest.mark.parametrize("rise", [7.75, 8.0, 8.25, 0.5])
+def test_attention_rises_about_the_slack(gkd, D, B, Tq, P, S, rise):
+    """Scores (base 2) that rise by a little less or more than 8 from chunk to
+    chunk, in some rows of a wave alone, and fall in others."""
+    print(f"[attn] B={B} Tq={Tq} {D} P={P} S={S} rise {rise}", flush=True)
+    q, kp, vp, ko, vo = (t.contiguous() for t in attn_inputs(rng(10), B, Tq, 2, 1, D, P, S))
+    for t in (q, kp, ko):
+        t[..., 1:] *= 0.125
+    steps = (torch.arange(P + S, device="cuda") // 64 % 12) * rise
+    kp[..., 0], ko[..., 0] = steps[:P, None].to(BF), steps[None, P:, None].to(BF)
+    kinds = torch.tensor([1.0, 0.0, 0.5, -1.0, 1.0], device="cuda").to(BF)
+    q[..., 0] = kinds[torch.arange(Tq, device="cuda") % 5][None, :, None]
+    scale = float(np.log(2.0))
+    got = gkd.prefix_attention(q, kp, vp, ko, vo, scale=scale)
+    want, mean_abs, worst = ot.prefix_attention(*(np64(t) for t in (q, kp, vp, ko, vo)), scale=scale)
+    err = np.abs(np64(got) - want)
+    assert np.all(err <= attn_tol(want, mean_abs, worst, D)), err.max()
+    # the rows that rise do not touch the bits of the others
+    calm = q.clone()
+    rising = torch.arange(Tq, device="cuda") % 5 == 0
+    calm[:, rising, :, 0] = 0
+    again = gkd.prefix_attention(calm, kp, vp, ko, vo, scale=scale)
+    assert torch.equal(again[:, ~rising], got[:, ~rising])
+
+
 # ------------------------------------------------------------ together
 def test_a_block_over_image_tokens_and_prompt_rows(gkd):
     """A pre-projection block as a user builds it: image tokens give the
