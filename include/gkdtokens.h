@@ -64,7 +64,9 @@ typedef struct {
  * Matrix product with bias, activation and residual:
  *   out[m,n] = act(sum_k x[m,k] w[n,k] + bias[n]) + residual[m,n]
  * (w as a torch Linear weight). bfloat16 operands, float32 accumulation and
- * epilogue, one rounding to out_dtype at the end.
+ * epilogue, one rounding to out_dtype at the end. The activations are right
+ * to 2^-20 |z| (GELU by a polynomial, in its tail down to z = -6 to 2^-12 of
+ * itself; quick GELU and SiLU by the hardware's exponential and reciprocal).
  *
  *   x        [M,K] bf16, row stride ldx >= K, 16-byte aligned
  *   w        [N,K] bf16, row stride ldw >= K, 16-byte aligned
@@ -104,8 +106,11 @@ GKD_API gkd_status gkd_linear(const void *x, int64_t ldx, const void *w, int64_t
  * alone has 0 in the other axes' rows, so sections of frequencies per axis
  * (time, height, width), frequencies dealt to the axes in turn and mixed
  * ones are all this one table. phi is summed and reduced to one turn in
- * float64 (positions of 10^6 keep their angle); norms, rotation and
- * weights are float32, rounded once to dtype.
+ * float64 (positions of 10^6 keep their angle), cosines and sines are right
+ * to 2^-25 for f32 and to 2^-22 for bf16 heads (the hardware's functions);
+ * norms, rotation and weights are float32 (a head's squares must stay
+ * finite there), rounded once to dtype. Without a norm a value that is not
+ * finite stays within its pair, and past rot within its element.
  *
  *   q, q_out [B,T,Hq,D] dtype; k, k_out [B,T,Hk,D] dtype, or both NULL with
  *            Hk = 0. An output may be its input itself (same data and
@@ -153,11 +158,11 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads *q, int Hq, const gkd_heads 
  * Own keys and values past own_len or masked may hold anything, NaN
  * included, and so may queries past q_len; every other input must be
  * finite, and the products q . K_j, as they are and scaled, at most 1e38
- * in magnitude. Scores, softmax statistics and outputs are float32; probabilities are rounded to bfloat16 for the
- * product with V. Limits: D 64 or 128, Hq a multiple of Hk, B Tq Hq below
- * 2^31, B Hk ceil(Tq Hq / Hk / 128) below 2^23, P and S below 2^30, 0 < scale <= 2e38; dtype must be
- * GKD_DTYPE_BF16. q, k, v and
- * out: 16-byte aligned data, strides multiples of 8 (else GKD_ERR_ALIGN);
+ * in magnitude. Scores, softmax statistics and outputs are float32;
+ * probabilities are rounded to bfloat16 for the product with V and summed
+ * as they are there. Limits: D 64 or 128, Hq a multiple of Hk, B Tq Hq
+ * below 2^31, B Hk ceil(Tq Hq / Hk / 128) below 2^23, P and S below 2^30,
+ * 0 < scale <= 2e38; dtype must be GKD_DTYPE_BF16. q, k, v and out: 16-byte aligned data, strides multiples of 8 (else GKD_ERR_ALIGN);
  * token strides of keys and values below 2^25 (else GKD_ERR_SHAPE).
  * `out` overlaps no input.
  */

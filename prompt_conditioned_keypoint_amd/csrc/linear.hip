@@ -12,10 +12,10 @@
 // The products run on v_mfma_f32_16x16x32_bf16 with w as the first operand,
 // so a lane ends with four adjacent columns of one row.
 //
-// Measured (a call, inputs that change from call to call; the card copies at
-// 5.08 TB/s):
-//   turn  36864 x 1024 x 4096, GELU             280 us, 1.10 PFLOP/s
-//   turn and ring  19706 x 1024 x 1024, float32 residual  72 us, 0.57 PFLOP/s,
+// Measured (M x K x N; a call, inputs that change from call to call; the card
+// copies at 5.08 TB/s; boxes differ by 3%):
+//   turn  36864 x 1024 x 4096, GELU             275-285 us, 1.1 PFLOP/s
+//   turn and ring  19706 x 1024 x 1024, float32 residual  70-72 us, 0.58 PFLOP/s,
 //         2.8 TB/s: one round of 256 x 256 tiles and 3322 rows apart; their
 //         epilogues, 161 MB of them, come when no products are left to hide them
 //   few   37 x 1024 x 4096, GELU 6.8 us on the GPU; 1 x 1024 x 1024 4.1 us
@@ -756,7 +756,7 @@ hipError_t run_turn(const LinParams& p, hipStream_t st) {
 }
 
 // The kernel follows from how many tiles there are for the 256 CUs. Measured
-// (us, this choice / the next best): 222 x 58 x 4096 19 / 31, 700 x 1209 x
+// (M x N x K; us, this choice / the next best): 222 x 58 x 4096 19 / 31, 700 x 1209 x
 // 2384 15 / 22 (64 x 64 tiles); 1425 x 777 x 646 15 / 18 (128 x 64); 3825 x
 // 610 x 3616 40 / 43, 8049 x 260 x 2952 35 / 38 (128 x 128, four stages);
 // 28607 x 2031 x 224 72 / 80, 35266 x 476 x 96 17 / 19 (128 x 128, two
@@ -771,11 +771,14 @@ hipError_t run_rows(const LinParams& p, hipStream_t st) {
   if (tiles(p.M, 128, 128) <= 256) return run_ring<128, 128, 2, 4, 1, 4>(p, st);
   // Beyond that the 256 x 256 kernel takes 1.35 us a step and 10 us a tile, all
   // CUs in step, and the 128 x 128 one 0.95 us and 7 us for each 512 tiles, one
-  // round of smaller tiles 1.2 us and 5: 15161 x 3143 x 1512 168 against 198,
-  // 4096 x 4096 x 1024 32 against 39. Rows beyond the 256 x 256 tiles' last
-  // whole round go to a launch of their own where that is the least: 19706 x
-  // 1024 x 1024 78 against 92 us (float32 with residual), 8917 x 3552 x 2079
-  // 135 against 185.
+  // round of smaller tiles 1.2 us and 5 (bfloat16 outputs, no residual; the model
+  // knows neither): 15161 x 3143 x 1512 168 against 198, 4096 x 4096 x 1024 32
+  // against 39, each in one launch. Rows beyond the 256 x 256 tiles' last whole
+  // round go to a launch of their own where that is the least (calls with it /
+  // without): 19706 x 1024 x 1024 70 / 86 us with a float32 residual, 44 / 49 in
+  // bfloat16 without; 15161 x 3143 x 1512 142 / 168; 8917 x 2079 x 3552 130 /
+  // 153. Over 45 drawn sizes it gained 4% on average, from 7% slower to 38%
+  // faster: what the model leaves out.
   const int nk = (p.K + kBK - 1) / kBK;
   auto ring = [&](long long m) {
     const long long n = tiles(m, 128, 128);

@@ -7,6 +7,13 @@
 // exp(s - m) and the output O scaled alike, and ranges of keys that were
 // taken apart are joined by
 //   m = max_i m_i,  l = sum_i l_i exp(m_i - m),  O = sum_i O_i exp(m_i - m).
+// Probabilities are rounded to bfloat16 (2^-8 of each) for the product with V,
+// whose instruction takes both sides in that type; l sums the rounded ones, so a
+// row's weights add to one and what is left is an error of the size of the
+// output's own rounding (2.3e-3 of an output in the mean, 1.7e-3 of it the
+// latter). Two products, of the high and the low half, would take half as many
+// matrix instructions again.
+//
 // So the prefix can be taken once for the rows of all sequences together
 // (their keys pass through LDS once per tile of rows, not once per
 // sequence), own keys sequence by sequence, and long ranges in parts.
@@ -19,8 +26,8 @@
 //
 // Measured (bfloat16, a call, inputs that change from call to call):
 //   8 x 1024 queries, 32 heads of 128 (8 of keys), causal, behind 8192 keys:
-//     1.06 ms, 1.10 PFLOP/s. A wave's chunk is 68 matrix instructions and the
-//     exponents between them; two waves a SIMD take turns with both.
+//     1.08-1.10 ms, 1.07 PFLOP/s. A wave's chunk is 68 matrix instructions and
+//     the exponents between them; two waves a SIMD take turns with both.
 //   48 x 1 query, the same heads, 1024 own keys at most, behind 32768: 82 us,
 //     287 MB at 3.5 TB/s. Up to 128 rows it is the reading (32 sequences: 52 us,
 //     4.5 TB/s); these 192 are two tiles, which read the prefix through L2 and
@@ -675,7 +682,9 @@ __device__ __forceinline__ void run_item(const PaParams& p, const List& list, un
     if (p.causal) {
       // every sequence's last rows, which see the most keys, come first, and the
       // short ones fill the gaps at the end (8 x 1024 rows, 16 heads of 128, no
-      // prefix: 66 -> 54 us; behind 8192 1139 -> 1083)
+      // prefix: 65 -> 53 us; 32 heads, 8 of keys, behind 8192 1125 -> 1083; but
+      // 33 x 464 rows of 120 heads of 64, 15 of keys, no prefix 239 -> 251, as own
+      // keys leave L2 between their tiles)
       const int turned = tiles - 1 - tile;
       b = turned % p.B;
       first = turned / p.B * T::kRows;
@@ -855,10 +864,14 @@ Plan make_plan(int B, int Tq, int Hq, int Hk, int P, int S) {
   // Packing the rows of all sequences reads the prefix once for 128 of them
   // and costs a second list of items, partial results and a join; tiles within
   // a sequence leave 128 - RS of their rows empty instead. Measured (us, packed
-  // / in sequence): 64 x 1 row of 16 heads of 64 behind 4096 keys 21 / 77,
-  // behind 256 20 / 16; two sequences behind 16384 29 / 21; 37 x 80 rows behind
-  // 2304 54 / 72, behind 1024 38 / 38; 64 x 96 rows of 8 heads of 128 behind
-  // 8192 236 / 246, behind 2304 89 / 77; 8 x 80 rows behind 2304 32 / 29.
+  // / in sequence): 64 x 1 row of 16 heads of 64 behind 4096 keys 17 / 80,
+  // behind 256 14 / 12; two sequences behind 16384 20 / 20; 37 x 80 rows behind
+  // 2304 53 / 69, and with half of them in use (q_len) 40 / 65; 64 x 96 rows of 8
+  // heads of 128 behind 8192 229 / 242, behind 2304 88 / 77; 8 x 80 rows behind
+  // 2304 27 / 27. The rule sees neither the rows in use nor the heads: 37 x 80
+  // rows, half in use, behind 1024 stay in sequence, 31 / 41. It asks for own
+  // keys, and for 1024 sequences at most, whose lengths fit LDS: prefix keys
+  // alone, or longer batches, take tiles in sequence.
   // (The last limit keeps the join's threads below 2^32.)
   const bool packed = S > 0 && B <= kMostPacked && RT * Hk < (1 << 25) &&
                       (RS <= 16 ? B >= 4 && P >= 1024

@@ -14,9 +14,11 @@
 // hardware's functions; for float32 heads it stays in float64 up to the cosine
 // and sine, which are rounded once.
 //
-// Measured (the card copies at 5.08 TB/s): 2 x 18432 tokens, 40 heads of 128,
-// three axes, norm, bfloat16: 755 MB in 142 us, 5.3 TB/s; 64 x 581 tokens, 32
-// heads of 64: 305 MB in 61 us, 5.0 TB/s; 8 tokens 5.7 us on the GPU.
+// Measured (a call; the card copies at 5.08 TB/s): 2 x 18432 tokens, 40 heads of
+// 128, three axes, norm, bfloat16: 755 MB in 141 us, 5.3 TB/s; 64 x 581 tokens,
+// 32 heads of 64: 305 MB in 59 us, 5.1 TB/s; 8 tokens 4.8 us on the GPU. Split
+// pairs of odd halves (kLoose) are at half that rate, their partners looked up
+// in LDS one by one: 9 x 2193 tokens, 16 heads of 96, 121 MB in 44 us.
 #include "gkd_device.hpp"
 #include "tokens_launch.hpp"
 
@@ -179,8 +181,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   if (p.wk) wk0 = gain(p.wk, e0, b0), wk1 = gain(p.wk, e1, b1);
 
   // A head is on its way while the one before is worked on, the first one
-  // while the table is made (kLoose: 54 instead of 51 us at 9 x 2193 tokens of
-  // 16 heads of 96, so there each head is loaded when it is due).
+  // while the table is made. Not so with kLoose, where it gains nothing on
+  // average (76 of 96 rotated, 9 x 2193 tokens, 16 heads, norm: 44.7 us with it,
+  // 43.9 without; 90 rotated, 62 x 455 tokens, 25 heads, no norm: 85.4, 87.7).
   constexpr int kStep = 256 / LP;  // heads a round
   const int units = nt * p.H;
   u32x4 next0 = z4, next1 = z4;
@@ -369,9 +372,9 @@ hipError_t run_pieces(RopeParams p, int pairs, hipStream_t st) {
   constexpr int N = Piece<T>::N;
   const int npair = (p.D + 2 * N - 1) / (2 * N) * N;
   // about 1024 pairs of pieces a workgroup (four rounds of its lanes), fewer
-  // where that leaves less than four workgroups a CU (3 x 1001 tokens of 8
-  // heads of 96 in float32 9.0 us, with 1024 10.5; 4 x 300 of 5 heads of 128
-  // 5.6, 10.2), while its table stays within 16 KB of LDS
+  // where that leaves less than four workgroups a CU (in a captured graph: 3 x
+  // 1001 tokens of 8 heads of 96 in float32 8.3 us, with 1024 10.6; 4 x 300 of 5
+  // heads of 128 4.4, 8.6), while its table stays within 16 KB of LDS
   const long long round = 256 / ((long long)p.H * LP);
   long long tt = 1024 / ((long long)p.H * LP);
   if (tt > p.n_tok / 1024) tt = p.n_tok / 1024 > round ? p.n_tok / 1024 : round;
