@@ -162,9 +162,10 @@ GKD_API gkd_status gkd_qk_norm_rope(const gkd_heads *q, int Hq, const gkd_heads 
  * probabilities are rounded to bfloat16 for the product with V and summed
  * as they are there. Limits: D 64 or 128, Hq a multiple of Hk, B Tq Hq
  * below 2^31, B Hk ceil(Tq Hq / Hk / 128) below 2^23, P and S below 2^30,
- * 0 < scale <= 2e38; dtype must be GKD_DTYPE_BF16. q, k, v and out: 16-byte aligned data, strides multiples of 8 (else GKD_ERR_ALIGN);
- * token strides of keys and values below 2^25 (else GKD_ERR_SHAPE).
- * `out` overlaps no input.
+ * 0 < scale <= 2e38; dtype must be GKD_DTYPE_BF16. q, k, v and out:
+ * 16-byte aligned data, strides multiples of 8 (else GKD_ERR_ALIGN); token
+ * strides of keys and values below 2^25 (else GKD_ERR_SHAPE). `out`
+ * overlaps no input.
  */
 GKD_API size_t gkd_prefix_attention_workspace_size(int B, int Tq, int Hq, int Hk, int D, int P,
                                                    int S);

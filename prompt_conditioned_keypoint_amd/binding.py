@@ -509,7 +509,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias=None, residual=None, act:
     bf16, bias [N] bf16, residual [..., N] in the output's dtype (bf16, or
     float32 by out_dtype, out or residual) -> [..., N]. Rows may be strided,
     evenly over all leading axes (of tokens [B, 5 + H*W, C] with B > 1, take
-    them all, or each sequence's); x and weight start on 16-byte places. act: "none", "relu", "gelu", "quick_gelu" or "silu". `out` may be
+    them all, or each sequence's); x and weight start on 16-byte places.
+    act: "none", "relu", "gelu", "quick_gelu" or "silu". `out` may be
     `residual` itself. workspace: a uint8 GPU tensor of at least
     linear_workspace_size() bytes (allocated here when None)."""
     lib = _lib or load()
