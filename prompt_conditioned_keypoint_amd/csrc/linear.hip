@@ -13,7 +13,7 @@
 // so a lane ends with four adjacent columns of one row.
 //
 // Measured (M x K x N; a call, inputs that change from call to call; the card
-// copies at 5.08 TB/s; boxes differ by 3%):
+// copies at 5.08 TB/s; cards differ by 3%):
 //   turn  36864 x 1024 x 4096, GELU             275-285 us, 1.1 PFLOP/s
 //   turn and ring  19706 x 1024 x 1024, float32 residual  70-72 us, 0.58 PFLOP/s,
 //         2.8 TB/s: one round of 256 x 256 tiles and 3322 rows apart; their
