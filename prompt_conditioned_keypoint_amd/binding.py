@@ -28,6 +28,7 @@ GKD_QUERY_TOKENS = 0x8       # query as [B, skip + H*W, C] tokens; skip in bits 
 GKD_TOKENS_VERSION = 1       # include/gkdtokens.h
 GKD_ROPE_INTERLEAVED = 0x1   # gkd_qk_norm_rope flag: pairs (2i, 2i + 1)
 GKD_ATTN_CAUSAL = 0x1        # gkd_prefix_attention flag: own keys up to the query's place
+GKD_FP4_VERSION = 1          # include/gkdfp4.h
 GKD_ACTS = {"none": 0, "relu": 1, "gelu": 2, "quick_gelu": 3, "silu": 4}
 STATUS = {0: "GKD_OK", 1: "GKD_ERR_NULL", 2: "GKD_ERR_SHAPE", 3: "GKD_ERR_DTYPE",
           4: "GKD_ERR_VALUE", 5: "GKD_ERR_UNSUPPORTED", 6: "GKD_ERR_HIP",
@@ -41,6 +42,11 @@ class GkdHeads(ctypes.Structure):
     """gkd_heads: data pointer and element strides of a [B,T,H,D] operand."""
     _fields_ = [("data", _P), ("batch", ctypes.c_int64), ("token", ctypes.c_int64),
                 ("head", ctypes.c_int64)]
+
+
+class GkdCache(ctypes.Structure):
+    """gkd_cache: a cache's arrays and sizes."""
+    _fields_ = [("codes", _P), ("scales", _P), ("pages", _I), ("page", _I), ("Hk", _I), ("D", _I)]
 
 
 class GkdError(RuntimeError):
@@ -85,7 +91,7 @@ def load():
     lib.gkd_kg_transformer_noalloc.restype = _I
     lib.gkd_kg_transformer_noalloc.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I,
                                                _I, _I, _U32, _P, _P]
-    _L, _Z, _H = ctypes.c_int64, ctypes.c_size_t, _P  # _H: gkd_heads *
+    _L, _Z, _H = ctypes.c_int64, ctypes.c_size_t, _P  # _H: gkd_heads * or gkd_cache *
     lib.gkd_tokens_version.restype = _I
     lib.gkd_linear_workspace_size.restype = _Z
     lib.gkd_linear_workspace_size.argtypes = [_I, _I, _I, _L, _L]
@@ -100,10 +106,29 @@ def load():
     lib.gkd_prefix_attention.restype = _I
     lib.gkd_prefix_attention.argtypes = [_H, _H, _H, _I, _H, _H, _I, _P, _P, _P, _I, _I, _I, _I,
                                          _I, _F, _I, _U32, _H, _P, _Z, _P]
+    lib.gkd_fp4_version.restype = _I
+    lib.gkd_quantize_fp4.restype = _I
+    lib.gkd_quantize_fp4.argtypes = [_P, _L, _I, _I, _I, _U32, _P, _P, _P]
+    lib.gkd_linear_fp4_workspace_size.restype = _Z
+    lib.gkd_linear_fp4_workspace_size.argtypes = [_I] * 3
+    lib.gkd_linear_fp4.restype = _I
+    lib.gkd_linear_fp4.argtypes = [_P, _L, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _U32, _P, _L,
+                                   _P, _Z, _P]
+    lib.gkd_cache_append.restype = _I
+    lib.gkd_cache_append.argtypes = [_H, _H, _I, _I, _P, _P, _H, _P, _I, _I, _U32, _P]
+    lib.gkd_cache_read.restype = _I
+    lib.gkd_cache_read.argtypes = [_H, _P, _I, _I, _I, _P, _P, _U32, _H, _H, _P]
+    lib.gkd_cache_attention_workspace_size.restype = _Z
+    lib.gkd_cache_attention_workspace_size.argtypes = [_I] * 7
+    lib.gkd_cache_attention.restype = _I
+    lib.gkd_cache_attention.argtypes = [_H, _H, _P, _I, _P, _P, _I, _I, _I, _F, _U32, _H, _P, _Z,
+                                        _P]
     if lib.gkd_abi_version() != GKD_ABI_VERSION:
         raise ImportError("libgkdhead ABI version mismatch")
     if lib.gkd_tokens_version() != GKD_TOKENS_VERSION:
         raise ImportError("libgkdhead token operators' version mismatch")
+    if lib.gkd_fp4_version() != GKD_FP4_VERSION:
+        raise ImportError("libgkdhead four-bit operators' version mismatch")
     _lib = lib
     return lib
 
@@ -443,6 +468,7 @@ def _heads(dev, t, name, dtype, ndim=4):
 _NO_HEADS = (0, 0, 0, 0)
 _HEADS_BYTES = ctypes.sizeof(GkdHeads)
 _pack4, _pack6 = struct.Struct("16q").pack_into, struct.Struct("24q").pack_into  # gkd_heads
+_pack_cached = struct.Struct("8q2q4i").pack_into  # two gkd_heads and a gkd_cache
 
 
 class _Records(threading.local):
@@ -689,6 +715,233 @@ def prefix_attention(q: torch.Tensor, k_prefix=None, v_prefix=None, k_own=None, 
                                       GKD_ATTN_CAUSAL if causal else 0, at + 5 * n,
                                       None if ws is None else ws.data_ptr(), ws_bytes,
                                       _raw_stream(dev))
+    if status:
+        _check(status)
+    return out
+
+
+def _codes(dev, codes, scales, shape):
+    """Addresses of the codes [..., n/2] and scale bytes [..., n/32] of values
+    of this shape."""
+    n = shape[-1]
+    return (_dense(dev, codes, "codes", torch.uint8, shape[:-1] + (n // 2,)),
+            _dense(dev, scales, "scales", torch.uint8, shape[:-1] + (n // 32,)))
+
+
+def quantize_fp4(x: torch.Tensor, codes=None, scales=None):
+    """Values x [..., K] (float32 or bf16, K a multiple of 32) as four-bit codes
+    [..., K/2] and scale bytes [..., K/32], both uint8: value = code * 2^(scale -
+    127), codes of 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a sign, a byte's low half
+    the earlier one. Rows may be strided, evenly over all leading axes, and start
+    on 16-byte places. A weight is laid out so once, for linear_fp4."""
+    lib = _lib or load()
+    dev = _place(x, "x")
+    code = _dtype_code(x)
+    if x.dim() < 1 or x.shape[-1] % 32 != 0 or x.shape[-1] == 0:
+        raise ValueError(f"x must be [..., K] with K a multiple of 32, got {tuple(x.shape)}")
+    lead, K = x.shape[:-1], x.shape[-1]
+    N = lead.numel()
+    _int_sizes("gkd_quantize_fp4", N, K)
+    if codes is None:
+        codes = x.new_empty(lead + (K // 2,), dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty(lead + (K // 32,), dtype=torch.uint8)
+    pc, ps = _codes(dev, codes, scales, x.shape)
+    status = lib.gkd_quantize_fp4(x.data_ptr(), _row_stride(x, "x"), N, K, code, 0, pc, ps,
+                                  _raw_stream(dev))
+    if status:
+        _check(status)
+    return codes, scales
+
+
+def linear_fp4_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of workspace gkd_linear_fp4 needs for these sizes."""
+    _int_sizes("gkd_linear_fp4_workspace_size", M, N, K)
+    return int(load().gkd_linear_fp4_workspace_size(M, N, K))
+
+
+def linear_fp4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias=None,
+               residual=None, act: str = "none", out_dtype=None, out=None,
+               workspace=None) -> torch.Tensor:
+    """act(x @ weight.T + bias) + residual with the weight [N, K] as quantize_fp4
+    leaves it: codes [N, K/2] and scales [N, K/32], uint8. x [..., K] bf16 (rows
+    evenly spaced and on 16-byte places), bias [N] bf16, residual [..., N] in the
+    output's dtype (bf16, or float32 by out_dtype, out or residual) -> [..., N].
+    act, out and workspace as linear's (linear_fp4_workspace_size() bytes)."""
+    lib = _lib or load()
+    dev = _place(x, "x")
+    bf16 = torch.bfloat16
+    if x.dtype != bf16:
+        raise TypeError(f"x must be bfloat16, got {x.dtype}")
+    lead, cshape = x.shape, codes.shape
+    if len(lead) < 1 or len(cshape) != 2 or lead[-1] != 2 * cshape[1]:
+        raise ValueError(f"x must be [..., K] and codes [N, K/2], got {tuple(lead)} and "
+                         f"{tuple(cshape)}")
+    act_code = GKD_ACTS.get(act)
+    if act_code is None:
+        raise ValueError(f"act must be one of {sorted(GKD_ACTS)}")
+    N, K = cshape[0], lead[-1]
+    lead = lead[:-1]
+    M = lead.numel()
+    _int_sizes("gkd_linear_fp4", M, N, K)
+    pc, ps = _codes(dev, codes, scales, (N, K))
+    shape = lead + (N,)
+    if out_dtype is None:
+        out_dtype = (out.dtype if out is not None else
+                     residual.dtype if residual is not None else bf16)
+    if out_dtype != bf16 and out_dtype != torch.float32:
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    if out is None:
+        out = x.new_empty(shape) if out_dtype == bf16 else x.new_empty(shape, dtype=out_dtype)
+        ldo = N
+    else:
+        if out.get_device() != dev:
+            _beside(dev, out, "out")
+        if out.shape != shape or out.dtype != out_dtype:
+            raise ValueError(f"out must be {tuple(shape)} of {out_dtype}")
+        ldo = _row_stride(out, "out")
+    rp = bp = None
+    ldr = 0
+    if residual is not None:
+        if residual.get_device() != dev:
+            _beside(dev, residual, "residual")
+        if residual.shape != shape or residual.dtype != out_dtype:
+            raise ValueError(f"residual must be {tuple(shape)} of {out_dtype}")
+        rp, ldr = residual.data_ptr(), _row_stride(residual, "residual")
+    if bias is not None:
+        bp = _dense(dev, bias, "bias", bf16, (N,))
+    ws, ws_bytes = _workspace(workspace, lib.gkd_linear_fp4_workspace_size(M, N, K), dev)
+    status = lib.gkd_linear_fp4(x.data_ptr(), _row_stride(x, "x"), pc, ps, bp, rp, ldr, M, N, K,
+                                act_code, 1 if out_dtype == bf16 else 0, 0, out.data_ptr(), ldo,
+                                None if ws is None else ws.data_ptr(), ws_bytes, _raw_stream(dev))
+    if status:
+        _check(status)
+    return out
+
+
+def _cache(dev, codes, scales, table):
+    """A cache's sizes (pages, page, Hk, D, L), its arrays' and its table's
+    addresses, and the table's sequences."""
+    shape = codes.shape
+    if len(shape) != 5 or shape[1] != 2:
+        raise ValueError(f"codes must be [pages, 2, Hk, page, D/2], got {tuple(shape)}")
+    if table.dim() != 2:
+        raise ValueError(f"table must be [B, L], got {tuple(table.shape)}")
+    pages, _, Hk, page, half = shape
+    B, L = table.shape
+    pc, ps = _codes(dev, codes, scales, (pages, 2, Hk, page, 2 * half))
+    return (pages, page, Hk, 2 * half, L), (pc, ps), _dense(dev, table, "table", torch.int32,
+                                                           (B, L)), B
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                 table: torch.Tensor, start=None, count=None) -> None:
+    """Quantises new tokens' k and v [B,T,Hk,D] (float32 or bf16, strided views
+    welcome) into a cache's pages: codes [pages, 2, Hk, page, D/2] and scales
+    [pages, 2, Hk, page, D/32], uint8, keys at [:, 0], values at [:, 1]; D 64 or
+    128, page a multiple of 32. Token t < count[b] (int32, default T) of sequence
+    b goes to place start[b] + t (int32, default 0), which is in row place % page
+    of page table[b, place // page] (int32 [B, L]). Places past the table or
+    without a page (an entry outside 0 .. pages - 1) are dropped; two tokens must
+    not have the same place."""
+    lib = _lib or load()
+    dev = _place(k, "k")
+    code = _dtype_code(k)
+    hk, hv = _heads(dev, k, "k", k.dtype), _heads(dev, v, "v", k.dtype)
+    sizes, arrays, pt, B = _cache(dev, codes, scales, table)
+    pages, page, Hk, D, L = sizes
+    T = k.shape[1]
+    if k.shape != (B, T, Hk, D) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{B}, T, {Hk}, {D}], got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    _int_sizes("gkd_cache_append", B, T, *sizes)
+    pst = None if start is None else _dense(dev, start, "start", torch.int32, (B,))
+    pct = None if count is None else _dense(dev, count, "count", torch.int32, (B,))
+    rec = _records
+    at = rec.at
+    _pack_cached(rec.buf, 0, *hk, *hv, *arrays, pages, page, Hk, D)
+    status = lib.gkd_cache_append(at, at + _HEADS_BYTES, B, T, pst, pct, at + 2 * _HEADS_BYTES, pt,
+                                  L, code, 0, _raw_stream(dev))
+    if status:
+        _check(status)
+
+
+def cache_read(codes: torch.Tensor, scales: torch.Tensor, table: torch.Tensor, T: int, start=None,
+               count=None, k_out=None, v_out=None):
+    """A cache's tokens in bfloat16: (k, v) [B,T,Hk,D] with the tokens at places
+    start[b] + t, t < count[b]; zeros where there is no such place or page.
+    Arguments as cache_append's. Tokens past count[b] of a given output stay as
+    they are, those of a new one are zeros."""
+    lib = _lib or load()
+    dev = _place(codes, "codes")
+    bf16 = torch.bfloat16
+    sizes, arrays, pt, B = _cache(dev, codes, scales, table)
+    pages, page, Hk, D, L = sizes
+    _int_sizes("gkd_cache_read", B, T, *sizes)
+    pst = None if start is None else _dense(dev, start, "start", torch.int32, (B,))
+    pct = None if count is None else _dense(dev, count, "count", torch.int32, (B,))
+    new = codes.new_empty if count is None else codes.new_zeros
+    if k_out is None:
+        k_out = new((B, T, Hk, D), dtype=bf16)
+    if v_out is None:
+        v_out = new((B, T, Hk, D), dtype=bf16)
+    hk, hv = _heads(dev, k_out, "k_out", bf16), _heads(dev, v_out, "v_out", bf16)
+    if k_out.shape != (B, T, Hk, D) or v_out.shape != (B, T, Hk, D):
+        raise ValueError(f"k_out and v_out must be {(B, T, Hk, D)}")
+    rec = _records
+    at = rec.at
+    _pack_cached(rec.buf, 0, *hk, *hv, *arrays, pages, page, Hk, D)
+    status = lib.gkd_cache_read(at + 2 * _HEADS_BYTES, pt, L, B, T, pst, pct, 0, at,
+                                at + _HEADS_BYTES, _raw_stream(dev))
+    if status:
+        _check(status)
+    return k_out, v_out
+
+
+def cache_attention_workspace_size(B: int, Tq: int, Hq: int, Hk: int, D: int, page: int,
+                                   L: int) -> int:
+    """Bytes of workspace gkd_cache_attention needs for these sizes."""
+    _int_sizes("gkd_cache_attention_workspace_size", B, Tq, Hq, Hk, D, page, L)
+    return int(load().gkd_cache_attention_workspace_size(B, Tq, Hq, Hk, D, page, L))
+
+
+def cache_attention(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                    table: torch.Tensor, length=None, q_len=None, causal: bool = False, scale=None,
+                    out=None, workspace=None) -> torch.Tensor:
+    """Attention of q [B,Tq,Hq,D] bf16 over the first length[b] (int32, default
+    all L * page) tokens of each sequence's pages in a cache (codes, scales and
+    table as cache_append's). causal: the q_len[b] (int32, default Tq) queries are
+    the last of the length[b] tokens and see those up to their place. Tokens
+    without a page do not count. Queries past q_len[b] are not computed: their
+    rows of a given `out` stay as they are, those of a new one are zeros. scale:
+    default D**-0.5. Returns out [B,Tq,Hq,D]; a query without keys gives zeros."""
+    lib = _lib or load()
+    bf16 = torch.bfloat16
+    dev = _place(q, "q")
+    hq = _heads(dev, q, "q", bf16)
+    sizes, arrays, pt, b = _cache(dev, codes, scales, table)
+    pages, page, Hk, D, L = sizes
+    B, Tq, Hq, d = q.shape
+    if b != B or d != D:
+        raise ValueError(f"q must be [{b}, Tq, Hq, {D}], got {tuple(q.shape)}")
+    _int_sizes("gkd_cache_attention", B, Tq, Hq, *sizes)
+    pl = None if length is None else _dense(dev, length, "length", torch.int32, (B,))
+    pql = None if q_len is None else _dense(dev, q_len, "q_len", torch.int32, (B,))
+    if out is None:
+        out = q.new_empty((B, Tq, Hq, D)) if q_len is None else q.new_zeros((B, Tq, Hq, D))
+    ho = _heads(dev, out, "out", bf16)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ws, ws_bytes = _workspace(workspace, lib.gkd_cache_attention_workspace_size(
+        B, Tq, Hq, Hk, D, page, L), dev)
+    rec = _records
+    at = rec.at
+    _pack_cached(rec.buf, 0, *hq, *ho, *arrays, pages, page, Hk, D)
+    status = lib.gkd_cache_attention(at, at + 2 * _HEADS_BYTES, pt, L, pl, pql, B, Tq, Hq,
+                                     D ** -0.5 if scale is None else scale,
+                                     GKD_ATTN_CAUSAL if causal else 0, at + _HEADS_BYTES,
+                                     None if ws is None else ws.data_ptr(), ws_bytes,
+                                     _raw_stream(dev))
     if status:
         _check(status)
     return out
