@@ -42,6 +42,9 @@ struct CaParams {
 constexpr float kFar = -3e38f;  // a reference point before any key: below every score
 constexpr float kSlack = 8.f;
 
+// Read through the scalar cache: the compiler does not prove that no store changes it.
+typedef const __attribute__((address_space(4))) int32_t const_int;
+
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
@@ -49,168 +52,213 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
-template <int D>
-struct StepCodes;
+// score * scale, rounded, less m: 0 for the score that m is the rounded product of,
+// however far out.
+__device__ __forceinline__ float far_exponent(float score, float scale, float m) {
+#pragma clang fp contract(off)
+  const float t = score * scale;
+  return t - m;
+}
+
 // A step's codes of a lane: of keys fr and 16 + fr the D/4 elements from g D/4, with
 // their group's scale byte; of the values the D/16 elements from fr D/16 of eight
 // keys, with the scale bytes of four neighbouring keys a piece.
-template <>
-struct StepCodes<128> {
-  u32x4 k[2];
+template <int D>
+struct Codes {
+  typedef uint32_t piece __attribute__((ext_vector_type(D / 32)));
+  piece k[2], vs[2];
   uint32_t ks[2], v[8];
-  u32x4 vs[2];
-};
-template <>
-struct StepCodes<64> {
-  u32x2 k[2];
-  uint32_t ks[2], v[8];
-  u32x2 vs[2];
 };
 
+// What a workgroup works on: R tiles of rows from row0, the last one rl, and the steps
+// [s0, s1) of a sequence's keys.
+struct Work {
+  int b, hk, bh, part, row0, rl;
+  int len, tq;  // tokens, queries
+  int all;      // keys that every row sees
+  int s0, s1;
+};
+
+// Few rows: a step's codes are on their way during the whole step before it, in registers
+// of their own. More tiles leave no room for those: keys are read again as soon as they
+// are multiplied, and values likewise, and most rows keep their queries in LDS.
 template <int D, int R, int NW>
-__global__ __launch_bounds__(64 * NW) void cache_attn_kernel(CaParams p) {
+__device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* lds) {
   constexpr int KT = D / 32, DT = D / 16;  // products of a score, tiles of the output
   constexpr int LD = D + 4;
-  extern __shared__ __attribute__((aligned(16))) float lds[];  // [NW][16][LD], [NW][16][2]
+  constexpr bool kAhead = R * D <= 128, kQueriesInLds = R * D > 256;
+  typedef typename Codes<D>::piece piece;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, g = lane >> 4;
-  const ItemCoord at = xcd_item(blockIdx.x, p.tiles);
-  if (at.crop >= p.groups) return;
-  const int part = at.crop % p.parts, bh = at.crop / p.parts;
-  const int b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
-  const int cap = p.c.L * p.c.page;
-  const int len = p.length ? min(max(p.length[b], 0), cap) : cap;
-  const int tq = p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq;
-  const int live = tq * p.G, row0 = at.item * 16 * R;
-  if (row0 >= live) return;
-  const int rl = min(row0 + 16 * R, live) - 1;
-  // keys that the last row sees, and those that every row sees
-  const int last = p.causal ? max(len - tq + rl / p.G + 1, 0) : len;
-  const int all = p.causal ? max(len - tq + row0 / p.G + 1, 0) : len;
-  const int steps = (last + 31) / 32, per = (steps + p.parts - 1) / p.parts;
-  const int s0 = part * per, s1 = min(steps, s0 + per);
+  const float scale = p.scale;
 
-  bf16x8 qf[R][KT];
+  bf16x8 qf[kQueriesInLds ? 1 : R][KT];
+  u32x4* ql = reinterpret_cast<u32x4*>(lds);  // [R][KT][lane]
   int lim[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = min(row0 + 16 * r + fr, rl), t = i / p.G, h = hk * p.G + i - t * p.G;
-    const uint16_t* q = static_cast<const uint16_t*>(p.q.p) + b * p.q.b + t * p.q.t + h * p.q.h + g * (D / 4);
+    const int i = min(w.row0 + 16 * r + fr, w.rl), t = i / p.G, h = w.hk * p.G + i - t * p.G;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q.p) + w.b * p.q.b + t * p.q.t + h * p.q.h + g * (D / 4);
+    if constexpr (kQueriesInLds) {
+      for (int k = wave; k < KT; k += NW) ql[(r * KT + k) * 64 + lane] = *reinterpret_cast<const u32x4*>(q + 8 * k);
+    } else {
 #pragma unroll
-    for (int k = 0; k < KT; ++k) qf[r][k] = frag(*reinterpret_cast<const u32x4*>(q + 8 * k));
-    lim[r] = p.causal ? len - tq + t + 1 : len;
+      for (int k = 0; k < KT; ++k) qf[r][k] = frag(*reinterpret_cast<const u32x4*>(q + 8 * k));
+    }
+    lim[r] = p.causal ? w.len - w.tq + t + 1 : w.len;
   }
+  if constexpr (kQueriesInLds) __syncthreads();
   f32x4 o[R][DT], l[R];
-  float m[R];
+  float m[R], next[R];  // the reference point and the score that moves it
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    m[r] = kFar;
+    m[r] = next[r] = kFar;
     l[r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < DT; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
+  bool far = false;  // some reference point is 2^24 or more out
 
-  // The step's place: page column and row in it.
-  int col = 0, row = (s0 + wave) * 32;
+  int s = w.s0 + wave;
+  int col = 0, row = s * 32;  // the next step's page column and row in the page
   if (row >= p.c.page) {
     col = row / p.c.page;
     row -= col * p.c.page;
   }
-  const int32_t* table = p.c.table + (long long)b * p.c.L;
+  const_int* table = (const_int*)(uintptr_t)(p.c.table + (long long)w.b * p.c.L);
   const long long head_rows = (long long)p.c.Hk * p.c.page;
-  const long long first_row = (long long)hk * p.c.page;
-  int page = s0 + wave < s1 ? table[col] : -1;
+  const uint8_t* kcodes = p.c.codes + w.hk * (long long)p.c.page * (D / 2) + fr * (D / 2) + g * (D / 8);
+  const uint8_t* kscales = p.c.scales + w.hk * (long long)p.c.page * (D / 32) + fr * (D / 32) + (D == 128 ? g : g / 2);
+  const uint8_t* vcodes = p.c.codes + (w.hk * (long long)p.c.page + head_rows) * (D / 2) + g * (2 * D) + fr * (D / 32);
+  const uint8_t* vscales = p.c.scales + (w.hk * (long long)p.c.page + head_rows) * (D / 32) + g * (D / 8);
+  int page = s < w.s1 ? table[col] : -1;
 
-  // Reads step s (at page, row) and moves on to step s + NW. False: it has no page.
-  StepCodes<D> buf[2];
-  auto read = [&](StepCodes<D>& c, int s) -> bool {
-    const bool there = page >= 0 && page < p.c.pages;
-    if (there) {
-      const long long kr = (long long)page * 2 * head_rows + first_row + row, vr = kr + head_rows;
-      const uint8_t* kc = p.c.codes + kr * (D / 2) + fr * (D / 2) + g * (D / 8);
-      const uint8_t* ks = p.c.scales + kr * (D / 32) + fr * (D / 32) + (D == 128 ? g : g / 2);
-      const uint8_t* vc = p.c.codes + vr * (D / 2) + g * (2 * D) + fr * (D / 32);
-      const uint8_t* vs = p.c.scales + vr * (D / 32) + g * (D / 8);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        c.k[i] = *reinterpret_cast<const decltype(c.k[0] + c.k[0])*>(kc + i * 8 * D);
-        c.ks[i] = ks[i * (D / 2)];
-        c.vs[i] = *reinterpret_cast<const decltype(c.vs[0] + c.vs[0])*>(vs + i * (D / 2));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint8_t* a = vc + i * 8 * D + e * (D / 2);
-          c.v[4 * i + e] = D == 128 ? *reinterpret_cast<const uint32_t*>(a) : *reinterpret_cast<const uint16_t*>(a);
-        }
-      }
-    }
-    row += 32 * NW;
-    while (row >= p.c.page) {
-      row -= p.c.page;
-      ++col;
-    }
-    page = s + NW < s1 ? table[col] : -1;
-    return there;
+  // A step's first row among a head's rows of the cache, and whether it has a page
+  // (else page 0 is read, and nothing of it counts). move_on: to step `then` if there
+  // is one, else the same step is read again: loads without a branch around them stay
+  // in flight.
+  struct Place {
+    long long at;
+    bool there;
   };
-
-  auto take = [&](StepCodes<D>& c, int s) {
-    f32x4 st[R][2];
+  auto place = [&]() -> Place {
+    const bool there = page >= 0 && page < p.c.pages;
+    return Place{(long long)(there ? page : 0) * 2 * head_rows + row, there};
+  };
+  auto move_on = [&](int then) {
+    if (then < w.s1) {
+      row += 32 * NW;
+      while (row >= p.c.page) {
+        row -= p.c.page;
+        ++col;
+      }
+      page = table[col];
+    }
+  };
+  auto read_keys = [&](Codes<D>& c, long long at) {
+    const uint8_t* kc = kcodes + at * (D / 2);
+    const uint8_t* ks = kscales + at * (D / 32);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      c.k[i] = *reinterpret_cast<const piece*>(kc + i * 8 * D);
+      c.ks[i] = ks[i * (D / 2)];
+    }
+  };
+  auto read_values = [&](Codes<D>& c, long long at) {
+    const uint8_t* vc = vcodes + at * (D / 2);
+    const uint8_t* vs = vscales + at * (D / 32);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      c.vs[i] = *reinterpret_cast<const piece*>(vs + i * (D / 2));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint8_t* a = vc + i * 8 * D + e * (D / 2);
+        c.v[4 * i + e] = D == 128 ? *reinterpret_cast<const uint32_t*>(a) : *reinterpret_cast<const uint16_t*>(a);
+      }
+    }
+  };
+
+  // S^T of a step
+  auto scores = [&](const Codes<D>& c, f32x4 (&st)[R][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < R; ++r) st[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const bf16x8 kf = frag(fp4_values(c.k[i][k], fp4_unit(c.ks[i])));
+    for (int k = 0; k < KT; ++k) {
+      const bf16x8 k0 = frag(fp4_values(c.k[0][k], fp4_unit(c.ks[0])));
+      const bf16x8 k1 = frag(fp4_values(c.k[1][k], fp4_unit(c.ks[1])));
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          st[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[r][k], st[r][i], 0, 0, 0);
+      for (int r = 0; r < R; ++r) {
+        const bf16x8 q = kQueriesInLds ? frag(ql[(r * KT + k) * 64 + lane]) : qf[kQueriesInLds ? 0 : r][k];
+        st[r][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q, st[r][0], 0, 0, 0);
+        st[r][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q, st[r][1], 0, 0, 0);
       }
     }
-    const int key = 32 * s + 4 * g;  // of place 0; place 4 i + e is 16 i + e further on
-    if (32 * s + 32 > len) {
-      // rows past the last token hold anything: no NaN of theirs may meet a 0
+  };
+  // Keys that a row does not see
+  auto hide = [&](f32x4 (&st)[R][2], int s, bool there) {
+    const int key = (there ? 32 * s : 0x7fffff00) + 4 * g;  // of place 0; place 4 i + e is 16 i + e further on
+#pragma unroll
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (key + 16 * (i / 4) + i % 4 >= len) {
-          c.v[i] = 0;
-          if constexpr (D == 128) c.vs[i / 4][i % 4] = 0;
-          else c.vs[i / 4][i % 4 / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
-        }
-    }
-    u32x4 pf[R];
+        if (key + 16 * (i / 4) + i % 4 >= lim[r]) st[r][i / 4][i % 4] = -INFINITY;
+  };
+  // Rows past the last token hold anything: no NaN of theirs may meet a 0
+  auto clear = [&](Codes<D>& c, int s, bool there) {
+    const int key = (there ? 32 * s : 0x7fffff00) + 4 * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (key + 16 * (i / 4) + i % 4 >= w.len) {
+        c.v[i] = 0;
+        if constexpr (D == 128) c.vs[i / 4][i % 4] = 0;
+        else c.vs[i / 4][i % 4 / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
+      }
+  };
+  // P^T of a step, the row sums with it
+  auto softmax = [&](const f32x4 (&st)[R][2], u32x4 (&pf)[R]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = st[r][i / 4][i % 4] * p.scale;
-      if (32 * s + 32 > all) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (key + 16 * (i / 4) + i % 4 >= lim[r]) x[i] = -INFINITY;
-      }
-      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      if (__any(top > m[r] + kSlack)) {
+      const f32x4 a = st[r][0], b = st[r][1];
+      float top = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])));
+      top *= scale;
+      if (__any(top > next[r])) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float to = top > m[r] + kSlack ? top : m[r];
+        const float to = top > next[r] ? top : m[r];
         const float f = __builtin_amdgcn_exp2f(m[r] - to);
         m[r] = to;
+        next[r] = to + kSlack;
+        far = far || __any(fabsf(to) >= 16777216.f && to != kFar);
         l[r] *= f;
 #pragma unroll
         for (int j = 0; j < DT; ++j) o[r][j] *= f;
       }
+      float x[8];
+      if (far) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pf[r][i] = bf16_pair(__builtin_amdgcn_exp2f(x[2 * i] - m[r]), __builtin_amdgcn_exp2f(x[2 * i + 1] - m[r]));
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(far_exponent(st[r][i / 4][i % 4], scale, m[r]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(st[r][i / 4][i % 4], scale, -m[r]));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pf[r][i] = bf16_pair(x[2 * i], x[2 * i + 1]);
       const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
       l[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(ones), frag(pf[r]), l[r], 0, 0, 0);
     }
-    // elements fr D/16 + (2 h, 2 h + 1) of the eight keys, turned into two operands
+  };
+  // O^T += V^T P^T: elements fr D/16 + (2 h, 2 h + 1) of the eight keys, turned into two
+  // operands. The lane's scale byte of a key is turned to the exponent's place: the
+  // conversions look at nothing else.
+  auto output = [&](const Codes<D>& c, const u32x4 (&pf)[R]) {
     float unit[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if constexpr (D == 128) unit[i] = fp4_unit((c.vs[i / 4][i % 4] >> (8 * (fr / 4))) & 255u);
-      else unit[i] = fp4_unit((c.vs[i / 4][i % 4 / 2] >> (16 * (i % 2) + 8 * (fr / 8))) & 255u);
+      const uint32_t word = D == 128 ? c.vs[i / 4][i % 4] : c.vs[i / 4][i % 4 / 2];
+      const int from = D == 128 ? 8 * (fr / 4) : 16 * (i % 2) + 8 * (fr / 8);
+      unit[i] = __uint_as_float(__builtin_amdgcn_alignbit(word, word, (uint32_t)(from + 9) & 31u));
     }
 #pragma unroll
     for (int h = 0; h < DT / 2; ++h) {
@@ -232,18 +280,60 @@ __global__ __launch_bounds__(64 * NW) void cache_attn_kernel(CaParams p) {
       }
     }
   };
+  auto edges = [&](Codes<D>& c, f32x4 (&st)[R][2], int s, bool there) {
+    const int end = there ? 32 * s + 32 : 0x7fffffff;
+    if (end > w.all) {
+      hide(st, s, there);
+      if (end > w.len) clear(c, s, there);
+    }
+  };
 
-  bool there[2] = {false, false};
-  int s = s0 + wave;
-  if (s < s1) there[0] = read(buf[0], s);
-  for (; s < s1; s += 2 * NW) {
-    if (s + NW < s1) there[1] = read(buf[1], s + NW);
-    if (there[0]) take(buf[0], s);
-    if (s + NW < s1) {
-      if (s + 2 * NW < s1) there[0] = read(buf[0], s + 2 * NW);
-      if (there[1]) take(buf[1], s + NW);
+  if (s < w.s1) {
+    f32x4 st[R][2];
+    u32x4 pf[R];
+    if constexpr (kAhead) {
+      Codes<D> c0, c1;
+      Place a0 = place(), a1 = a0;
+      auto step = [&](Codes<D>& c, Place& a, Codes<D>& cn, Place& an) {
+        an = place();
+        read_keys(cn, an.at);
+        read_values(cn, an.at);
+        move_on(s + 2 * NW);
+        scores(c, st);
+        edges(c, st, s, a.there);
+        softmax(st, pf);
+        output(c, pf);
+        s += NW;
+      };
+      read_keys(c0, a0.at);
+      read_values(c0, a0.at);
+      move_on(s + NW);
+      for (;;) {
+        step(c0, a0, c1, a1);
+        if (s >= w.s1) break;
+        step(c1, a1, c0, a0);
+        if (s >= w.s1) break;
+      }
+    } else {
+      Codes<D> c;
+      Place a = place();
+      read_keys(c, a.at);
+      read_values(c, a.at);
+      move_on(s + NW);
+      for (; s < w.s1; s += NW) {
+        const Place n = place();
+        scores(c, st);
+        read_keys(c, n.at);
+        move_on(s + 2 * NW);
+        edges(c, st, s, a.there);
+        softmax(st, pf);
+        output(c, pf);
+        read_values(c, n.at);
+        a = n;
+      }
     }
   }
+  if constexpr (kQueriesInLds) __syncthreads();
 
   // The waves join, 16 rows at a time.
   constexpr int TPR = 64 * NW / 16, PER = D / TPR;  // threads of a row, elements of a thread
@@ -266,28 +356,28 @@ __global__ __launch_bounds__(64 * NW) void cache_attn_kernel(CaParams p) {
       stat[(wave * 16 + fr) * 2 + 1] = l[r][0];
     }
     __syncthreads();
-    const int i = row0 + 16 * r + jr;
-    if (i > rl) continue;
+    const int i = w.row0 + 16 * r + jr;
+    if (i > w.rl) continue;
     float top = kFar, sum = 0.f, y[PER];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, stat[(w * 16 + jr) * 2]);
+    for (int v = 0; v < NW; ++v) top = fmaxf(top, stat[(v * 16 + jr) * 2]);
 #pragma unroll
     for (int d = 0; d < PER; ++d) y[d] = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float f = __builtin_amdgcn_exp2f(stat[(w * 16 + jr) * 2] - top);
-      sum = fmaf(f, stat[(w * 16 + jr) * 2 + 1], sum);
+    for (int v = 0; v < NW; ++v) {
+      const float f = __builtin_amdgcn_exp2f(stat[(v * 16 + jr) * 2] - top);
+      sum = fmaf(f, stat[(v * 16 + jr) * 2 + 1], sum);
 #pragma unroll
-      for (int d = 0; d < PER; ++d) y[d] = fmaf(f, lds[(w * 16 + jr) * LD + jd + d], y[d]);
+      for (int d = 0; d < PER; ++d) y[d] = fmaf(f, lds[(v * 16 + jr) * LD + jd + d], y[d]);
     }
     if (p.parts == 1) {
-      const int t = i / p.G, h = hk * p.G + i - t * p.G;
-      uint16_t* out = static_cast<uint16_t*>(p.out.p) + b * p.out.b + t * p.out.t + h * p.out.h + jd;
+      const int t = i / p.G, h = w.hk * p.G + i - t * p.G;
+      uint16_t* out = static_cast<uint16_t*>(p.out.p) + w.b * p.out.b + t * p.out.t + h * p.out.h + jd;
       const float f = sum == 0.f ? 0.f : 1.f / sum;  // no key: O is 0
 #pragma unroll
       for (int d = 0; d < PER; d += 2) reinterpret_cast<uint32_t*>(out)[d / 2] = bf16_pair(y[d] * f, y[d + 1] * f);
     } else {
-      const long long at_row = (long long)part * rows + (long long)bh * p.Tq * p.G + i;
+      const long long at_row = (long long)w.part * rows + (long long)w.bh * p.Tq * p.G + i;
 #pragma unroll
       for (int d = 0; d < PER; ++d) p.po[at_row * D + jd + d] = y[d];
       if (jd == 0) {
@@ -296,6 +386,43 @@ __global__ __launch_bounds__(64 * NW) void cache_attn_kernel(CaParams p) {
       }
     }
   }
+}
+
+// A workgroup of R tiles of rows; where the last ones hold no row in use, the work of
+// fewer tiles.
+template <int D, int R, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void cache_attn_kernel(CaParams p) {
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // [NW][16][D + 4], [NW][16][2]
+  const ItemCoord at = xcd_item(blockIdx.x, p.tiles);
+  if (at.crop >= p.groups) return;
+  Work w;
+  w.part = at.crop % p.parts;
+  w.bh = at.crop / p.parts;
+  w.b = w.bh / p.c.Hk;
+  w.hk = w.bh - w.b * p.c.Hk;
+  const int cap = p.c.L * p.c.page;
+  w.len = p.length ? min(max(p.length[w.b], 0), cap) : cap;
+  w.tq = p.q_len ? min(max(p.q_len[w.b], 0), p.Tq) : p.Tq;
+  const int live = w.tq * p.G;
+  w.row0 = at.item * 16 * R;
+  if (w.row0 >= live) return;
+  w.rl = min(w.row0 + 16 * R, live) - 1;
+  const int last = p.causal ? max(w.len - w.tq + w.rl / p.G + 1, 0) : w.len;  // keys that the last row sees
+  w.all = p.causal ? max(w.len - w.tq + w.row0 / p.G + 1, 0) : w.len;
+  const int steps = (last + 31) / 32, per = (steps + p.parts - 1) / p.parts;
+  w.s0 = w.part * per;
+  w.s1 = min(steps, w.s0 + per);
+  const int tiles = (w.rl - w.row0) / 16 + 1;
+  if constexpr (R >= 4) {
+    if (tiles == 3) return attend<D, 3, NW>(p, w, lds);
+  }
+  if constexpr (R >= 3) {
+    if (tiles == 2) return attend<D, 2, NW>(p, w, lds);
+  }
+  if constexpr (R >= 2) {
+    if (tiles == 1) return attend<D, 1, NW>(p, w, lds);
+  }
+  attend<D, R, NW>(p, w, lds);
 }
 
 // Joins the parts of a row, a wave a row.
@@ -344,7 +471,7 @@ constexpr int kMaxParts = 64;  // a lane of the join each
 Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   Plan x;
   const int rows = Tq * (Hq / Hk);
-  x.R = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  x.R = rows <= 16 ? 1 : rows <= 32 ? 2 : D == 128 || rows <= 48 ? 3 : 4;
   x.tiles = (rows + 16 * x.R - 1) / (16 * x.R);
   const long long items = (long long)B * Hk * x.tiles, steps = ((long long)L * page + 31) / 32;
   long long parts = (512 + items - 1) / items;
@@ -371,7 +498,10 @@ hipError_t run(const CaParams& p, hipStream_t st) {
 
 template <int D>
 hipError_t run_rows(const CaParams& p, int R, hipStream_t st) {
-  return R == 1 ? run<D, 1>(p, st) : R == 2 ? run<D, 2>(p, st) : run<D, 4>(p, st);
+  if constexpr (D == 64) {
+    if (R == 4) return run<D, 4>(p, st);
+  }
+  return R == 1 ? run<D, 1>(p, st) : R == 2 ? run<D, 2>(p, st) : run<D, 3>(p, st);
 }
 
 }  // namespace
@@ -390,6 +520,8 @@ hipError_t launch_cache_attn(const CacheAttnArgs& a, hipStream_t st) {
   p.q = a.q;
   p.out = a.out;
   p.c = a.c;
+  // (a step without a page reads the first one; where there is none, no token has a page)
+  if (p.c.pages == 0) p.c.L = 0;
   p.length = a.length;
   p.q_len = a.q_len;
   p.B = a.B;
