@@ -109,10 +109,10 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
   }
   if constexpr (kQueriesInLds) __syncthreads();
   f32x4 o[R][DT], l[R];
-  float m[R], next[R];  // the reference point and the score that moves it
+  float m[R];  // reference points
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    m[r] = next[r] = kFar;
+    m[r] = kFar;
     l[r] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < DT; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -216,35 +216,55 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
         else c.vs[i / 4][i % 4 / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
       }
   };
-  // P^T of a step, the row sums with it
-  auto softmax = [&](const f32x4 (&st)[R][2], u32x4 (&pf)[R]) {
+  // The exponents of a step against the reference points as they are, and the largest
+  // of them (compared as integers: that orders positive ones, which is what counts).
+  auto exponents = [&](const f32x4 (&st)[R][2], f32x4 (&x)[R][2]) -> int {
+    int top = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[r][i / 4][i % 4] = fmaf(st[r][i / 4][i % 4], scale, -m[r]);
+        top = max(top, __float_as_int(x[r][i / 4][i % 4]));
+      }
+    return top;
+  };
+  // Where one passes the slack, its row's reference point moves to the row's largest
+  // score of the step.
+  auto move = [&](const f32x4 (&st)[R][2], f32x4 (&x)[R][2]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const f32x4 a = st[r][0], b = st[r][1];
-      float top = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])));
-      top *= scale;
-      if (__any(top > next[r])) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float to = top > next[r] ? top : m[r];
-        const float f = __builtin_amdgcn_exp2f(m[r] - to);
-        m[r] = to;
-        next[r] = to + kSlack;
-        far = far || __any(fabsf(to) >= 16777216.f && to != kFar);
-        l[r] *= f;
+      float top = st[r][0][0];
 #pragma unroll
-        for (int j = 0; j < DT; ++j) o[r][j] *= f;
-      }
-      float x[8];
-      if (far) {
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, st[r][i / 4][i % 4]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32)) * scale;
+      const float to = top > m[r] + kSlack ? top : m[r];
+      const float f = __builtin_amdgcn_exp2f(m[r] - to);
+      m[r] = to;
+      far = far || __any(fabsf(to) >= 16777216.f && to != kFar);
+      l[r] *= f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(far_exponent(st[r][i / 4][i % 4], scale, m[r]));
-      } else {
+      for (int j = 0; j < DT; ++j) o[r][j] *= f;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(fmaf(st[r][i / 4][i % 4], scale, -m[r]));
-      }
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pf[r][i] = bf16_pair(x[2 * i], x[2 * i + 1]);
+      for (int i = 0; i < 8; ++i)
+        x[r][i / 4][i % 4] = far ? far_exponent(st[r][i / 4][i % 4], scale, m[r])
+                                 : fmaf(st[r][i / 4][i % 4], scale, -m[r]);
+  };
+  // P^T of a step, the row sums with it
+  auto softmax = [&](const f32x4 (&st)[R][2], u32x4 (&pf)[R]) {
+    f32x4 x[R][2];
+    const int top = exponents(st, x);
+    if (far || __any(top > __float_as_int(kSlack))) move(st, x);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pf[r][i] = bf16_pair(__builtin_amdgcn_exp2f(x[r][i / 2][i % 2 * 2]),
+                             __builtin_amdgcn_exp2f(x[r][i / 2][i % 2 * 2 + 1]));
       const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
       l[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(ones), frag(pf[r]), l[r], 0, 0, 0);
     }
