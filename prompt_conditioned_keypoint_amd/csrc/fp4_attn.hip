@@ -34,9 +34,11 @@ struct CaParams {
   int B, Tq, G;
   float scale;      // times log2(e)
   int causal;
-  int tiles, parts, groups;  // tiles of rows, parts of the keys; B Hk parts
-  float* po;        // [parts][B Hk Tq G][D]
-  float* ml;        // [parts][B Hk Tq G][2]
+  int tiles;        // tiles of 16 R rows that a sequence's key head can have
+  int shares;       // workgroups that share the work; 0: each takes a tile with all its keys
+  int32_t* ends;    // [B Hk tiles][2] first and last share of a cut tile; first -1: not cut
+  float* po;        // [shares][2][16 R][D] parts of rows
+  float* ml;        // [shares][2][16 R][2]
 };
 
 constexpr float kFar = -3e38f;  // a reference point before any key: below every score
@@ -44,6 +46,13 @@ constexpr float kSlack = 8.f;
 
 // Read through the scalar cache: the compiler does not prove that no store changes it.
 typedef const __attribute__((address_space(4))) int32_t const_int;
+__device__ __forceinline__ const_int* scalar(const int32_t* p) { return (const_int*)(uintptr_t)p; }
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ long long uniform(long long v) {
+  const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(v >> 32));
+  return (long long)((unsigned long long)hi << 32 | lo);
+}
 
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
@@ -70,25 +79,90 @@ struct Codes {
   uint32_t ks[2], v[8];
 };
 
-// What a workgroup works on: R tiles of rows from row0, the last one rl, and the steps
-// [s0, s1) of a sequence's keys.
+// A sequence's work: `tiles` tiles of `sub` times 16 rows of each key head, `steps`
+// steps of keys each. A step is taken to cost 3 + sub: its conversions beside the
+// products and exponents of its rows.
+struct Sequence {
+  int len, tq, live, tiles, sub, steps;
+  __device__ int weight() const { return 3 + sub; }
+  __device__ long long tile_work() const { return (long long)steps * weight(); }
+};
+
+template <int R>
+__device__ __forceinline__ Sequence sequence(const CaParams& p, int b) {
+  Sequence q;
+  const int cap = p.c.L * p.c.page;
+  q.len = p.length ? min(max(scalar(p.length)[b], 0), cap) : cap;
+  q.tq = p.q_len ? min(max(scalar(p.q_len)[b], 0), p.Tq) : p.Tq;
+  q.live = q.tq * p.G;
+  const int subs = (q.live + 15) / 16;
+  q.tiles = (subs + R - 1) / R;
+  q.sub = q.tiles > 0 ? (subs + q.tiles - 1) / q.tiles : 1;  // spread evenly
+  q.steps = (q.len + 31) / 32;
+  return q;
+}
+
+// The work is cut into `n` equal shares; where share i begins.
+__device__ __forceinline__ long long share_begin(long long total, int n, int i) {
+  const long long q = total / n;
+  return q * i + (total - q * n) * i / n;
+}
+
+// The steps of a tile that begins at `tile` which lie before `at`: a step belongs to the
+// share that holds its first unit of work.
+__device__ __forceinline__ int steps_before(const Sequence& q, long long tile, long long at) {
+  if (at <= tile) return 0;
+  const long long n = (at - tile + q.weight() - 1) / q.weight();
+  return (int)min(n, (long long)q.steps);
+}
+
+// No share is worth having below two steps a wave (and one holds more than a step, which
+// costs 7 at most: the join counts on that).
+template <int NW>
+__device__ __forceinline__ int share_count(const CaParams& p, long long total) {
+  return (int)min((long long)p.shares, total / (2 * NW * 4) + 1);
+}
+
+// What a workgroup works on: rows row0 .. rl of a key head, and the steps [s0, s1) of
+// the sequence's keys; `part`: -1 where these are all its keys, else where the partial
+// results go.
 struct Work {
-  int b, hk, bh, part, row0, rl;
+  int b, hk, row0, rl;
   int len, tq;  // tokens, queries
   int all;      // keys that every row sees
-  int s0, s1;
+  int s0, s1, part;
 };
+
+template <int R>
+__device__ __forceinline__ Work work_of(const CaParams& p, const Sequence& q, int b, int hk, int tile, int s0, int s1,
+                                        int part) {
+  Work w;
+  w.b = b;
+  w.hk = hk;
+  w.row0 = tile * 16 * q.sub;
+  w.rl = min(w.row0 + 16 * q.sub, q.live) - 1;
+  w.len = q.len;
+  w.tq = q.tq;
+  w.all = p.causal ? max(q.len - q.tq + w.row0 / p.G + 1, 0) : q.len;
+  const int last = p.causal ? max(q.len - q.tq + w.rl / p.G + 1, 0) : q.len;  // keys that the last row sees
+  w.s0 = s0;
+  w.s1 = min(s1, (last + 31) / 32);
+  w.part = part;
+  return w;
+}
 
 // Few rows: a step's codes are on their way during the whole step before it, in registers
 // of their own. More tiles leave no room for those: keys are read again as soon as they
 // are multiplied, and values likewise, and most rows keep their queries in LDS.
-template <int D, int R, int NW>
+template <int D, int R, int NW, int RMAX>
 __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* lds) {
   constexpr int KT = D / 32, DT = D / 16;  // products of a score, tiles of the output
   constexpr int LD = D + 4;
   constexpr bool kAhead = R * D <= 128, kQueriesInLds = R * D > 256;
   typedef typename Codes<D>::piece piece;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int thread = threadIdx.x;
+  asm volatile("" : "+v"(thread));  // what follows from it is not kept in registers from tile to tile
+  const int lane = thread & 63, wave = uniform(thread >> 6);
   const int fr = lane & 15, g = lane >> 4;
   const float scale = p.scale;
 
@@ -125,7 +199,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
     col = row / p.c.page;
     row -= col * p.c.page;
   }
-  const_int* table = (const_int*)(uintptr_t)(p.c.table + (long long)w.b * p.c.L);
+  const_int* table = scalar(p.c.table + (long long)w.b * p.c.L);
   const long long head_rows = (long long)p.c.Hk * p.c.page;
   const uint8_t* kcodes = p.c.codes + w.hk * (long long)p.c.page * (D / 2) + fr * (D / 2) + g * (D / 8);
   const uint8_t* kscales = p.c.scales + w.hk * (long long)p.c.page * (D / 32) + fr * (D / 32) + (D == 128 ? g : g / 2);
@@ -358,8 +432,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
   // The waves join, 16 rows at a time.
   constexpr int TPR = 64 * NW / 16, PER = D / TPR;  // threads of a row, elements of a thread
   float* stat = lds + NW * 16 * LD;
-  const int jr = threadIdx.x / TPR, jd = threadIdx.x % TPR * PER;
-  const long long rows = (long long)p.B * p.c.Hk * p.Tq * p.G;
+  const int jr = thread / TPR, jd = thread % TPR * PER;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (r > 0) __syncthreads();
@@ -390,129 +463,296 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
 #pragma unroll
       for (int d = 0; d < PER; ++d) y[d] = fmaf(f, lds[(v * 16 + jr) * LD + jd + d], y[d]);
     }
-    if (p.parts == 1) {
+    if (w.part < 0) {
       const int t = i / p.G, h = w.hk * p.G + i - t * p.G;
       uint16_t* out = static_cast<uint16_t*>(p.out.p) + w.b * p.out.b + t * p.out.t + h * p.out.h + jd;
       const float f = sum == 0.f ? 0.f : 1.f / sum;  // no key: O is 0
 #pragma unroll
       for (int d = 0; d < PER; d += 2) reinterpret_cast<uint32_t*>(out)[d / 2] = bf16_pair(y[d] * f, y[d + 1] * f);
     } else {
-      const long long at_row = (long long)w.part * rows + (long long)w.bh * p.Tq * p.G + i;
+      const long long at = (long long)w.part * (16 * RMAX) + 16 * r + jr;
 #pragma unroll
-      for (int d = 0; d < PER; ++d) p.po[at_row * D + jd + d] = y[d];
+      for (int d = 0; d < PER; ++d) p.po[at * D + jd + d] = y[d];
       if (jd == 0) {
-        p.ml[at_row * 2] = top;
-        p.ml[at_row * 2 + 1] = sum;
+        p.ml[at * 2] = top;
+        p.ml[at * 2 + 1] = sum;
       }
     }
   }
 }
 
-// A workgroup of R tiles of rows; where the last ones hold no row in use, the work of
-// fewer tiles.
+// A tile of up to R times 16 rows.
 template <int D, int R, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void cache_attn_kernel(CaParams p) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];  // [NW][16][D + 4], [NW][16][2]
-  const ItemCoord at = xcd_item(blockIdx.x, p.tiles);
-  if (at.crop >= p.groups) return;
-  Work w;
-  w.part = at.crop % p.parts;
-  w.bh = at.crop / p.parts;
-  w.b = w.bh / p.c.Hk;
-  w.hk = w.bh - w.b * p.c.Hk;
-  const int cap = p.c.L * p.c.page;
-  w.len = p.length ? min(max(p.length[w.b], 0), cap) : cap;
-  w.tq = p.q_len ? min(max(p.q_len[w.b], 0), p.Tq) : p.Tq;
-  const int live = w.tq * p.G;
-  w.row0 = at.item * 16 * R;
-  if (w.row0 >= live) return;
-  w.rl = min(w.row0 + 16 * R, live) - 1;
-  const int last = p.causal ? max(w.len - w.tq + w.rl / p.G + 1, 0) : w.len;  // keys that the last row sees
-  w.all = p.causal ? max(w.len - w.tq + w.row0 / p.G + 1, 0) : w.len;
-  const int steps = (last + 31) / 32, per = (steps + p.parts - 1) / p.parts;
-  w.s0 = w.part * per;
-  w.s1 = min(steps, w.s0 + per);
+__device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, float* lds) {
   const int tiles = (w.rl - w.row0) / 16 + 1;
   if constexpr (R >= 4) {
-    if (tiles == 3) return attend<D, 3, NW>(p, w, lds);
+    if (tiles == 3) return attend<D, 3, NW, R>(p, w, lds);
   }
   if constexpr (R >= 3) {
-    if (tiles == 2) return attend<D, 2, NW>(p, w, lds);
+    if (tiles == 2) return attend<D, 2, NW, R>(p, w, lds);
   }
   if constexpr (R >= 2) {
-    if (tiles == 1) return attend<D, 1, NW>(p, w, lds);
+    if (tiles == 1) return attend<D, 1, NW, R>(p, w, lds);
   }
-  attend<D, R, NW>(p, w, lds);
+  attend<D, R, NW, R>(p, w, lds);
 }
 
-// Joins the parts of a row, a wave a row.
-template <int D>
+// Waves a SIMD that the registers are shared out to.
+constexpr int waves_of(int D, int R) { return R > 1 ? 2 : D == 128 ? 3 : 4; }
+
+constexpr int kMaxSequences = 1024;  // whose work is shared evenly
+
+// A workgroup a tile, with all its keys.
+template <int D, int R, int NW>
+__global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_attn_kernel(CaParams p) {
+  extern __shared__ __attribute__((aligned(16))) float lds[];  // [NW][16][D + 4], [NW][16][2]
+  const ItemCoord at = xcd_item(blockIdx.x, p.tiles);
+  if (at.crop >= p.B * p.c.Hk) return;
+  const int b = at.crop / p.c.Hk;
+  const Sequence q = sequence<R>(p, b);
+  if (at.item >= q.tiles) return;
+  attend_tile<D, R, NW>(p, work_of<R>(p, q, b, at.crop - b * p.c.Hk, at.item, 0, q.steps, -1), lds);
+}
+
+// The next pieces of the workgroup's share, after those before state[1], state[2] (-1: from
+// its begin; and left so when they are all listed).
+constexpr int kPieces = 32;
+
+template <int R, int NW>
+__device__ __forceinline__ void list_pieces(const CaParams& p, const long long* cum, int32_t (*piece)[4],
+                                            int32_t* state) {
+  const bool first = threadIdx.x == 0;
+  int n = 0, b = uniform(state[1]), tile = uniform(state[2]);
+  const long long total = uniform(cum[p.B]);
+  const int shares = uniform(share_count<NW>(p, total));
+  const bool any = (int)blockIdx.x < shares && total > 0;
+  // neighbouring shares, which read the same keys, on one XCD
+  const int x = blockIdx.x % kXcds, share = x * (shares / kXcds) + min(x, shares % kXcds) + blockIdx.x / kXcds;
+  const long long begin = any ? uniform(share_begin(total, shares, share)) : 0;
+  const long long end = any ? uniform(share_begin(total, shares, share + 1)) : 0;
+  if (any && b < 0) {
+    int hi = p.B;  // cum[b] <= begin < cum[hi]
+    b = 0;
+    while (hi - b > 1) {
+      const int mid = (b + hi) / 2;
+      if (uniform(cum[mid]) <= begin) b = mid;
+      else hi = mid;
+    }
+  }
+  for (; any && b < p.B; ++b, tile = -1) {
+    const long long base = uniform(cum[b]);
+    if (base >= end) break;
+    const Sequence q = sequence<R>(p, b);
+    const long long per = q.tile_work();
+    if (per == 0 || q.tiles == 0) continue;
+    if (tile < 0) tile = begin > base ? uniform((int)((begin - base) / per)) : 0;
+    for (; tile < q.tiles * p.c.Hk && n < kPieces; ++tile) {
+      const long long at = base + tile * per;
+      if (at >= end) break;
+      const int s0 = uniform(steps_before(q, at, begin)), s1 = uniform(steps_before(q, at, end));
+      if (s0 >= s1) continue;
+      if (first) {
+        piece[n][0] = b;
+        piece[n][1] = tile;
+        piece[n][2] = s0;
+        piece[n][3] = s1;
+        const int hk = tile / q.tiles;
+        int32_t* ends = p.ends + (((long long)b * p.c.Hk + hk) * p.tiles + tile - hk * q.tiles) * 2;
+        if (s0 == 0) ends[0] = s1 == q.steps ? -1 : share;
+        if (s1 == q.steps) ends[1] = share;
+      }
+      ++n;
+    }
+    if (n == kPieces) break;
+  }
+  if (first) {
+    state[0] = n;
+    state[1] = n == kPieces ? b : -1;
+    state[2] = tile;
+    state[3] = share;
+  }
+}
+
+// An equal share of all steps a workgroup: the sequences' tiles stand one after another,
+// and a share may begin and end within a tile. What it holds of such tiles goes to two
+// places of its own: the tile that it begins within to the first, the one that it leaves
+// unfinished to the second.
+template <int D, int R, int NW>
+__global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(CaParams p) {
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  __shared__ long long cum[kMaxSequences + 1];
+  __shared__ int32_t piece[kPieces][4];  // sequence, tile of it, first step, end
+  __shared__ int32_t state[4];           // pieces, where to go on (sequence, tile), the share
+  for (int b = threadIdx.x; b < p.B; b += 64 * NW) {
+    const Sequence q = sequence<R>(p, b);
+    cum[b + 1] = q.tile_work() * q.tiles * p.c.Hk;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    long long sum = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64) {
+      const int b = b0 + threadIdx.x;
+      long long v = b < p.B ? cum[b + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const long long u = __shfl_up(v, d);
+        if ((int)threadIdx.x >= d) v += u;
+      }
+      if (b < p.B) cum[b + 1] = sum + v;
+      sum += __shfl(v, 63);
+    }
+    if (threadIdx.x == 0) {
+      cum[0] = 0;
+      state[1] = state[2] = -1;
+    }
+  }
+  __syncthreads();
+  // Wave 0 lists the share's pieces, some at a time, so that nothing of the sharing stays
+  // in registers while they are worked on.
+  for (;;) {
+    if (threadIdx.x < 64) list_pieces<R, NW>(p, cum, piece, state);
+    __syncthreads();
+    const int n = uniform(state[0]);
+    for (int k = 0; k < n; ++k) {
+      const int b = uniform(piece[k][0]), at = uniform(piece[k][1]), s0 = uniform(piece[k][2]), s1 = uniform(piece[k][3]);
+      const Sequence q = sequence<R>(p, b);
+      const int hk = uniform(at / q.tiles), share = uniform(state[3]);
+      if (k > 0) __syncthreads();
+      attend_tile<D, R, NW>(p, work_of<R>(p, q, b, hk, at - hk * q.tiles, s0, s1,
+                                          s0 == 0 && s1 == q.steps ? -1 : 2 * share + (s0 == 0 ? 1 : 0)), lds);
+    }
+    __syncthreads();
+    if (uniform(state[1]) < 0) break;
+  }
+}
+
+// Rows whose tiles were cut, and zeros for rows without a key. The parts of a tile lie in
+// the second place of its first share and the first place of every one after it (a share
+// holds more than a step, so none between them is empty). D/4 lanes take a row, four
+// elements each; with FEW all of a workgroup's lanes take one row, its parts dealt to
+// them in turn.
+template <int D, int R, bool FEW>
 __global__ __launch_bounds__(256) void cache_join_kernel(CaParams p) {
-  constexpr int PER = D / 64;
-  const int lane = threadIdx.x & 63;
+  constexpr int GL = D / 4, GROUPS = 256 / GL;
+  __shared__ f32x4 part[FEW ? GROUPS : 1][GL];
+  __shared__ float stat[FEW ? GROUPS : 1][2];
+  const int lane = threadIdx.x % GL, group = threadIdx.x / GL;
   const int per = p.Tq * p.G;
-  const long long rows = (long long)p.B * p.c.Hk * per;
-  const long long at = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= rows) return;
+  const long long rows = (long long)p.B * p.c.Hk * per, at = FEW ? blockIdx.x : (long long)blockIdx.x * GROUPS + group;
+  if (at >= rows) return;  // (FEW: never)
   const int bh = (int)(at / per), i = (int)(at - (long long)bh * per);
   const int b = bh / p.c.Hk, hk = bh - b * p.c.Hk, t = i / p.G, h = hk * p.G + i - t * p.G;
-  if (p.q_len && t >= p.q_len[b]) return;
+  const int cap = p.c.L * p.c.page;
+  const int len = p.length ? min(max(p.length[b], 0), cap) : cap;
+  const int live = (p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq) * p.G;
+  if (i >= live) return;
+  const int subs = (live + 15) / 16, tiles = (subs + R - 1) / R, sub = (subs + tiles - 1) / tiles;
+  const int tile = i / (16 * sub), r = i - tile * 16 * sub;
   float m = kFar, l = 0.f;
-  if (lane < p.parts) {
-    m = p.ml[(lane * rows + at) * 2];
-    l = p.ml[(lane * rows + at) * 2 + 1];
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  if (len > 0) {
+    const int32_t* ends = p.ends + ((long long)bh * p.tiles + tile) * 2;
+    const int first = ends[0], n = ends[1] - first + 1;
+    if (first < 0) return;  // written as it is
+    auto slot = [&](int k) { return (long long)(2 * (first + k) + (k == 0 ? 1 : 0)) * (16 * R) + r; };
+    constexpr int STEP = FEW ? GROUPS : 1, BATCH = 8;
+    for (int k0 = FEW ? group : 0; k0 < n; k0 += BATCH * STEP) {
+      float pm[BATCH], pl[BATCH];
+      f32x4 v[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int x = k0 + k * STEP;
+        const long long from = slot(x < n ? x : k0);
+        pm[k] = x < n ? p.ml[from * 2] : kFar;
+        pl[k] = x < n ? p.ml[from * 2 + 1] : 0.f;
+        v[k] = reinterpret_cast<const f32x4*>(p.po + from * D)[lane];
+      }
+      float to = m;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) to = fmaxf(to, pm[k]);
+      const float f = __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= f;
+      y *= f;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const float g = k0 + k * STEP < n ? __builtin_amdgcn_exp2f(pm[k] - to) : 0.f;
+        l = fmaf(pl[k], g, l);
+        y += v[k] * g;
+      }
+    }
   }
-  float top = m;
-#pragma unroll
-  for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const float f = __builtin_amdgcn_exp2f(m - top);
-  const float sum = wave_sum(f * l);
-  float y[PER];
-#pragma unroll
-  for (int d = 0; d < PER; ++d) y[d] = 0.f;
-  for (int x = 0; x < p.parts; ++x) {
-    const float fx = __shfl(f, x);
-#pragma unroll
-    for (int d = 0; d < PER; ++d) y[d] = fmaf(fx, p.po[(x * rows + at) * D + lane * PER + d], y[d]);
+  if constexpr (FEW) {
+    part[group][lane] = y;
+    if (lane == 0) {
+      stat[group][0] = m;
+      stat[group][1] = l;
+    }
+    __syncthreads();
+    if (group > 0) return;
+    float to = m;
+    for (int k = 1; k < GROUPS; ++k) to = fmaxf(to, stat[k][0]);
+    const float f = __builtin_amdgcn_exp2f(m - to);
+    l *= f;
+    y *= f;
+    for (int k = 1; k < GROUPS; ++k) {
+      const float g = __builtin_amdgcn_exp2f(stat[k][0] - to);
+      l = fmaf(stat[k][1], g, l);
+      y += part[k][lane] * g;
+    }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* out = static_cast<uint16_t*>(p.out.p) + b * p.out.b + t * p.out.t + h * p.out.h + lane * PER;
-  if constexpr (PER == 2) *reinterpret_cast<uint32_t*>(out) = bf16_pair(y[0] * inv, y[1] * inv);
-  else *out = f32_to_bf16_bits(y[0] * inv);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint16_t* out = static_cast<uint16_t*>(p.out.p) + b * p.out.b + t * p.out.t + h * p.out.h + lane * 4;
+  *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv)};
 }
 
 struct Plan {
-  int R, tiles, parts;
+  int R, tiles;
+  int shares;  // 0: a workgroup a tile
 };
 
 constexpr int kWaves = 4;
-constexpr int kMaxParts = 64;  // a lane of the join each
 
+// R: as many tiles of 16 rows as two waves a SIMD have registers for. Work is shared where
+// there are neither enough tiles for the card nor so few keys that joining would take longer.
 Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   Plan x;
   const int rows = Tq * (Hq / Hk);
   x.R = rows <= 16 ? 1 : rows <= 32 ? 2 : D == 128 || rows <= 48 ? 3 : 4;
   x.tiles = (rows + 16 * x.R - 1) / (16 * x.R);
   const long long items = (long long)B * Hk * x.tiles, steps = ((long long)L * page + 31) / 32;
-  long long parts = (512 + items - 1) / items;
-  const long long most = steps / (2 * kWaves);
-  if (parts > most) parts = most;
-  if (parts > kMaxParts) parts = kMaxParts;
-  x.parts = parts < 1 ? 1 : (int)parts;
+  const int resident = x.R > 1 ? 512 : D == 128 ? 768 : 1024;
+  x.shares = 0;
+  if (B <= kMaxSequences && items < 4 * resident && steps > 4 * kWaves) {
+    const long long most = items * steps / (2 * kWaves);
+    x.shares = most < resident ? (int)most : resident;
+  }
   return x;
 }
 
 size_t al256(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t ends_bytes(const Plan& x, int B, int Hk) { return al256((size_t)B * Hk * x.tiles * 8); }
+size_t po_bytes(const Plan& x, int D) { return al256((size_t)x.shares * 2 * 16 * x.R * D * 4); }
 
 template <int D, int R>
 hipError_t run(const CaParams& p, hipStream_t st) {
-  const long long groups8 = ((long long)p.groups + kXcds - 1) / kXcds * kXcds;
-  hipLaunchKernelGGL((cache_attn_kernel<D, R, kWaves>), dim3((unsigned)(groups8 * p.tiles)), dim3(64 * kWaves),
-                     kWaves * 16 * (D + 4 + 2) * 4, st, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.parts == 1) return e;
+  constexpr int kLds = kWaves * 16 * (D + 4 + 2) * 4;
+  if (p.shares == 0) {
+    const long long groups8 = ((long long)p.B * p.c.Hk + kXcds - 1) / kXcds * kXcds;
+    hipLaunchKernelGGL((cache_attn_kernel<D, R, kWaves>), dim3((unsigned)(groups8 * p.tiles)), dim3(64 * kWaves), kLds,
+                       st, p);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((cache_share_kernel<D, R, kWaves>), dim3((unsigned)p.shares), dim3(64 * kWaves), kLds, st, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   const long long rows = (long long)p.B * p.c.Hk * p.Tq * p.G;
-  hipLaunchKernelGGL(cache_join_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, p);
+  constexpr int kRows = 1024 / D;  // of a workgroup
+  if (rows <= 512)
+    hipLaunchKernelGGL((cache_join_kernel<D, R, true>), dim3((unsigned)rows), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((cache_join_kernel<D, R, false>), dim3((unsigned)((rows + kRows - 1) / kRows)), dim3(256), 0, st,
+                       p);
   return hipGetLastError();
 }
 
@@ -528,9 +768,8 @@ hipError_t run_rows(const CaParams& p, int R, hipStream_t st) {
 
 size_t cache_attn_workspace_bytes(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   const Plan x = plan_for(B, Tq, Hq, Hk, D, page, L);
-  if (x.parts == 1) return 0;
-  const size_t rows = (size_t)B * Tq * Hq;
-  return al256(x.parts * rows * D * 4) + al256(x.parts * rows * 8);
+  if (x.shares == 0) return 0;
+  return ends_bytes(x, B, Hk) + po_bytes(x, D) + al256((size_t)x.shares * 2 * 16 * x.R * 8);
 }
 
 hipError_t launch_cache_attn(const CacheAttnArgs& a, hipStream_t st) {
@@ -550,11 +789,14 @@ hipError_t launch_cache_attn(const CacheAttnArgs& a, hipStream_t st) {
   p.scale = a.scale * 1.4426950408889634f;
   p.causal = a.causal;
   p.tiles = x.tiles;
-  p.parts = x.parts;
-  p.groups = a.B * a.c.Hk * x.parts;
-  const size_t rows = (size_t)a.B * a.Tq * a.Hq;
-  p.po = static_cast<float*>(a.ws);
-  if (x.parts > 1) p.ml = p.po + al256(x.parts * rows * a.c.D * 4) / 4;
+  p.shares = x.shares;
+  if (x.shares > 0) {
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    p.ends = reinterpret_cast<int32_t*>(ws);
+    ws += ends_bytes(x, a.B, a.c.Hk);
+    p.po = reinterpret_cast<float*>(ws);
+    p.ml = reinterpret_cast<float*>(ws + po_bytes(x, a.c.D));
+  }
   return a.c.D == 128 ? run_rows<128>(p, x.R, st) : run_rows<64>(p, x.R, st);
 }
 
