@@ -43,6 +43,10 @@ struct CaParams {
 
 constexpr float kFar = -3e38f;  // a reference point before any key: below every score
 constexpr float kSlack = 8.f;
+constexpr int kStages = 2;      // of a wave's ring
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void glb_void;
 
 // Read through the scalar cache: the compiler does not prove that no store changes it.
 typedef const __attribute__((address_space(4))) int32_t const_int;
@@ -69,15 +73,26 @@ __device__ __forceinline__ float far_exponent(float score, float scale, float m)
   return t - m;
 }
 
-// A step's codes of a lane: of keys fr and 16 + fr the D/4 elements from g D/4, with
-// their group's scale byte; of the values the D/16 elements from fr D/16 of eight
-// keys, with the scale bytes of four neighbouring keys a piece.
+// A step's place in a wave's ring in LDS: the codes of 32 keys, those of their values,
+// and the scale bytes of both. LDS has 64 banks of 4 bytes, a row of codes is D/2 bytes,
+// and rows are placed so that no reading below meets itself in a bank:
+//   keys     16-byte piece c of row r at piece c ^ (r / 4) % 4 (D 64: c ^ (r / 8) % 2), for
+//            lanes that read the same piece of 16 rows;
+//   values   row 4 g + e of 16 at row 4 g + (e ^ g) (D 64: e ^ (g & 2)), for lanes that
+//            read all of the rows 4 g + e, g = 0 .. 3.
+// Loads go straight to LDS, so it is the lanes' global addresses that are permuted.
 template <int D>
-struct Codes {
-  typedef uint32_t piece __attribute__((ext_vector_type(D / 32)));
-  piece k[2], vs[2];
-  uint32_t ks[2], v[8];
+struct Stage {
+  static constexpr int kCodes = 32 * D / 2, kValues = kCodes, kScales = 2 * kCodes;
+  static constexpr int kBytes = 2 * kCodes + 256, kLoads = D == 128 ? 5 : 3;
 };
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N), the other counters left alone
+  asm volatile("" ::: "memory");
+}
 
 // A sequence's work: `tiles` tiles of `sub` times 16 rows of each key head, `steps`
 // steps of keys each. A step is taken to cost 3 + sub: its conversions beside the
@@ -151,37 +166,29 @@ __device__ __forceinline__ Work work_of(const CaParams& p, const Sequence& q, in
   return w;
 }
 
-// Few rows: a step's codes are on their way during the whole step before it, in registers
-// of their own. More tiles leave no room for those: keys are read again as soon as they
-// are multiplied, and values likewise, and most rows keep their queries in LDS.
+// R tiles of 16 rows against the steps of `w`, the waves taking turns at them.
 template <int D, int R, int NW, int RMAX>
-__device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* lds) {
+__device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigned char* lds) {
   constexpr int KT = D / 32, DT = D / 16;  // products of a score, tiles of the output
   constexpr int LD = D + 4;
-  constexpr bool kAhead = R * D <= 128, kQueriesInLds = R * D > 256;
-  typedef typename Codes<D>::piece piece;
+  typedef Stage<D> St;
+  typedef uint32_t piece __attribute__((ext_vector_type(D / 32)));
   int thread = threadIdx.x;
   asm volatile("" : "+v"(thread));  // what follows from it is not kept in registers from tile to tile
   const int lane = thread & 63, wave = uniform(thread >> 6);
   const int fr = lane & 15, g = lane >> 4;
   const float scale = p.scale;
 
-  bf16x8 qf[kQueriesInLds ? 1 : R][KT];
-  u32x4* ql = reinterpret_cast<u32x4*>(lds);  // [R][KT][lane]
+  bf16x8 qf[R][KT];
   int lim[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int i = min(w.row0 + 16 * r + fr, w.rl), t = i / p.G, h = w.hk * p.G + i - t * p.G;
     const uint16_t* q = static_cast<const uint16_t*>(p.q.p) + w.b * p.q.b + t * p.q.t + h * p.q.h + g * (D / 4);
-    if constexpr (kQueriesInLds) {
-      for (int k = wave; k < KT; k += NW) ql[(r * KT + k) * 64 + lane] = *reinterpret_cast<const u32x4*>(q + 8 * k);
-    } else {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) qf[r][k] = frag(*reinterpret_cast<const u32x4*>(q + 8 * k));
-    }
+    for (int k = 0; k < KT; ++k) qf[r][k] = frag(*reinterpret_cast<const u32x4*>(q + 8 * k));
     lim[r] = p.causal ? w.len - w.tq + t + 1 : w.len;
   }
-  if constexpr (kQueriesInLds) __syncthreads();
   f32x4 o[R][DT], l[R];
   float m[R];  // reference points
 #pragma unroll
@@ -200,26 +207,34 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
     row -= col * p.c.page;
   }
   const_int* table = scalar(p.c.table + (long long)w.b * p.c.L);
-  const long long head_rows = (long long)p.c.Hk * p.c.page;
-  const uint8_t* kcodes = p.c.codes + w.hk * (long long)p.c.page * (D / 2) + fr * (D / 2) + g * (D / 8);
-  const uint8_t* kscales = p.c.scales + w.hk * (long long)p.c.page * (D / 32) + fr * (D / 32) + (D == 128 ? g : g / 2);
-  const uint8_t* vcodes = p.c.codes + (w.hk * (long long)p.c.page + head_rows) * (D / 2) + g * (2 * D) + fr * (D / 32);
-  const uint8_t* vscales = p.c.scales + (w.hk * (long long)p.c.page + head_rows) * (D / 32) + g * (D / 8);
+  const long long head_rows = (long long)p.c.Hk * p.c.page, first_row = w.hk * (long long)p.c.page;
   int page = s < w.s1 ? table[col] : -1;
 
-  // A step's first row among a head's rows of the cache, and whether it has a page
-  // (else page 0 is read, and nothing of it counts). move_on: to step `then` if there
-  // is one, else the same step is read again: loads without a branch around them stay
-  // in flight.
-  struct Place {
-    long long at;
-    bool there;
-  };
-  auto place = [&]() -> Place {
+  // What a lane loads of a step, 16 bytes of codes and 4 of scales at a time.
+  constexpr int PR = D / 32;  // 16-byte pieces of a row
+  const int lr = lane / PR, lc = lane % PR;
+  const int kc = lc ^ (D == 128 ? (lr >> 2) & 3 : (lr >> 3) & 1);
+  const int vr = (lr & ~3) | ((lr & 3) ^ (D == 128 ? (lr >> 2) & 3 : (lr >> 2) & 2));
+  const uint8_t* kcodes = p.c.codes + first_row * (D / 2) + lr * (D / 2) + kc * 16;
+  const uint8_t* vcodes = p.c.codes + (first_row + head_rows) * (D / 2) + vr * (D / 2) + lc * 16;
+  const int ls = lane % (2 * D / 4), half = ls >= D / 4;  // D / 4 lanes for the keys' scales, as many for the values'
+  const uint8_t* scales = p.c.scales + (first_row + (half ? head_rows : 0)) * (D / 32) + (ls - half * (D / 4)) * 4;
+
+  // Loads the next step to a stage and moves on, to step `then` if there is one; else the
+  // same step is loaded again, so that as many loads are under way as are waited for.
+  // False: the step has no page (page 0 is loaded, and nothing of it counts).
+  unsigned char* ring = lds + wave * kStages * St::kBytes;
+  auto load = [&](int stage, int then) -> bool {
     const bool there = page >= 0 && page < p.c.pages;
-    return Place{(long long)(there ? page : 0) * 2 * head_rows + row, there};
-  };
-  auto move_on = [&](int then) {
+    const long long at = (long long)(there ? page : 0) * 2 * head_rows + row;
+    unsigned char* dst = ring + stage * St::kBytes;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      __builtin_amdgcn_global_load_lds((glb_void*)(kcodes + at * (D / 2) + i * 1024), (lds_void*)(dst + i * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((glb_void*)(vcodes + at * (D / 2) + i * 1024),
+                                       (lds_void*)(dst + St::kValues + i * 1024), 16, 0, 0);
+    }
+    __builtin_amdgcn_global_load_lds((glb_void*)(scales + at * (D / 32)), (lds_void*)(dst + St::kScales), 4, 0, 0);
     if (then < w.s1) {
       row += 32 * NW;
       while (row >= p.c.page) {
@@ -228,47 +243,40 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
       }
       page = table[col];
     }
-  };
-  auto read_keys = [&](Codes<D>& c, long long at) {
-    const uint8_t* kc = kcodes + at * (D / 2);
-    const uint8_t* ks = kscales + at * (D / 32);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c.k[i] = *reinterpret_cast<const piece*>(kc + i * 8 * D);
-      c.ks[i] = ks[i * (D / 2)];
-    }
-  };
-  auto read_values = [&](Codes<D>& c, long long at) {
-    const uint8_t* vc = vcodes + at * (D / 2);
-    const uint8_t* vs = vscales + at * (D / 32);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      c.vs[i] = *reinterpret_cast<const piece*>(vs + i * (D / 2));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint8_t* a = vc + i * 8 * D + e * (D / 2);
-        c.v[4 * i + e] = D == 128 ? *reinterpret_cast<const uint32_t*>(a) : *reinterpret_cast<const uint16_t*>(a);
-      }
-    }
+    return there;
   };
 
-  // S^T of a step
-  auto scores = [&](const Codes<D>& c, f32x4 (&st)[R][2]) {
+  // Where a lane reads: of keys fr and 16 + fr the D/4 elements from g D/4, with their
+  // group's scale byte; of the values the D/16 elements from fr D/16 of eight keys, with
+  // the scale bytes of four neighbouring keys at a time.
+  const int kat = D == 128 ? fr * 64 + ((g ^ (fr >> 2)) << 4) : fr * 32 + (((g >> 1) ^ (fr >> 3)) << 4) + (g & 1) * 8;
+  const int ksat = St::kScales + fr * (D / 32) + (D == 128 ? g : g / 2);
+  const int vsat = St::kScales + D + g * (D / 8);
+  int vat[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int e = 0; e < 4; ++e)
+    vat[e] = St::kValues + (4 * g + (e ^ (D == 128 ? g : g & 2))) * (D / 2) + fr * (D / 32);
+
+  // S^T of a step
+  auto scores = [&](const unsigned char* at, f32x4 (&st)[R][2]) {
+    piece k[2];
+    float unit[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k[i] = *reinterpret_cast<const piece*>(at + kat + i * 8 * D);
+      unit[i] = fp4_unit(at[ksat + i * (D / 2)]);
 #pragma unroll
       for (int r = 0; r < R; ++r) st[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-      const bf16x8 k0 = frag(fp4_values(c.k[0][k], fp4_unit(c.ks[0])));
-      const bf16x8 k1 = frag(fp4_values(c.k[1][k], fp4_unit(c.ks[1])));
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bf16x8 q = kQueriesInLds ? frag(ql[(r * KT + k) * 64 + lane]) : qf[kQueriesInLds ? 0 : r][k];
-        st[r][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q, st[r][0], 0, 0, 0);
-        st[r][1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q, st[r][1], 0, 0, 0);
-      }
     }
+#pragma unroll
+    for (int x = 0; x < KT; ++x)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bf16x8 kf = frag(fp4_values(k[i][x], unit[i]));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          st[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[r][x], st[r][i], 0, 0, 0);
+      }
   };
   // Keys that a row does not see
   auto hide = [&](f32x4 (&st)[R][2], int s, bool there) {
@@ -278,17 +286,6 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (key + 16 * (i / 4) + i % 4 >= lim[r]) st[r][i / 4][i % 4] = -INFINITY;
-  };
-  // Rows past the last token hold anything: no NaN of theirs may meet a 0
-  auto clear = [&](Codes<D>& c, int s, bool there) {
-    const int key = (there ? 32 * s : 0x7fffff00) + 4 * g;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (key + 16 * (i / 4) + i % 4 >= w.len) {
-        c.v[i] = 0;
-        if constexpr (D == 128) c.vs[i / 4][i % 4] = 0;
-        else c.vs[i / 4][i % 4 / 2] &= i % 2 ? 0x0000ffffu : 0xffff0000u;
-      }
   };
   // The exponents of a step against the reference points as they are, and the largest
   // of them (compared as integers: that orders positive ones, which is what counts).
@@ -346,21 +343,38 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
   // O^T += V^T P^T: elements fr D/16 + (2 h, 2 h + 1) of the eight keys, turned into two
   // operands. The lane's scale byte of a key is turned to the exponent's place: the
   // conversions look at nothing else.
-  auto output = [&](const Codes<D>& c, const u32x4 (&pf)[R]) {
+  auto output = [&](const unsigned char* at, const u32x4 (&pf)[R], int s, bool there) {
+    uint32_t v[8];
     float unit[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t word = D == 128 ? c.vs[i / 4][i % 4] : c.vs[i / 4][i % 4 / 2];
-      const int from = D == 128 ? 8 * (fr / 4) : 16 * (i % 2) + 8 * (fr / 8);
-      unit[i] = __uint_as_float(__builtin_amdgcn_alignbit(word, word, (uint32_t)(from + 9) & 31u));
+    for (int i = 0; i < 2; ++i) {
+      const piece word = *reinterpret_cast<const piece*>(at + vsat + i * (D / 2));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned char* c = at + vat[e] + i * 8 * D;
+        v[4 * i + e] = D == 128 ? *reinterpret_cast<const uint32_t*>(c) : *reinterpret_cast<const uint16_t*>(c);
+        const uint32_t x = D == 128 ? word[e] : word[e / 2];
+        const int from = D == 128 ? 8 * (fr / 4) : 16 * (e % 2) + 8 * (fr / 8);
+        unit[4 * i + e] = __uint_as_float(__builtin_amdgcn_alignbit(x, x, (uint32_t)(from + 9) & 31u));
+      }
+    }
+    if ((there ? 32 * s + 32 : 0x7fffffff) > w.len) {
+      // rows past the last token hold anything: no NaN of theirs may meet a 0
+      const int key = (there ? 32 * s : 0x7fffff00) + 4 * g;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (key + 16 * (i / 4) + i % 4 >= w.len) {
+          v[i] = 0;
+          unit[i] = 1.f;
+        }
     }
 #pragma unroll
     for (int h = 0; h < DT / 2; ++h) {
       uint32_t a[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        a[i] = h == 0 ? fp4_pair<0>(c.v[i], unit[i]) : h == 1 ? fp4_pair<1>(c.v[i], unit[i])
-             : h == 2 ? fp4_pair<2>(c.v[i], unit[i]) : fp4_pair<3>(c.v[i], unit[i]);
+        a[i] = h == 0 ? fp4_pair<0>(v[i], unit[i]) : h == 1 ? fp4_pair<1>(v[i], unit[i])
+             : h == 2 ? fp4_pair<2>(v[i], unit[i]) : fp4_pair<3>(v[i], unit[i]);
       u32x4 lo, hi;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -374,70 +388,41 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
       }
     }
   };
-  auto edges = [&](Codes<D>& c, f32x4 (&st)[R][2], int s, bool there) {
-    const int end = there ? 32 * s + 32 : 0x7fffffff;
-    if (end > w.all) {
-      hide(st, s, there);
-      if (end > w.len) clear(c, s, there);
-    }
-  };
 
   if (s < w.s1) {
-    f32x4 st[R][2];
-    u32x4 pf[R];
-    if constexpr (kAhead) {
-      Codes<D> c0, c1;
-      Place a0 = place(), a1 = a0;
-      auto step = [&](Codes<D>& c, Place& a, Codes<D>& cn, Place& an) {
-        an = place();
-        read_keys(cn, an.at);
-        read_values(cn, an.at);
-        move_on(s + 2 * NW);
-        scores(c, st);
-        edges(c, st, s, a.there);
-        softmax(st, pf);
-        output(c, pf);
-        s += NW;
-      };
-      read_keys(c0, a0.at);
-      read_values(c0, a0.at);
-      move_on(s + NW);
-      for (;;) {
-        step(c0, a0, c1, a1);
-        if (s >= w.s1) break;
-        step(c1, a1, c0, a0);
-        if (s >= w.s1) break;
-      }
-    } else {
-      Codes<D> c;
-      Place a = place();
-      read_keys(c, a.at);
-      read_values(c, a.at);
-      move_on(s + NW);
-      for (; s < w.s1; s += NW) {
-        const Place n = place();
-        scores(c, st);
-        read_keys(c, n.at);
-        move_on(s + 2 * NW);
-        edges(c, st, s, a.there);
-        softmax(st, pf);
-        output(c, pf);
-        read_values(c, n.at);
-        a = n;
-      }
+    bool there[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) there[i] = load(i, s + (i + 1) * NW);
+    there[kStages - 1] = false;
+    for (int stage = 0; s < w.s1; s += NW) {
+      const int next = stage == 0 ? kStages - 1 : stage - 1;  // the stage of the step before: it has been read
+      there[kStages - 1] = load(next, s + kStages * NW);
+      wait_vm<(kStages - 1) * St::kLoads>();
+      const unsigned char* at = ring + stage * St::kBytes;
+      f32x4 st[R][2];
+      u32x4 pf[R];
+      scores(at, st);
+      if ((there[0] ? 32 * s + 32 : 0x7fffffff) > w.all) hide(st, s, there[0]);
+      softmax(st, pf);
+      output(at, pf, s, there[0]);
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) there[i] = there[i + 1];
+      stage = stage + 1 < kStages ? stage + 1 : 0;
     }
+    wait_vm<0>();
   }
-  if constexpr (kQueriesInLds) __syncthreads();
+  __syncthreads();  // the ring's places are the join's
 
   // The waves join, 16 rows at a time.
   constexpr int TPR = 64 * NW / 16, PER = D / TPR;  // threads of a row, elements of a thread
-  float* stat = lds + NW * 16 * LD;
+  float* join = reinterpret_cast<float*>(lds);  // [NW][16][LD], then [NW][16][2]
+  float* stat = join + NW * 16 * LD;
   const int jr = thread / TPR, jd = thread % TPR * PER;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (r > 0) __syncthreads();
     // element j + e D/16 of the lane's D/4 from g D/4 is o[j][e]
-    float* mine = lds + (wave * 16 + fr) * LD + g * (D / 4);
+    float* mine = join + (wave * 16 + fr) * LD + g * (D / 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -461,7 +446,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
       const float f = __builtin_amdgcn_exp2f(stat[(v * 16 + jr) * 2] - top);
       sum = fmaf(f, stat[(v * 16 + jr) * 2 + 1], sum);
 #pragma unroll
-      for (int d = 0; d < PER; ++d) y[d] = fmaf(f, lds[(v * 16 + jr) * LD + jd + d], y[d]);
+      for (int d = 0; d < PER; ++d) y[d] = fmaf(f, join[(v * 16 + jr) * LD + jd + d], y[d]);
     }
     if (w.part < 0) {
       const int t = i / p.G, h = w.hk * p.G + i - t * p.G;
@@ -483,7 +468,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, float* 
 
 // A tile of up to R times 16 rows.
 template <int D, int R, int NW>
-__device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, float* lds) {
+__device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, unsigned char* lds) {
   const int tiles = (w.rl - w.row0) / 16 + 1;
   if constexpr (R >= 4) {
     if (tiles == 3) return attend<D, 3, NW, R>(p, w, lds);
@@ -498,14 +483,14 @@ __device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, fl
 }
 
 // Waves a SIMD that the registers are shared out to.
-constexpr int waves_of(int D, int R) { return R > 1 ? 2 : D == 128 ? 3 : 4; }
+constexpr int waves_of(int D, int R) { return D == 128 ? (R == 1 ? 4 : R == 2 ? 3 : 2) : (R == 1 ? 5 : R == 2 ? 4 : R == 3 ? 3 : 2); }
 
 constexpr int kMaxSequences = 1024;  // whose work is shared evenly
 
 // A workgroup a tile, with all its keys.
 template <int D, int R, int NW>
 __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_attn_kernel(CaParams p) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];  // [NW][16][D + 4], [NW][16][2]
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const ItemCoord at = xcd_item(blockIdx.x, p.tiles);
   if (at.crop >= p.B * p.c.Hk) return;
   const int b = at.crop / p.c.Hk;
@@ -579,38 +564,35 @@ __device__ __forceinline__ void list_pieces(const CaParams& p, const long long* 
 // unfinished to the second.
 template <int D, int R, int NW>
 __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(CaParams p) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];
-  __shared__ long long cum[kMaxSequences + 1];
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int32_t piece[kPieces][4];  // sequence, tile of it, first step, end
   __shared__ int32_t state[4];           // pieces, where to go on (sequence, tile), the share
-  for (int b = threadIdx.x; b < p.B; b += 64 * NW) {
-    const Sequence q = sequence<R>(p, b);
-    cum[b + 1] = q.tile_work() * q.tiles * p.c.Hk;
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    long long sum = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 64) {
-      const int b = b0 + threadIdx.x;
-      long long v = b < p.B ? cum[b + 1] : 0;
-#pragma unroll
-      for (int d = 1; d < 64; d *= 2) {
-        const long long u = __shfl_up(v, d);
-        if ((int)threadIdx.x >= d) v += u;
-      }
-      if (b < p.B) cum[b + 1] = sum + v;
-      sum += __shfl(v, 63);
-    }
-    if (threadIdx.x == 0) {
-      cum[0] = 0;
-      state[1] = state[2] = -1;
-    }
-  }
-  __syncthreads();
-  // Wave 0 lists the share's pieces, some at a time, so that nothing of the sharing stays
-  // in registers while they are worked on.
+  long long* cum = reinterpret_cast<long long*>(lds);  // [B + 1] work before each sequence
+  if (threadIdx.x == 0) state[1] = state[2] = -1;
+  // The share's pieces are listed some at a time, and nothing of the sharing stays in
+  // registers while they are worked on.
   for (;;) {
-    if (threadIdx.x < 64) list_pieces<R, NW>(p, cum, piece, state);
+    for (int b = threadIdx.x; b < p.B; b += 64 * NW) {
+      const Sequence q = sequence<R>(p, b);
+      cum[b + 1] = q.tile_work() * q.tiles * p.c.Hk;
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      long long sum = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 64) {
+        const int b = b0 + threadIdx.x;
+        long long v = b < p.B ? cum[b + 1] : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const long long u = __shfl_up(v, d);
+          if ((int)threadIdx.x >= d) v += u;
+        }
+        if (b < p.B) cum[b + 1] = sum + v;
+        sum += __shfl(v, 63);
+      }
+      if (threadIdx.x == 0) cum[0] = 0;
+      list_pieces<R, NW>(p, cum, piece, state);
+    }
     __syncthreads();
     const int n = uniform(state[0]);
     for (int k = 0; k < n; ++k) {
@@ -721,7 +703,7 @@ Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   x.R = rows <= 16 ? 1 : rows <= 32 ? 2 : D == 128 || rows <= 48 ? 3 : 4;
   x.tiles = (rows + 16 * x.R - 1) / (16 * x.R);
   const long long items = (long long)B * Hk * x.tiles, steps = ((long long)L * page + 31) / 32;
-  const int resident = x.R > 1 ? 512 : D == 128 ? 768 : 1024;
+  const int resident = 256 * waves_of(D, x.R);
   x.shares = 0;
   if (B <= kMaxSequences && items < 4 * resident && steps > 4 * kWaves) {
     const long long most = items * steps / (2 * kWaves);
@@ -736,7 +718,9 @@ size_t po_bytes(const Plan& x, int D) { return al256((size_t)x.shares * 2 * 16 *
 
 template <int D, int R>
 hipError_t run(const CaParams& p, hipStream_t st) {
-  constexpr int kLds = kWaves * 16 * (D + 4 + 2) * 4;
+  constexpr int kRing = kWaves * kStages * Stage<D>::kBytes, kJoin = kWaves * 16 * (D + 4 + 2) * 4;
+  constexpr int kLds = kRing > kJoin ? kRing : kJoin;
+  static_assert((kMaxSequences + 1) * 8 <= kLds, "the work before each sequence fits");
   if (p.shares == 0) {
     const long long groups8 = ((long long)p.B * p.c.Hk + kXcds - 1) / kXcds * kXcds;
     hipLaunchKernelGGL((cache_attn_kernel<D, R, kWaves>), dim3((unsigned)(groups8 * p.tiles)), dim3(64 * kWaves), kLds,
