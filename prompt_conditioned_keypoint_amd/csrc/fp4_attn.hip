@@ -117,25 +117,49 @@ __device__ __forceinline__ Sequence sequence(const CaParams& p, int b) {
   return q;
 }
 
-// The work is cut into `n` equal shares; where share i begins.
-__device__ __forceinline__ long long share_begin(long long total, int n, int i) {
-  const long long q = total / n;
-  return q * i + (total - q * n) * i / n;
+// a / b for 0 <= a < 2^53, b > 0, without the long way of 64-bit division.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  long long q = (long long)((double)a / (double)b);
+  const long long r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
+}
+
+// The work (below 2^52: 2^21 tiles of 2^25 steps) is cut into `n` equal shares; share i
+// begins at total i / n.
+struct Shares {
+  long long each;
+  int rest, n;
+  __device__ long long begin(int i) const { return each * i + (uint32_t)(rest * i) / (uint32_t)n; }
+};
+
+__device__ __forceinline__ Shares shares_of(long long total, int n) {
+  Shares x;
+  x.each = quotient(total, n);
+  x.rest = (int)(total - x.each * n);
+  x.n = n;
+  return x;
 }
 
 // The steps of a tile that begins at `tile` which lie before `at`: a step belongs to the
 // share that holds its first unit of work.
 __device__ __forceinline__ int steps_before(const Sequence& q, long long tile, long long at) {
   if (at <= tile) return 0;
-  const long long n = (at - tile + q.weight() - 1) / q.weight();
-  return (int)min(n, (long long)q.steps);
+  if (at - tile >= q.tile_work()) return q.steps;
+  return (int)(((uint32_t)(at - tile) + q.weight() - 1) / (uint32_t)q.weight());
+}
+
+// Row i's query: i / G
+__device__ __forceinline__ int query_of(const CaParams& p, int i) {
+  return (p.G & (p.G - 1)) == 0 ? i >> (31 - __builtin_clz(p.G)) : (int)((uint32_t)i / (uint32_t)p.G);
 }
 
 // No share is worth having below two steps a wave (and one holds more than a step, which
 // costs 7 at most: the join counts on that).
 template <int NW>
 __device__ __forceinline__ int share_count(const CaParams& p, long long total) {
-  return (int)min((long long)p.shares, total / (2 * NW * 4) + 1);
+  return (int)min((long long)p.shares, quotient(total, 2 * NW * 4) + 1);
 }
 
 // What a workgroup works on: rows row0 .. rl of a key head, and the steps [s0, s1) of
@@ -147,6 +171,7 @@ struct Work {
   int all;      // keys that every row sees
   int s0, s1, part;
 };
+constexpr int kWorkInts = sizeof(Work) / 4;
 
 template <int R>
 __device__ __forceinline__ Work work_of(const CaParams& p, const Sequence& q, int b, int hk, int tile, int s0, int s1,
@@ -158,8 +183,8 @@ __device__ __forceinline__ Work work_of(const CaParams& p, const Sequence& q, in
   w.rl = min(w.row0 + 16 * q.sub, q.live) - 1;
   w.len = q.len;
   w.tq = q.tq;
-  w.all = p.causal ? max(q.len - q.tq + w.row0 / p.G + 1, 0) : q.len;
-  const int last = p.causal ? max(q.len - q.tq + w.rl / p.G + 1, 0) : q.len;  // keys that the last row sees
+  w.all = p.causal ? max(q.len - q.tq + query_of(p, w.row0) + 1, 0) : q.len;
+  const int last = p.causal ? max(q.len - q.tq + query_of(p, w.rl) + 1, 0) : q.len;  // keys that the last row sees
   w.s0 = s0;
   w.s1 = min(s1, (last + 31) / 32);
   w.part = part;
@@ -183,7 +208,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
   int lim[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = min(w.row0 + 16 * r + fr, w.rl), t = i / p.G, h = w.hk * p.G + i - t * p.G;
+    const int i = min(w.row0 + 16 * r + fr, w.rl), t = query_of(p, i), h = w.hk * p.G + i - t * p.G;
     const uint16_t* q = static_cast<const uint16_t*>(p.q.p) + w.b * p.q.b + t * p.q.t + h * p.q.h + g * (D / 4);
 #pragma unroll
     for (int k = 0; k < KT; ++k) qf[r][k] = frag(*reinterpret_cast<const u32x4*>(q + 8 * k));
@@ -449,7 +474,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
       for (int d = 0; d < PER; ++d) y[d] = fmaf(f, join[(v * 16 + jr) * LD + jd + d], y[d]);
     }
     if (w.part < 0) {
-      const int t = i / p.G, h = w.hk * p.G + i - t * p.G;
+      const int t = query_of(p, i), h = w.hk * p.G + i - t * p.G;
       uint16_t* out = static_cast<uint16_t*>(p.out.p) + w.b * p.out.b + t * p.out.t + h * p.out.h + jd;
       const float f = sum == 0.f ? 0.f : 1.f / sum;  // no key: O is 0
 #pragma unroll
@@ -504,17 +529,17 @@ __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_attn_kernel(CaP
 constexpr int kPieces = 32;
 
 template <int R, int NW>
-__device__ __forceinline__ void list_pieces(const CaParams& p, const long long* cum, int32_t (*piece)[4],
+__device__ __forceinline__ void list_pieces(const CaParams& p, const long long* cum, int32_t (*piece)[kWorkInts],
                                             int32_t* state) {
   const bool first = threadIdx.x == 0;
   int n = 0, b = uniform(state[1]), tile = uniform(state[2]);
   const long long total = uniform(cum[p.B]);
-  const int shares = uniform(share_count<NW>(p, total));
-  const bool any = (int)blockIdx.x < shares && total > 0;
+  const int count = uniform(share_count<NW>(p, total));
+  const bool any = (int)blockIdx.x < count && total > 0;
   // neighbouring shares, which read the same keys, on one XCD
-  const int x = blockIdx.x % kXcds, share = x * (shares / kXcds) + min(x, shares % kXcds) + blockIdx.x / kXcds;
-  const long long begin = any ? uniform(share_begin(total, shares, share)) : 0;
-  const long long end = any ? uniform(share_begin(total, shares, share + 1)) : 0;
+  const int x = blockIdx.x % kXcds, share = x * (count / kXcds) + min(x, count % kXcds) + blockIdx.x / kXcds;
+  const Shares shares = shares_of(total, count);
+  const long long begin = any ? uniform(shares.begin(share)) : 0, end = any ? uniform(shares.begin(share + 1)) : 0;
   if (any && b < 0) {
     int hi = p.B;  // cum[b] <= begin < cum[hi]
     b = 0;
@@ -530,20 +555,19 @@ __device__ __forceinline__ void list_pieces(const CaParams& p, const long long* 
     const Sequence q = sequence<R>(p, b);
     const long long per = q.tile_work();
     if (per == 0 || q.tiles == 0) continue;
-    if (tile < 0) tile = begin > base ? uniform((int)((begin - base) / per)) : 0;
+    if (tile < 0) tile = begin > base ? uniform((int)quotient(begin - base, per)) : 0;
     for (; tile < q.tiles * p.c.Hk && n < kPieces; ++tile) {
       const long long at = base + tile * per;
       if (at >= end) break;
       const int s0 = uniform(steps_before(q, at, begin)), s1 = uniform(steps_before(q, at, end));
       if (s0 >= s1) continue;
+      const int hk = uniform(tile / q.tiles), i = tile - hk * q.tiles;
+      const bool whole = s0 == 0 && s1 == q.steps;
+      const Work w = work_of<R>(p, q, b, hk, i, s0, s1, whole ? -1 : 2 * share + (s0 == 0 ? 1 : 0));
       if (first) {
-        piece[n][0] = b;
-        piece[n][1] = tile;
-        piece[n][2] = s0;
-        piece[n][3] = s1;
-        const int hk = tile / q.tiles;
-        int32_t* ends = p.ends + (((long long)b * p.c.Hk + hk) * p.tiles + tile - hk * q.tiles) * 2;
-        if (s0 == 0) ends[0] = s1 == q.steps ? -1 : share;
+        __builtin_memcpy(piece[n], &w, sizeof w);
+        int32_t* ends = p.ends + (((long long)b * p.c.Hk + hk) * p.tiles + i) * 2;
+        if (s0 == 0) ends[0] = whole ? -1 : share;
         if (s1 == q.steps) ends[1] = share;
       }
       ++n;
@@ -554,7 +578,6 @@ __device__ __forceinline__ void list_pieces(const CaParams& p, const long long* 
     state[0] = n;
     state[1] = n == kPieces ? b : -1;
     state[2] = tile;
-    state[3] = share;
   }
 }
 
@@ -565,8 +588,8 @@ __device__ __forceinline__ void list_pieces(const CaParams& p, const long long* 
 template <int D, int R, int NW>
 __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(CaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ int32_t piece[kPieces][4];  // sequence, tile of it, first step, end
-  __shared__ int32_t state[4];           // pieces, where to go on (sequence, tile), the share
+  __shared__ int32_t piece[kPieces][kWorkInts];
+  __shared__ int32_t state[3];  // pieces, where to go on (sequence, tile)
   long long* cum = reinterpret_cast<long long*>(lds);  // [B + 1] work before each sequence
   if (threadIdx.x == 0) state[1] = state[2] = -1;
   // The share's pieces are listed some at a time, and nothing of the sharing stays in
@@ -596,12 +619,13 @@ __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(Ca
     __syncthreads();
     const int n = uniform(state[0]);
     for (int k = 0; k < n; ++k) {
-      const int b = uniform(piece[k][0]), at = uniform(piece[k][1]), s0 = uniform(piece[k][2]), s1 = uniform(piece[k][3]);
-      const Sequence q = sequence<R>(p, b);
-      const int hk = uniform(at / q.tiles), share = uniform(state[3]);
-      if (k > 0) __syncthreads();
-      attend_tile<D, R, NW>(p, work_of<R>(p, q, b, hk, at - hk * q.tiles, s0, s1,
-                                          s0 == 0 && s1 == q.steps ? -1 : 2 * share + (s0 == 0 ? 1 : 0)), lds);
+      int32_t v[kWorkInts];
+#pragma unroll
+      for (int i = 0; i < kWorkInts; ++i) v[i] = uniform(piece[k][i]);
+      Work w;
+      __builtin_memcpy(&w, v, sizeof w);
+      __syncthreads();  // the last piece's join, or the listing, has been read
+      attend_tile<D, R, NW>(p, w, lds);
     }
     __syncthreads();
     if (uniform(state[1]) < 0) break;
@@ -619,20 +643,20 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CaParams p) {
   __shared__ f32x4 part[FEW ? GROUPS : 1][GL];
   __shared__ float stat[FEW ? GROUPS : 1][2];
   const int lane = threadIdx.x % GL, group = threadIdx.x / GL;
-  const int per = p.Tq * p.G;
-  const long long rows = (long long)p.B * p.c.Hk * per, at = FEW ? blockIdx.x : (long long)blockIdx.x * GROUPS + group;
-  if (at >= rows) return;  // (FEW: never)
-  const int bh = (int)(at / per), i = (int)(at - (long long)bh * per);
-  const int b = bh / p.c.Hk, hk = bh - b * p.c.Hk, t = i / p.G, h = hk * p.G + i - t * p.G;
-  const int cap = p.c.L * p.c.page;
-  const int len = p.length ? min(max(p.length[b], 0), cap) : cap;
-  const int live = (p.q_len ? min(max(p.q_len[b], 0), p.Tq) : p.Tq) * p.G;
-  if (i >= live) return;
-  const int subs = (live + 15) / 16, tiles = (subs + R - 1) / R, sub = (subs + tiles - 1) / tiles;
-  const int tile = i / (16 * sub), r = i - tile * 16 * sub;
+  const int blocks = FEW ? p.Tq * p.G : (p.Tq * p.G + GROUPS - 1) / GROUPS;  // of a key head
+  const int bh = blockIdx.x / blocks, b = bh / p.c.Hk, hk = bh - b * p.c.Hk;
+  const Sequence q = sequence<R>(p, b);
+  const int i = (blockIdx.x - bh * blocks) * (FEW ? 1 : GROUPS) + (FEW ? 0 : group);
+  if (i >= q.live) return;
+  const int t = query_of(p, i), h = hk * p.G + i - t * p.G;
+  int tile = i / 16;  // by q.sub
+  if (q.sub == 2) tile /= 2;
+  if (q.sub == 3) tile /= 3;
+  if (q.sub == 4) tile /= 4;
+  const int r = i - tile * 16 * q.sub;
   float m = kFar, l = 0.f;
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
-  if (len > 0) {
+  if (q.steps > 0) {
     const int32_t* ends = p.ends + ((long long)bh * p.tiles + tile) * 2;
     const int first = ends[0], n = ends[1] - first + 1;
     if (first < 0) return;  // written as it is
@@ -730,13 +754,13 @@ hipError_t run(const CaParams& p, hipStream_t st) {
   hipLaunchKernelGGL((cache_share_kernel<D, R, kWaves>), dim3((unsigned)p.shares), dim3(64 * kWaves), kLds, st, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const long long rows = (long long)p.B * p.c.Hk * p.Tq * p.G;
+  const long long heads = (long long)p.B * p.c.Hk, rows = (long long)p.Tq * p.G;
   constexpr int kRows = 1024 / D;  // of a workgroup
-  if (rows <= 512)
-    hipLaunchKernelGGL((cache_join_kernel<D, R, true>), dim3((unsigned)rows), dim3(256), 0, st, p);
+  if (heads * rows <= 512)
+    hipLaunchKernelGGL((cache_join_kernel<D, R, true>), dim3((unsigned)(heads * rows)), dim3(256), 0, st, p);
   else
-    hipLaunchKernelGGL((cache_join_kernel<D, R, false>), dim3((unsigned)((rows + kRows - 1) / kRows)), dim3(256), 0, st,
-                       p);
+    hipLaunchKernelGGL((cache_join_kernel<D, R, false>), dim3((unsigned)(heads * ((rows + kRows - 1) / kRows))), dim3(256),
+                       0, st, p);
   return hipGetLastError();
 }
 
