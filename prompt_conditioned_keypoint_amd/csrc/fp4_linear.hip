@@ -38,10 +38,36 @@ constexpr uint32_t kNowhere = 0xf0000000u;  // past every such buffer: 2^31 byte
 
 typedef __attribute__((address_space(3))) void lds_void;
 
+// Rows of w and x are often a multiple of 4 KB long, over which the channels of L2 and of
+// memory repeat: workgroups that went through K in step would all ask the same channel. So
+// each begins elsewhere in its n pieces; those of an XCD (every eighth) at neighbouring ones.
+__device__ __forceinline__ int first_piece(int n) {
+  return n > 0 ? (int)((blockIdx.x / kXcds + blockIdx.x % kXcds * ((n + kXcds - 1) / kXcds)) % n) : 0;
+}
+
+// Bytes at `from` of a buffer straight to LDS, 16, 4 or 1 a lane: to dst + 16 lane or dst + 4
+// lane. (Functions of their own: in a template the host's pass does not take the builtin.)
+__device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t b, unsigned char* dst, uint32_t from) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 16, (int)from, 0, 0, 0);
+}
+__device__ __forceinline__ void load4(__amdgpu_buffer_rsrc_t b, unsigned char* dst, uint32_t from) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 4, (int)from, 0, 0, 0);
+}
+__device__ __forceinline__ void load1(__amdgpu_buffer_rsrc_t b, unsigned char* dst, uint32_t from) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 1, (int)from, 0, 0, 0);
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N), the other counters left alone
+  asm volatile("" ::: "memory");
+}
+
+// All waves, with what they read of LDS in their registers.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
+  __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
@@ -82,7 +108,7 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(Fp4Params p) {
   // rows a load, or 8), its 16 bytes of x (2 rows).
   const int cr = lane >> 3, sr = BYTES ? lane >> 3 : lane >> 1, xr = lane >> 5;
   const int pieces = (p.K + 255) / 256, from = pieces * wave / NW, n = pieces * (wave + 1) / NW - from;
-  int at = n > 0 ? blockIdx.x % n : 0, left = n;  // the next piece to load, and how many
+  int at = first_piece(n), left = n;  // the next piece to load, and how many
   unsigned char* ring = lds + wave * STAGES * St::kBytes;
   auto load = [&](int stage) {
     unsigned char* dst = ring + stage * St::kBytes;
@@ -91,22 +117,22 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(Fp4Params p) {
     for (int i = 0; i < 2 * NT; ++i) {
       const int r = 8 * i + cr, k = k0 + 32 * ((lane & 7) ^ ((r >> 1) & 7));
       const uint32_t a = k < p.K ? (uint32_t)r * (p.K / 2) + k / 2 : kNowhere;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(cb, (lds_void*)(dst + i * 1024), 16, (int)a, 0, 0, 0);
+      load16(cb, dst + i * 1024, a);
     }
 #pragma unroll
     for (int i = 0; i < St::kLoadsS; ++i) {
       const int r = (BYTES ? 8 : 32) * i + sr, k = k0 + (BYTES ? 32 * (lane & 7) : 128 * (lane & 1));
       const uint32_t a = k < p.K ? (uint32_t)r * (p.K / 32) + k / 32 : kNowhere;
       if constexpr (BYTES)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(sb, (lds_void*)(dst + St::kScales + i * 256), 1, (int)a, 0, 0, 0);
+        load1(sb, dst + St::kScales + i * 256, a);
       else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(sb, (lds_void*)(dst + St::kScales + i * 256), 4, (int)a, 0, 0, 0);
+        load4(sb, dst + St::kScales + i * 256, a);
     }
 #pragma unroll
     for (int i = 0; i < St::kRowsX / 2; ++i) {
       const int r = 2 * i + xr, k = k0 + 8 * ((lane & 31) ^ (r & 15));
       const uint32_t a = k < p.K && r < MX ? (uint32_t)r * (uint32_t)p.ldx * 2u + 2 * k : kNowhere;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void*)(dst + St::kX + i * 1024), 16, (int)a, 0, 0, 0);
+      load16(xb, dst + St::kX + i * 1024, a);
     }
     if (++at == n) at = 0;
     --left;
@@ -190,9 +216,238 @@ hipError_t run_few(const Fp4Params& p, hipStream_t st) {
   return p.K % 128 == 0 ? launch_few<MX, NT, NW, STAGES, false>(p, st) : launch_few<MX, NT, NW, STAGES, true>(p, st);
 }
 
+// ---------------------------------------------------------------------------
+// More rows: tiles of BM = 16 MT WM rows of x and BN = 16 NT WN rows of w, two groups of
+// WM x WN waves that take half of each product's k and join at the end. Both operands go
+// through rings in LDS: x in DX stages of KC of K, the codes in DC stages of 256, which are
+// whole lines of memory. One group loads x, the other the codes: a wave's loads return in
+// order, so were they loaded by one wave, waiting for x, which comes from L2, would be
+// waiting for the codes behind it, which come from memory. Where there are few tiles,
+// `splits` workgroups share a tile's K and their sums meet in a kernel of their own.
+// ---------------------------------------------------------------------------
+template <int MT, int NT, int WM, int WN, int KC, bool BYTES>
+struct TileStage {
+  static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, W = WM * WN;
+  static constexpr int kRowsS = BYTES ? 8 : 32;  // rows of scales a load
+  static constexpr int kNC = BN / 8, kNS = (BN + kRowsS - 1) / kRowsS, kNX = BM * KC / 512;
+  static constexpr int kScales = BN * 128, kBytesC = kScales + 256 * kNS, kBytesX = BM * KC * 2;
+  static constexpr int kLoadsC = (kNC + W - 1) / W + (kNS + W - 1) / W, kLoadsX = (kNX + W - 1) / W;  // a wave
+};
+
+struct TileParams {
+  Fp4Params p;
+  int splits;
+  float* part;   // [splits][M][ldp] sums, or null
+  int ldp;
+};
+
+template <int MT, int NT, int WM, int WN, int KC, int DX, int DC, bool BYTES>
+__global__ __launch_bounds__(128 * WM * WN) void fp4_tile_kernel(TileParams tp) {
+  typedef TileStage<MT, NT, WM, WN, KC, BYTES> St;
+  const Fp4Params& p = tp.p;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];  // x's ring, then the codes'
+  unsigned char* const codes = lds + DX * St::kBytesX;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % tp.splits, tile = blockIdx.x / tp.splits;
+  const int tiles_n = (p.N + St::BN - 1) / St::BN, tm = tile / tiles_n;
+  const int n0 = (tile - tm * tiles_n) * St::BN, m0 = tm * St::BM;
+  const int kg = wave / St::W, gw = wave % St::W, wm = gw / WN, wn = gw % WN;
+  const auto cb = rows_of(p.codes + (long long)n0 * (p.K / 2), min(0 + St::BN, p.N - n0), p.K / 2, p.K / 2);
+  const auto sb = rows_of(p.scales + (long long)n0 * (p.K / 32), min(0 + St::BN, p.N - n0), p.K / 32, p.K / 32);
+  const auto xb = rows_of(p.x + (long long)m0 * p.ldx, min(0 + St::BM, p.M - m0), 2LL * p.ldx, 2 * p.K);
+  const int steps = (p.K + 255) / 256;
+  const int from = (int)((long long)steps * split / tp.splits), n = (int)((long long)steps * (split + 1) / tp.splits) - from;
+
+  constexpr int SUB = 256 / KC, XR = 512 / KC, XP = KC / 8;  // rows of x a load brings, pieces of a row
+  int at = first_piece(n), left = n, sub = 0, stage = 0;  // what to load next: step, how many, part of it; its stage
+  auto load_x = [&] {
+    unsigned char* dst = lds + stage * St::kBytesX;
+    const int k0 = left > 0 ? (from + at) * 256 + sub * KC : p.K;  // past K: zeros
+#pragma unroll
+    for (int u = 0; u < St::kLoadsX; ++u) {
+      const int i = (gw + u * St::W) % St::kNX, r = i * XR + lane / XP, k = k0 + 8 * ((lane % XP) ^ (r & 15));
+      const uint32_t a = k < p.K ? (uint32_t)r * (uint32_t)p.ldx * 2u + 2 * k : kNowhere;
+      load16(xb, dst + i * 1024, a);
+    }
+    stage = stage + 1 < DX ? stage + 1 : 0;
+    if (++sub < SUB) return;
+    sub = 0;
+    if (++at == n) at = 0;
+    --left;
+  };
+  auto load_codes = [&] {
+    unsigned char* dst = codes + stage * St::kBytesC;
+    const int k0 = left > 0 ? (from + at) * 256 : p.K;
+#pragma unroll
+    for (int u = 0; u < (St::kNC + St::W - 1) / St::W; ++u) {
+      const int i = (gw + u * St::W) % St::kNC, r = i * 8 + lane / 8, k = k0 + 32 * ((lane & 7) ^ ((r >> 1) & 7));
+      const uint32_t a = k < p.K ? (uint32_t)r * (p.K / 2) + k / 2 : kNowhere;
+      load16(cb, dst + i * 1024, a);
+    }
+#pragma unroll
+    for (int u = 0; u < (St::kNS + St::W - 1) / St::W; ++u) {
+      const int i = (gw + u * St::W) % St::kNS;
+      constexpr int PER = BYTES ? 8 : 2;  // loads of a row
+      const int r = i * St::kRowsS + lane / PER, k = k0 + lane % PER * (BYTES ? 32 : 128);
+      const uint32_t a = k < p.K ? (uint32_t)r * (p.K / 32) + k / 32 : kNowhere;
+      if constexpr (BYTES)
+        load1(sb, dst + St::kScales + i * 256, a);
+      else
+        load4(sb, dst + St::kScales + i * 256, a);
+    }
+    stage = stage + 1 < DC ? stage + 1 : 0;
+    if (++at == n) at = 0;
+    --left;
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int wrow = wn * 16 * NT + fr, xrow = wm * 16 * MT + fr;
+  // 128 of K, the h-th of their stages; this wave's half of each group
+  auto product = [&](const unsigned char* sx, int hx, const unsigned char* sc, int hc) {
+    u32x2 c[NT];
+    float unit[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      c[j] = *reinterpret_cast<const u32x2*>(sc + (wrow + 16 * j) * 128 + (((4 * hc + g) ^ (fr >> 1)) << 4) + 8 * kg);
+      unit[j] = fp4_unit(sc[St::kScales + ((wrow + 16 * j) * 8 + 4 * hc + g) * (BYTES ? 4 : 1)]);
+    }
+    bf16x8 x[2][MT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        x[u][i] = frag(*reinterpret_cast<const u32x4*>(sx + (xrow + 16 * i) * (2 * KC) +
+                                                       (((16 * hx + 4 * g + 2 * kg + u) ^ fr) << 4)));
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const bf16x8 w = frag(fp4_values(c[j][u], unit[j]));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x[u][i], acc[i][j], 0, 0, 0);
+      }
+  };
+  if (kg == 0) {
+#pragma unroll
+    for (int i = 0; i < DX - 1; ++i) load_x();
+  } else {
+#pragma unroll
+    for (int i = 0; i < DC - 1; ++i) load_codes();
+  }
+  for (int it = 0, sx = 0, sc = 0; it < n; ++it) {
+#pragma unroll
+    for (int part = 0; part < SUB; ++part) {
+      if (kg == 0) wait_vm<(DX - 2) * St::kLoadsX>();
+      else if (part == 0) wait_vm<(DC - 2) * St::kLoadsC>();
+      meet();  // everyone's loads of the part are here, and everyone has read the part before
+      if (kg == 0) load_x();
+      else if (part == 0) load_codes();
+#pragma unroll
+      for (int h = 0; h < KC / 128; ++h)
+        product(lds + sx * St::kBytesX, h, codes + sc * St::kBytesC, part * (KC / 128) + h);
+      sx = sx + 1 < DX ? sx + 1 : 0;
+    }
+    sc = sc + 1 < DC ? sc + 1 : 0;
+  }
+  wait_vm<0>();
+  f32x4* other = reinterpret_cast<f32x4*>(lds) + gw * MT * NT * 64 + lane;
+  meet();
+  if (kg > 0) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) other[(i * NT + j) * 64] = acc[i][j];
+  }
+  __syncthreads();
+  if (kg > 0) return;
+
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int col = n0 + wn * 16 * NT + 16 * j + 4 * g;
+    float b[4];
+    if (!tp.part) load_bias(p, col, b);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = m0 + xrow + 16 * i;
+      const f32x4 sum = acc[i][j] + other[(i * NT + j) * 64];
+      if (m >= p.M || col >= p.N) continue;
+      if (tp.part) {
+        *reinterpret_cast<f32x4*>(tp.part + ((long long)split * p.M + m) * tp.ldp + col) = sum;
+      } else {
+        float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+        with_act(p.act, [&](auto act) { finish<act, 4>(p, m, col, v, b); });
+      }
+    }
+  }
+}
+
+// The sums of a tile's splits, in their order, and the epilogue; four columns a thread.
+__global__ __launch_bounds__(256) void fp4_join_kernel(TileParams tp) {
+  const Fp4Params& p = tp.p;
+  const int per = tp.ldp / 4;
+  const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(u / per), col = (int)(u - (long long)m * per) * 4;
+  if (m >= p.M) return;
+  const float* at = tp.part + (long long)m * tp.ldp + col;
+  const long long step = (long long)p.M * tp.ldp;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll 4
+  for (int i = 1; i < tp.splits; ++i) sum += *reinterpret_cast<const f32x4*>(at + i * step);
+  float b[4], v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  load_bias(p, col, b);
+  with_act(p.act, [&](auto act) { finish<act, 4>(p, m, col, v, b); });
+}
+
+struct TilePlan {
+  int bm, bn, splits;
+};
+
+TilePlan tile_plan(int M, int N, int K) {
+  TilePlan t;
+  t.bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  t.bn = t.bm <= 32 ? 64 : 128;
+  const long long tiles = (long long)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn), steps = (K + 255) / 256;
+  const char* e = getenv("GKD_S");
+  long long splits = e ? atoi(e) : (tiles >= 192 ? 1 : (256 + tiles / 2) / tiles);
+  if (splits > steps / 2) splits = steps / 2;
+  t.splits = splits < 1 ? 1 : (int)splits;
+  return t;
+}
+
+template <int MT, int NT, int WM, int WN, int KC, int DX, int DC, bool BYTES>
+hipError_t launch_tile(const TileParams& tp, hipStream_t st) {
+  typedef TileStage<MT, NT, WM, WN, KC, BYTES> St;
+  constexpr int kLds = DX * St::kBytesX + DC * St::kBytesC;
+  static_assert(kLds <= 160 * 1024 && DX >= 2 && DC >= 2 && (DX - 2) * St::kLoadsX < 64 && (DC - 2) * St::kLoadsC < 64, "the rings fit");
+  static_assert(WM * WN * MT * NT * 1024 <= kLds, "the sums fit");
+  const long long tiles = (long long)((tp.p.M + St::BM - 1) / St::BM) * ((tp.p.N + St::BN - 1) / St::BN);
+  hipLaunchKernelGGL((fp4_tile_kernel<MT, NT, WM, WN, KC, DX, DC, BYTES>), dim3((unsigned)(tiles * tp.splits)),
+                     dim3(128 * WM * WN), kLds, st, tp);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !tp.part) return e;
+  const long long n = (long long)tp.p.M * (tp.ldp / 4);
+  hipLaunchKernelGGL(fp4_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, tp);
+  return hipGetLastError();
+}
+
+template <int MT, int NT, int WM, int WN, int KC, int DX, int DC>
+hipError_t run_tile(const TileParams& tp, hipStream_t st) {
+  return tp.p.K % 128 == 0 ? launch_tile<MT, NT, WM, WN, KC, DX, DC, false>(tp, st)
+                           : launch_tile<MT, NT, WM, WN, KC, DX, 3, true>(tp, st);
+}
+
 }  // namespace
 
-size_t linear_fp4_workspace_bytes(int, int, int) { return 0; }
+size_t linear_fp4_workspace_bytes(int M, int N, int K) {
+  if (M <= 4) return 0;
+  const TilePlan t = tile_plan(M, N, K);
+  return t.splits == 1 ? 0 : (size_t)t.splits * M * ((N + 3) / 4 * 4) * 4;
+}
 
 hipError_t launch_linear_fp4(const LinearFp4Args& a, hipStream_t st) {
   Fp4Params p{};
@@ -228,6 +483,15 @@ hipError_t launch_linear_fp4(const LinearFp4Args& a, hipStream_t st) {
   if (f == 15) return run_few<32, 2, 2, 2>(p, st);
   if (f == 16) return run_few<4, 1, 8, 2>(p, st);
   if (f == 17) return run_few<4, 1, 4, 3>(p, st);
+  if (f == 20 || (f == 0 && p.M > 4)) {
+    const TilePlan t = tile_plan(p.M, p.N, p.K);
+    TileParams tp{p, t.splits, t.splits > 1 ? static_cast<float*>(a.ws) : nullptr, (p.N + 3) / 4 * 4};
+    const int v = getenv("GKD_V") ? atoi(getenv("GKD_V")) : 0;
+    if (t.bm == 16) return v == 1 ? run_tile<1, 1, 1, 4, 256, 3, 5>(tp, st) : run_tile<1, 1, 1, 4, 256, 3, 8>(tp, st);
+    if (t.bm == 32) return v == 1 ? run_tile<2, 1, 1, 4, 256, 3, 3>(tp, st) : run_tile<2, 1, 1, 4, 256, 3, 6>(tp, st);
+    if (t.bm == 64) return v == 1 ? run_tile<4, 2, 1, 4, 128, 3, 3>(tp, st) : run_tile<4, 2, 1, 4, 128, 3, 5>(tp, st);
+    return v == 1 ? run_tile<4, 4, 2, 2, 128, 2, 4>(tp, st) : run_tile<4, 4, 2, 2, 128, 3, 3>(tp, st);
+  }
   if (p.M <= 1) return run_few<1, 1, 8, 2>(p, st);
   if (p.M <= 4) return run_few<4, 1, 8, 2>(p, st);
   if (p.M <= 16) return run_few<16, 1, 4, 2>(p, st);
