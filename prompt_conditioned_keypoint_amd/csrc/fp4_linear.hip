@@ -10,7 +10,6 @@
 #include "epilogue.hpp"
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
-#include <cstdlib>
 
 namespace gkd {
 namespace {
@@ -403,20 +402,33 @@ __global__ __launch_bounds__(256) void fp4_join_kernel(TileParams tp) {
   with_act(p.act, [&](auto act) { finish<act, 4>(p, m, col, v, b); });
 }
 
+// Which kernel takes more than 16 rows, and in how many splits: by what both take, in us, as
+// measured (M x K x N, few / tiles: 20 x 2048 x 16384 14.0 / 8.8, 64 x 4096 x 4096 10.8 / 15.7,
+// 64 x 8192 x 8192 35.7 / 21.8, 128 x 1024 x 4096 9.9 / 13.6, 128 x 2048 x 16384 47.8 / 22.5,
+// 128 x 8192 x 8192 67 / 31): the few rows' kernel 1.03 for each 1024 of K of 256 tiles of
+// 16 x 32, tiles 0.7, 1.4 or 2.0 for each 256 of K of as many as there are CUs, their join
+// 2.5 and the time of its bytes at 4 TB/s.
 struct TilePlan {
-  int bm, bn, splits;
+  int bm, bn, splits;  // bm 0: the few rows' kernel
 };
 
 TilePlan tile_plan(int M, int N, int K) {
-  TilePlan t;
-  t.bm = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  t.bn = t.bm <= 32 ? 64 : 128;
-  const long long tiles = (long long)((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn), steps = (K + 255) / 256;
-  const char* e = getenv("GKD_S");
-  long long splits = e ? atoi(e) : (tiles >= 192 ? 1 : (256 + tiles / 2) / tiles);
-  if (splits > steps / 2) splits = steps / 2;
-  t.splits = splits < 1 ? 1 : (int)splits;
-  return t;
+  TilePlan best{0, 0, 1};
+  if (M <= 16) return best;
+  const int bm = M <= 32 ? 32 : M <= 64 ? 64 : 128, bn = bm == 32 ? 64 : 128;
+  const double step = bm == 32 ? 0.7 : bm == 64 ? 1.4 : 2.0;
+  auto over = [](long long a, long long b) { return (a + b - 1) / b; };
+  const long long few = over(M, 16) * over(N, 32), tiles = over(M, bm) * over(N, bn), steps = over(K, 256);
+  double least = 2.5 + (double)over(few, 256) * K / 1024 * 1.03;
+  for (int s = 1; s <= 8 && 2 * s <= steps && (s == 1 || tiles * s <= 256); ++s) {
+    const double t = 3.0 + (double)over(tiles * s, 256) * (double)over(steps, s) * step +
+                     (s > 1 ? 2.5 + s * 8e-6 * M * N / 4.0 : 0.0);
+    if (t < least) {
+      least = t;
+      best = TilePlan{bm, bn, s};
+    }
+  }
+  return best;
 }
 
 template <int MT, int NT, int WM, int WN, int KC, int DX, int DC, bool BYTES>
@@ -444,7 +456,6 @@ hipError_t run_tile(const TileParams& tp, hipStream_t st) {
 }  // namespace
 
 size_t linear_fp4_workspace_bytes(int M, int N, int K) {
-  if (M <= 4) return 0;
   const TilePlan t = tile_plan(M, N, K);
   return t.splits == 1 ? 0 : (size_t)t.splits * M * ((N + 3) / 4 * 4) * 4;
 }
@@ -465,37 +476,23 @@ hipError_t launch_linear_fp4(const LinearFp4Args& a, hipStream_t st) {
   p.K = a.K;
   p.act = a.act;
   p.out_f32 = a.out_f32;
-  const char* e = getenv("GKD_F");
-  const int f = e ? atoi(e) : 0;
-  if (f == 1) return run_few<1, 1, 4, 2>(p, st);
-  if (f == 2) return run_few<1, 1, 4, 3>(p, st);
-  if (f == 3) return run_few<1, 1, 8, 2>(p, st);
-  if (f == 4) return run_few<1, 1, 8, 3>(p, st);
-  if (f == 5) return run_few<1, 1, 16, 2>(p, st);
-  if (f == 6) return run_few<1, 2, 4, 2>(p, st);
-  if (f == 7) return run_few<1, 2, 8, 2>(p, st);
-  if (f == 8) return run_few<1, 2, 4, 3>(p, st);
-  if (f == 9) return run_few<16, 1, 4, 2>(p, st);
-  if (f == 10) return run_few<16, 1, 4, 3>(p, st);
-  if (f == 12) return run_few<16, 2, 4, 2>(p, st);
-  if (f == 13) return run_few<16, 2, 4, 3>(p, st);
-  if (f == 14) return run_few<32, 1, 4, 2>(p, st);
-  if (f == 15) return run_few<32, 2, 2, 2>(p, st);
-  if (f == 16) return run_few<4, 1, 8, 2>(p, st);
-  if (f == 17) return run_few<4, 1, 4, 3>(p, st);
-  if (f == 20 || (f == 0 && p.M > 4)) {
-    const TilePlan t = tile_plan(p.M, p.N, p.K);
+  const TilePlan t = tile_plan(p.M, p.N, p.K);
+  if (t.bm > 0) {
     TileParams tp{p, t.splits, t.splits > 1 ? static_cast<float*>(a.ws) : nullptr, (p.N + 3) / 4 * 4};
-    const int v = getenv("GKD_V") ? atoi(getenv("GKD_V")) : 0;
-    if (t.bm == 16) return v == 1 ? run_tile<1, 1, 1, 4, 256, 3, 5>(tp, st) : run_tile<1, 1, 1, 4, 256, 3, 8>(tp, st);
-    if (t.bm == 32) return v == 1 ? run_tile<2, 1, 1, 4, 256, 3, 3>(tp, st) : run_tile<2, 1, 1, 4, 256, 3, 6>(tp, st);
-    if (t.bm == 64) return v == 1 ? run_tile<4, 2, 1, 4, 128, 3, 3>(tp, st) : run_tile<4, 2, 1, 4, 128, 3, 5>(tp, st);
-    return v == 1 ? run_tile<4, 4, 2, 2, 128, 2, 4>(tp, st) : run_tile<4, 4, 2, 2, 128, 3, 3>(tp, st);
+    if (t.bm == 32) return run_tile<2, 1, 1, 4, 256, 3, 3>(tp, st);
+    if (t.bm == 64) return run_tile<4, 2, 1, 4, 128, 3, 3>(tp, st);
+    return run_tile<4, 4, 2, 2, 128, 3, 3>(tp, st);
   }
-  if (p.M <= 1) return run_few<1, 1, 8, 2>(p, st);
-  if (p.M <= 4) return run_few<4, 1, 8, 2>(p, st);
-  if (p.M <= 16) return run_few<16, 1, 4, 2>(p, st);
-  return run_few<32, 1, 4, 2>(p, st);
+  // Eight waves share a long K, four a short one (M x K x N; us, eight / four): 1 x 1024 x
+  // 1024 2.9 / 2.6, 1 x 2048 x 16384 6.5 / 5.9, 1 x 8192 x 8192 9.4 / 10.0,
+  // 1 x 16384 x 4096 8.9 / 11.5; 3 x 16384 x 4096 9.7 / 10.7.
+  if (p.M == 1) return p.K < 4096 ? run_few<1, 1, 4, 2>(p, st) : run_few<1, 1, 8, 2>(p, st);
+  if (p.M <= 4) return p.K < 4096 ? run_few<4, 1, 4, 3>(p, st) : run_few<4, 1, 8, 2>(p, st);
+  // 16 rows of w a workgroup while that is no more than one a CU, 32 beyond, which load x half
+  // as often (us, 16 / 32): 16 x 16384 x 4096 15.7 / 20.8, 20 x 1024 x 4096 5.0 / 3.5, 16 x 8192 x
+  // 8192 16.5 / 12.6.
+  const long long tiles = (long long)((p.M + 15) / 16) * ((p.N + 15) / 16);
+  return tiles <= 256 ? run_few<16, 1, 4, 2>(p, st) : run_few<16, 2, 4, 2>(p, st);
 }
 
 }  // namespace gkd
