@@ -4,6 +4,11 @@
 //
 // A thread takes 8 neighbouring values, one 16-byte piece of bfloat16; four
 // neighbouring lanes hold a group and agree on its largest magnitude.
+//
+// A token's keys lie together outside a cache, a head's tokens together in its pages. So
+// a workgroup takes up to 32 tokens, the lanes of a wave neighbouring tokens of a head:
+// both sides move in whole lines, and a thread's place, the same for all its heads, is
+// looked up once, while its values are on their way.
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 
@@ -61,65 +66,88 @@ __global__ __launch_bounds__(256) void fp4_quantize_kernel(QuantParams p) {
   }
 }
 
+constexpr int kHeads = 4;  // a thread's heads, keys' and values'
+
 struct MoveParams {
   Heads k, v;
   Pages c;
-  int T, per;           // pieces of a token: 2 Hk D / 8
+  int T, dlog, tlog;   // D / 8 pieces of a row and 2^tlog tokens of a workgroup: 256 threads at most
+  int chunks, blocks;  // of a sequence's tokens, of a chunk's heads
   const int32_t *start, *count;
-  long long pieces;
+  long long groups;
 };
 
-// A thread's piece: 8 values of token t of sequence b, of the keys or the values.
+// A thread's piece of a token: place `piece` of its row, and the heads it takes.
 struct Piece {
-  long long at;   // element offset in k or v
-  long long code; // piece of the cache's codes, -1 without a place
-  bool value, live;
+  int t, d, head, step;  // the first head, of 2 Hk, and how far the next one is
+  long long at[2];       // element offset of the row in k, in v
+  long long code;        // piece of head 0's codes in the cache, -1 without a place
+  bool live;
 };
 
-__device__ __forceinline__ Piece piece(const MoveParams& p, long long u) {
+__device__ __forceinline__ Piece piece(const MoveParams& p, long long group) {
   Piece w;
-  const long long token = u / p.per;
-  int r = (int)(u - token * p.per);
-  const int b = (int)(token / p.T), t = (int)(token - (long long)b * p.T);
-  const int D8 = p.c.D / 8, half = p.per / 2;
-  w.value = r >= half;
-  if (w.value) r -= half;
-  const int h = r / D8, d = r - h * D8;
-  const Heads& x = w.value ? p.v : p.k;
-  w.at = b * x.b + t * x.t + h * x.h + 8 * d;
-  w.live = !p.count || t < p.count[b];
+  const int hb = (int)(group % p.blocks), chunk = (int)(group / p.blocks % p.chunks);
+  const int b = (int)(group / p.blocks / p.chunks);
+  const int x = threadIdx.x;
+  w.d = x & ((1 << p.dlog) - 1);
+  w.t = (chunk << p.tlog) + ((x >> p.dlog) & ((1 << p.tlog) - 1));
+  w.step = 256 >> (p.dlog + p.tlog);
+  w.head = hb * kHeads * w.step + (x >> (p.dlog + p.tlog));
+  w.at[0] = b * p.k.b + w.t * p.k.t + 8 * w.d;
+  w.at[1] = b * p.v.b + w.t * p.v.t + 8 * w.d;
+  w.live = w.t < p.T && (!p.count || w.t < p.count[b]);
   w.code = -1;
-  const long long pos = (long long)(p.start ? p.start[b] : 0) + t;
-  if (pos >= 0 && pos < (long long)p.c.L * p.c.page) {
-    const int col = (int)pos / p.c.page, row = (int)pos - col * p.c.page;
+  const long long pos = (long long)(p.start ? p.start[b] : 0) + w.t;
+  if (w.live && pos >= 0 && pos < (long long)p.c.L * p.c.page) {
+    const int col = (int)((uint32_t)pos / (uint32_t)p.c.page), row = (int)pos - col * p.c.page;
     const int page = p.c.table[(long long)b * p.c.L + col];
-    if (page >= 0 && page < p.c.pages)
-      w.code = ((((long long)page * 2 + (w.value ? 1 : 0)) * p.c.Hk + h) * p.c.page + row) * D8 + d;
+    if (page >= 0 && page < p.c.pages) w.code = (((long long)page * 2 * p.c.Hk * p.c.page + row) << p.dlog) + w.d;
   }
   return w;
 }
 
+// Its heads, one after another: f(j, value, element offset, piece of the cache's codes).
+template <class F>
+__device__ __forceinline__ void heads_of(const MoveParams& p, const Piece& w, F&& f) {
+#pragma unroll
+  for (int j = 0; j < kHeads; ++j) {
+    const int h = w.head + j * w.step;
+    if (h >= 2 * p.c.Hk) break;
+    const bool value = h >= p.c.Hk;
+    const long long at = value ? w.at[1] + (h - p.c.Hk) * p.v.h : w.at[0] + h * p.k.h;
+    f(j, value, at, w.code + (((long long)h * p.c.page) << p.dlog));
+  }
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(256) void fp4_append_kernel(MoveParams p) {
-  for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; u < p.pieces; u += (long long)gridDim.x * 256) {
-    const Piece w = piece(p, u);
-    if (!w.live || w.code < 0) continue;  // the four lanes of a group alike
-    float v[8];
-    load8<BF16>(w.value ? p.v.p : p.k.p, w.at, v);
-    const uint32_t s = fp4_scale(group_max(v));
-    reinterpret_cast<uint32_t*>(p.c.codes)[w.code] = fp4_codes(v, s);
-    if ((w.code & 3) == 0) p.c.scales[w.code >> 2] = (uint8_t)s;
+  for (long long group = blockIdx.x; group < p.groups; group += gridDim.x) {
+    const Piece w = piece(p, group);
+    float v[kHeads][8];
+    if (w.live) heads_of(p, w, [&](int j, bool value, long long at, long long) {
+      load8<BF16>(value ? p.v.p : p.k.p, at, v[j]);
+    });
+    if (w.code >= 0) heads_of(p, w, [&](int j, bool, long long, long long code) {  // the four lanes of a group alike
+      const uint32_t s = fp4_scale(group_max(v[j]));
+      reinterpret_cast<uint32_t*>(p.c.codes)[code] = fp4_codes(v[j], s);
+      if ((code & 3) == 0) p.c.scales[code >> 2] = (uint8_t)s;
+    });
   }
 }
 
 __global__ __launch_bounds__(256) void fp4_read_kernel(MoveParams p) {
-  for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; u < p.pieces; u += (long long)gridDim.x * 256) {
-    const Piece w = piece(p, u);
+  for (long long group = blockIdx.x; group < p.groups; group += gridDim.x) {
+    const Piece w = piece(p, group);
     if (!w.live) continue;
-    u32x4 y = {0u, 0u, 0u, 0u};
-    if (w.code >= 0)
-      y = fp4_values(reinterpret_cast<const uint32_t*>(p.c.codes)[w.code], fp4_unit(p.c.scales[w.code >> 2]));
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(w.value ? p.v.p : p.k.p) + w.at) = y;
+    uint32_t c[kHeads] = {}, s[kHeads] = {};
+    if (w.code >= 0) heads_of(p, w, [&](int j, bool, long long, long long code) {
+      c[j] = reinterpret_cast<const uint32_t*>(p.c.codes)[code];
+      s[j] = p.c.scales[code >> 2];
+    });
+    heads_of(p, w, [&](int j, bool value, long long at, long long) {
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(value ? p.v.p : p.k.p) + at) = fp4_values(c[j], fp4_unit(s[j]));
+    });
   }
 }
 
@@ -134,12 +162,18 @@ MoveParams move_params(const CacheMoveArgs& a) {
   p.v = a.v;
   p.c = a.c;
   p.T = a.T;
-  p.per = 2 * a.c.Hk * (a.c.D / 8);
+  p.dlog = a.c.D == 64 ? 3 : 4;
+  while (p.dlog + p.tlog < 8 && (1 << p.tlog) < a.T) ++p.tlog;
+  p.chunks = (int)(((long long)a.T + (1 << p.tlog) - 1) >> p.tlog);
+  const int heads = kHeads * (256 >> (p.dlog + p.tlog));
+  p.blocks = (2 * a.c.Hk + heads - 1) / heads;
   p.start = a.start;
   p.count = a.count;
-  p.pieces = (long long)a.B * a.T * p.per;
+  p.groups = (long long)a.B * p.chunks * p.blocks;
   return p;
 }
+
+unsigned grid_for(long long groups) { return (unsigned)(groups < (1 << 20) ? groups : 1 << 20); }
 
 }  // namespace
 
@@ -155,15 +189,15 @@ hipError_t launch_quantize_fp4(const QuantizeArgs& a, hipStream_t st) {
 hipError_t launch_cache_append(const CacheMoveArgs& a, hipStream_t st) {
   const MoveParams p = move_params(a);
   if (a.bf16)
-    hipLaunchKernelGGL(fp4_append_kernel<true>, dim3(groups_for(p.pieces)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL(fp4_append_kernel<true>, dim3(grid_for(p.groups)), dim3(256), 0, st, p);
   else
-    hipLaunchKernelGGL(fp4_append_kernel<false>, dim3(groups_for(p.pieces)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL(fp4_append_kernel<false>, dim3(grid_for(p.groups)), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const CacheMoveArgs& a, hipStream_t st) {
   const MoveParams p = move_params(a);
-  hipLaunchKernelGGL(fp4_read_kernel, dim3(groups_for(p.pieces)), dim3(256), 0, st, p);
+  hipLaunchKernelGGL(fp4_read_kernel, dim3(grid_for(p.groups)), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
