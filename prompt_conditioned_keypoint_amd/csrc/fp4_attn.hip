@@ -4,14 +4,15 @@
 // A row is one query of one query head; the rows of a sequence's key head are
 // numbered i = t G + g (G = Hq / Hk query heads share the key head). A workgroup
 // takes 16 R of them and a range of keys, its waves every NW-th step of 32 keys.
-// A wave reads a step's codes straight into registers, where the conversion
-// instructions make bfloat16 of them (0.5 instructions a value, exact), and takes
-//   S^T = K Q^T    keys as rows, queries as columns,
+// Each wave loads its steps straight to a ring of its own in LDS, one ahead of the
+// one at work, so that no wave waits for another before they join. The conversion
+// instructions make bfloat16 of the codes (0.5 instructions a value, exact), and
+//   S^T = K Q^T    has keys as rows, queries as columns,
 //   O^T = V^T P^T  head elements as rows, queries as columns,
 // so that the probabilities leave the first product in the very places that the
 // second one wants them: a lane's eight scores of a step are its eight k of the
 // operand P^T, if V's keys are taken in that order (place (g, i) is key
-// 16 (i / 4) + 4 g + i % 4). Nothing passes through LDS before the waves join.
+// 16 (i / 4) + 4 g + i % 4). They never leave the registers.
 //
 // The softmax runs online, in base 2: a row keeps its reference point m, the sum l
 // of 2^(s - m) and the output O scaled alike, and ranges of keys are joined by
@@ -21,6 +22,14 @@
 // Probabilities are rounded to bfloat16 (2^-8 of each) for the product with V, whose
 // instruction takes both sides in that type; l sums the rounded ones, in the same
 // product with a column of ones.
+//
+// What bounds it: few rows, memory. 48 sequences of 32 heads on 8 heads of 128 and up to
+// 8192 tokens, one new token each: 316 MB in 70 to 76 us, 4.2 to 4.5 TB/s, where a large
+// copy on the same card moves 5.0. One sequence of 262144 tokens: 279 MB in 64 to 67 us.
+// Many rows, the issue of instructions: a step of 48 rows of 128 elements takes 48 products
+// for S, 48 for O and 3 for l, beside 1536 exponents and what turns scores into operands,
+// and 4 sequences of 128 rows of 32 heads on up to 16384 tokens take 157 us, 0.84 PF (a
+// large product of the library 1.3 to 1.4).
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 
@@ -440,6 +449,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
 
   // The waves join, 16 rows at a time.
   constexpr int TPR = 64 * NW / 16, PER = D / TPR;  // threads of a row, elements of a thread
+  static_assert(PER >= 2 && PER * TPR == D);
   float* join = reinterpret_cast<float*>(lds);  // [NW][16][LD], then [NW][16][2]
   float* stat = join + NW * 16 * LD;
   const int jr = thread / TPR, jd = thread % TPR * PER;
@@ -714,13 +724,27 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CaParams p) {
 
 struct Plan {
   int R, tiles;
+  int waves;   // of a workgroup
   int shares;  // 0: a workgroup a tile
 };
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kManyWaves = 8;
 
-// R: as many tiles of 16 rows as two waves a SIMD have registers for. Work is shared where
-// there are neither enough tiles for the card nor so few keys that joining would take longer.
+// R: as many tiles of 16 rows as two waves a SIMD have registers for.
+//
+// A workgroup a tile, or equal shares: the shares' listing and their join take 10 us
+// beside the reading (1 x 16 heads of 64 on 576 tokens: 13.4 us against 5.7), and spare a
+// tile's 0.8 us a step and wave where the other compute units would wait for it (1 x 32
+// heads on 8 heads of 128 and 8192 tokens: 12.0 us against 35.3). Without a tile for every
+// compute unit they meet between 2048 tokens (11.7 us against 12.3) and 4096 (11.9 against
+// 20.1), with one near 4096 (4 x 300 rows of 16 heads of 64: both 51 us; 48 x 32 heads of
+// 128 at one length: 48 against 37, and at lengths from 1 to 8192 76 against 74). Beyond that
+// the longest of many sequences would decide (4 x 128 rows of 32 heads up to 16384 tokens:
+// 157 against 190 us), and even among four times as many tiles as stay resident it does not.
+//
+// Eight waves a workgroup halve a tile's time where there is a compute unit for each (16
+// heads of 64, 2304 tokens: 10.8 us against 13.8 with four; 256 tiles of 2304: 12.3 against
+// 15.5), and cost where workgroups wait for their turn (384 tiles of 2048: 24.9 against 22.2).
 Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   Plan x;
   const int rows = Tq * (Hq / Hk);
@@ -729,7 +753,8 @@ Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   const long long items = (long long)B * Hk * x.tiles, steps = ((long long)L * page + 31) / 32;
   const int resident = 256 * waves_of(D, x.R);
   x.shares = 0;
-  if (B <= kMaxSequences && items < 4 * resident && steps > 4 * kWaves) {
+  x.waves = x.R == 1 && items <= 256 ? kManyWaves : kWaves;
+  if (B <= kMaxSequences && items < 4 * resident && steps > (items < 256 ? 64 : 128)) {
     const long long most = items * steps / (2 * kWaves);
     x.shares = most < resident ? (int)most : resident;
   }
@@ -740,17 +765,30 @@ size_t al256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t ends_bytes(const Plan& x, int B, int Hk) { return al256((size_t)B * Hk * x.tiles * 8); }
 size_t po_bytes(const Plan& x, int D) { return al256((size_t)x.shares * 2 * 16 * x.R * D * 4); }
 
+template <int D, int NW>
+constexpr int lds_bytes() {
+  constexpr int kRing = NW * kStages * Stage<D>::kBytes, kJoin = NW * 16 * (D + 4 + 2) * 4;
+  static_assert((kMaxSequences + 1) * 8 <= kRing, "the work before each sequence fits");
+  return kRing > kJoin ? kRing : kJoin;
+}
+
+template <int D, int R, int NW>
+hipError_t run_tiles(const CaParams& p, hipStream_t st) {
+  const long long groups8 = ((long long)p.B * p.c.Hk + kXcds - 1) / kXcds * kXcds;
+  hipLaunchKernelGGL((cache_attn_kernel<D, R, NW>), dim3((unsigned)(groups8 * p.tiles)), dim3(64 * NW),
+                     (lds_bytes<D, NW>()), st, p);
+  return hipGetLastError();
+}
+
 template <int D, int R>
-hipError_t run(const CaParams& p, hipStream_t st) {
-  constexpr int kRing = kWaves * kStages * Stage<D>::kBytes, kJoin = kWaves * 16 * (D + 4 + 2) * 4;
-  constexpr int kLds = kRing > kJoin ? kRing : kJoin;
-  static_assert((kMaxSequences + 1) * 8 <= kLds, "the work before each sequence fits");
+hipError_t run(const CaParams& p, int waves, hipStream_t st) {
   if (p.shares == 0) {
-    const long long groups8 = ((long long)p.B * p.c.Hk + kXcds - 1) / kXcds * kXcds;
-    hipLaunchKernelGGL((cache_attn_kernel<D, R, kWaves>), dim3((unsigned)(groups8 * p.tiles)), dim3(64 * kWaves), kLds,
-                       st, p);
-    return hipGetLastError();
+    if constexpr (R == 1) {
+      if (waves == kManyWaves) return run_tiles<D, 1, kManyWaves>(p, st);
+    }
+    return run_tiles<D, R, kWaves>(p, st);
   }
+  constexpr int kLds = lds_bytes<D, kWaves>();
   hipLaunchKernelGGL((cache_share_kernel<D, R, kWaves>), dim3((unsigned)p.shares), dim3(64 * kWaves), kLds, st, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -765,11 +803,11 @@ hipError_t run(const CaParams& p, hipStream_t st) {
 }
 
 template <int D>
-hipError_t run_rows(const CaParams& p, int R, hipStream_t st) {
+hipError_t run_rows(const CaParams& p, const Plan& x, hipStream_t st) {
   if constexpr (D == 64) {
-    if (R == 4) return run<D, 4>(p, st);
+    if (x.R == 4) return run<D, 4>(p, x.waves, st);
   }
-  return R == 1 ? run<D, 1>(p, st) : R == 2 ? run<D, 2>(p, st) : run<D, 3>(p, st);
+  return x.R == 1 ? run<D, 1>(p, x.waves, st) : x.R == 2 ? run<D, 2>(p, x.waves, st) : run<D, 3>(p, x.waves, st);
 }
 
 }  // namespace
@@ -805,7 +843,7 @@ hipError_t launch_cache_attn(const CacheAttnArgs& a, hipStream_t st) {
     p.po = reinterpret_cast<float*>(ws);
     p.ml = reinterpret_cast<float*>(ws + po_bytes(x, a.c.D));
   }
-  return a.c.D == 128 ? run_rows<128>(p, x.R, st) : run_rows<64>(p, x.R, st);
+  return a.c.D == 128 ? run_rows<128>(p, x, st) : run_rows<64>(p, x, st);
 }
 
 }  // namespace gkd
