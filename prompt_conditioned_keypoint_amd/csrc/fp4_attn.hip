@@ -26,10 +26,10 @@
 // What bounds it: few rows, memory. 48 sequences of 32 heads on 8 heads of 128 and up to
 // 8192 tokens, one new token each: 316 MB in 70 to 76 us, 4.2 to 4.5 TB/s, where a large
 // copy on the same card moves 5.0. One sequence of 262144 tokens: 279 MB in 64 to 67 us.
-// Many rows, the issue of instructions: a step of 48 rows of 128 elements takes 48 products
-// for S, 48 for O and 3 for l, beside 1536 exponents and what turns scores into operands,
-// and 4 sequences of 128 rows of 32 heads on up to 16384 tokens take 157 us, 0.84 PF (a
-// large product of the library 1.3 to 1.4).
+// Many rows, the issue of instructions: a step of 32 rows of 128 elements takes 16 products
+// for S, 16 for O and 2 for l, beside 1024 exponents and what turns codes and scores into
+// operands, and 16 sequences of 128 rows of 32 heads on 8192 tokens take 293 us, 0.94 PF
+// (a large product of the library 1.3 to 1.4).
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 
@@ -104,12 +104,15 @@ __device__ __forceinline__ void wait_vm() {
 }
 
 // A sequence's work: `tiles` tiles of `sub` times 16 rows of each key head, `steps`
-// steps of keys each. A step is taken to cost 3 + sub: its conversions beside the
-// products and exponents of its rows.
+// steps of keys each. A step is taken to cost 3 + sub, its conversions beside the
+// products and exponents of its rows, and a tile kStart more, the wait for its queries and
+// first keys and its waves' join (without that 88 tiles of one step each would be one
+// share: 16 sequences of 128 rows of 32 heads, 1 to 8192 tokens, took 670 us, now 214).
+constexpr int kStart = 64;
 struct Sequence {
   int len, tq, live, tiles, sub, steps;
   __device__ int weight() const { return 3 + sub; }
-  __device__ long long tile_work() const { return (long long)steps * weight(); }
+  __device__ long long tile_work() const { return steps > 0 ? kStart + (long long)steps * weight() : 0; }
 };
 
 template <int R>
@@ -135,7 +138,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return q;
 }
 
-// The work (below 2^52: 2^21 tiles of 2^25 steps) is cut into `n` equal shares; share i
+// The work (below 2^51: 2^21 tiles of 2^26 steps) is cut into `n` equal shares; share i
 // begins at total i / n.
 struct Shares {
   long long each;
@@ -152,11 +155,13 @@ __device__ __forceinline__ Shares shares_of(long long total, int n) {
 }
 
 // The steps of a tile that begins at `tile` which lie before `at`: a step belongs to the
-// share that holds its first unit of work.
+// share that holds its first unit of work, and kStart lies between the first two steps' first
+// units.
 __device__ __forceinline__ int steps_before(const Sequence& q, long long tile, long long at) {
   if (at <= tile) return 0;
   if (at - tile >= q.tile_work()) return q.steps;
-  return (int)(((uint32_t)(at - tile) + q.weight() - 1) / (uint32_t)q.weight());
+  const int x = (int)(at - tile) - kStart, w = q.weight();
+  return x <= w ? 1 : (int)((uint32_t)(x + w - 1) / (uint32_t)w);
 }
 
 // Row i's query: i / G
@@ -164,11 +169,10 @@ __device__ __forceinline__ int query_of(const CaParams& p, int i) {
   return (p.G & (p.G - 1)) == 0 ? i >> (31 - __builtin_clz(p.G)) : (int)((uint32_t)i / (uint32_t)p.G);
 }
 
-// No share is worth having below two steps a wave (and one holds more than a step, which
-// costs 7 at most: the join counts on that).
-template <int NW>
+// A share holds at least kStart + 8 units, so more than lie between any two steps' first
+// units (a step costs 6 at most): the join counts on that.
 __device__ __forceinline__ int share_count(const CaParams& p, long long total) {
-  return (int)min((long long)p.shares, quotient(total, 2 * NW * 4) + 1);
+  return (int)min((long long)p.shares, max(quotient(total, kStart + 8), 1LL));
 }
 
 // What a workgroup works on: rows row0 .. rl of a key head, and the steps [s0, s1) of
@@ -505,9 +509,6 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
 template <int D, int R, int NW>
 __device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, unsigned char* lds) {
   const int tiles = (w.rl - w.row0) / 16 + 1;
-  if constexpr (R >= 4) {
-    if (tiles == 3) return attend<D, 3, NW, R>(p, w, lds);
-  }
   if constexpr (R >= 3) {
     if (tiles == 2) return attend<D, 2, NW, R>(p, w, lds);
   }
@@ -517,8 +518,9 @@ __device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, un
   attend<D, R, NW, R>(p, w, lds);
 }
 
-// Waves a SIMD that the registers are shared out to.
-constexpr int waves_of(int D, int R) { return D == 128 ? (R == 1 ? 4 : R == 2 ? 3 : 2) : (R == 1 ? 5 : R == 2 ? 4 : R == 3 ? 3 : 2); }
+// Waves a SIMD that the registers are shared out to, and so workgroups of four waves that a
+// compute unit holds.
+constexpr int waves_of(int D, int R) { return (D == 128 ? 5 : 6) - R; }
 
 constexpr int kMaxSequences = 1024;  // whose work is shared evenly
 
@@ -538,13 +540,13 @@ __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_attn_kernel(CaP
 // its begin; and left so when they are all listed).
 constexpr int kPieces = 32;
 
-template <int R, int NW>
+template <int R>
 __device__ __forceinline__ void list_pieces(const CaParams& p, const long long* cum, int32_t (*piece)[kWorkInts],
                                             int32_t* state) {
   const bool first = threadIdx.x == 0;
   int n = 0, b = uniform(state[1]), tile = uniform(state[2]);
   const long long total = uniform(cum[p.B]);
-  const int count = uniform(share_count<NW>(p, total));
+  const int count = uniform(share_count(p, total));
   const bool any = (int)blockIdx.x < count && total > 0;
   // neighbouring shares, which read the same keys, on one XCD
   const int x = blockIdx.x % kXcds, share = x * (count / kXcds) + min(x, count % kXcds) + blockIdx.x / kXcds;
@@ -624,7 +626,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(Ca
         sum += __shfl(v, 63);
       }
       if (threadIdx.x == 0) cum[0] = 0;
-      list_pieces<R, NW>(p, cum, piece, state);
+      list_pieces<R>(p, cum, piece, state);
     }
     __syncthreads();
     const int n = uniform(state[0]);
@@ -662,7 +664,6 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CaParams p) {
   int tile = i / 16;  // by q.sub
   if (q.sub == 2) tile /= 2;
   if (q.sub == 3) tile /= 3;
-  if (q.sub == 4) tile /= 4;
   const int r = i - tile * 16 * q.sub;
   float m = kFar, l = 0.f;
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
@@ -730,34 +731,40 @@ struct Plan {
 
 constexpr int kWaves = 4, kManyWaves = 8;
 
-// R: as many tiles of 16 rows as two waves a SIMD have registers for.
+// R, tiles of 16 rows that go through the keys together, and a workgroup's waves. With no
+// more than a tile of 16 rows for each compute unit, every tile has a workgroup of eight
+// waves (80 rows of 2 x 8 heads of 64, 2304 tokens: 11.1 us, in twos 17.3; one row of 16
+// heads and 2304 tokens: 10.8 us, with four waves 13.8; 384 tiles of 2048 tokens would take
+// 24.9 with eight, 22.2 with four). Else up to three tiles go together (37 x 40 rows of 16
+// heads of 64, 2304 tokens: 39 us, in twos 47), and more than three in twos: as fast as in
+// threes where all have as many (37 x 80 rows: 65 us and 62; 16 x 128 rows of 32 heads of
+// 128, 4096 tokens: 165 and 166) and ahead where not (37 sets of up to 80 rows: 35 and 44).
 //
-// A workgroup a tile, or equal shares: the shares' listing and their join take 10 us
-// beside the reading (1 x 16 heads of 64 on 576 tokens: 13.4 us against 5.7), and spare a
-// tile's 0.8 us a step and wave where the other compute units would wait for it (1 x 32
-// heads on 8 heads of 128 and 8192 tokens: 12.0 us against 35.3). Without a tile for every
-// compute unit they meet between 2048 tokens (11.7 us against 12.3) and 4096 (11.9 against
-// 20.1), with one near 4096 (4 x 300 rows of 16 heads of 64: both 51 us; 48 x 32 heads of
-// 128 at one length: 48 against 37, and at lengths from 1 to 8192 76 against 74). Beyond that
-// the longest of many sequences would decide (4 x 128 rows of 32 heads up to 16384 tokens:
-// 157 against 190 us), and even among four times as many tiles as stay resident it does not.
-//
-// Eight waves a workgroup halve a tile's time where there is a compute unit for each (16
-// heads of 64, 2304 tokens: 10.8 us against 13.8 with four; 256 tiles of 2304: 12.3 against
-// 15.5), and cost where workgroups wait for their turn (384 tiles of 2048: 24.9 against 22.2).
+// A workgroup a tile, or equal shares: listing and joining the shares takes 10 us beside the
+// reading, and spares the others' wait for the longest tile, 0.8 us a step and wave. One
+// sequence of 32 heads on 8 of 128: 2048 tokens 12.2 us in tiles and 15.2 in shares, 4096
+// 20.1 and 14.0, 32768 128 and 20; 16 of them: 4096 tokens 22 and 25, 8192 37 and 36; 48 at
+// 8192 81 and 93, at lengths from 1 to 8192 54 and 46, one at 8000 among short ones 47 and
+// 22. Among four times as many tiles as stay resident the longest one does not count.
 Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
+  const int rows = Tq * (Hq / Hk), subs = (rows + 15) / 16;
+  const long long heads = (long long)B * Hk, steps = ((long long)L * page + 31) / 32;
+  const bool few = heads * subs <= 256;
   Plan x;
-  const int rows = Tq * (Hq / Hk);
-  x.R = rows <= 16 ? 1 : rows <= 32 ? 2 : D == 128 || rows <= 48 ? 3 : 4;
-  x.tiles = (rows + 16 * x.R - 1) / (16 * x.R);
-  const long long items = (long long)B * Hk * x.tiles, steps = ((long long)L * page + 31) / 32;
-  const int resident = 256 * waves_of(D, x.R);
+  x.R = few ? 1 : subs <= 3 ? subs : 2;
+  x.tiles = (subs + x.R - 1) / x.R;
+  x.waves = few ? kManyWaves : kWaves;
   x.shares = 0;
-  x.waves = x.R == 1 && items <= 256 ? kManyWaves : kWaves;
-  if (B <= kMaxSequences && items < 4 * resident && steps > (items < 256 ? 64 : 128)) {
-    const long long most = items * steps / (2 * kWaves);
-    x.shares = most < resident ? (int)most : resident;
-  }
+  const long long items = heads * x.tiles;
+  if (B > kMaxSequences || steps <= 96 + (items < 640 ? items : 640) / 4) return x;
+  // (shares are even whatever the tiles are, so theirs are as large as can be)
+  const int R = subs < 3 ? subs : 3, tiles = (subs + R - 1) / R, resident = 256 * waves_of(D, R);
+  if (heads * tiles >= 4 * resident) return x;
+  const long long most = heads * tiles * steps / (2 * kWaves);
+  x.R = R;
+  x.tiles = tiles;
+  x.waves = kWaves;
+  x.shares = most < resident ? (int)most : resident;
   return x;
 }
 
@@ -804,9 +811,6 @@ hipError_t run(const CaParams& p, int waves, hipStream_t st) {
 
 template <int D>
 hipError_t run_rows(const CaParams& p, const Plan& x, hipStream_t st) {
-  if constexpr (D == 64) {
-    if (x.R == 4) return run<D, 4>(p, x.waves, st);
-  }
   return x.R == 1 ? run<D, 1>(p, x.waves, st) : x.R == 2 ? run<D, 2>(p, x.waves, st) : run<D, 3>(p, x.waves, st);
 }
 
