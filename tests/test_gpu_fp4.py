@@ -266,6 +266,42 @@ def test_linear_large(gkd, M, K, N):
     check_linear(gkd, M, K, N, "gelu", seed=N)
 
 
+# rows and weights for which work goes by tiles of 32, 64 and 128 rows, with K split and
+# not, with rows of scales that are whole words and not
+TILES = [(20, 2048, 9000), (31, 4128, 9001), (17, 8224, 4100), (63, 544, 16390), (50, 4096, 4100), (50, 4128, 8200),
+         (128, 8192, 1030), (130, 8224, 2050), (1500, 544, 2050), (2000, 1024, 1030)]
+
+
+@pytest.mark.parametrize("M,K,N", TILES)
+def test_linear_tiles(gkd, M, K, N):
+    check_linear(gkd, M, K, N, "silu", seed=N)
+    check_linear(gkd, M, K, N, bias=False, residual=False, out=F32, seed=M)
+
+
+@pytest.mark.parametrize("M,K,N", [(31, 4128, 9001), (50, 4128, 8200), (130, 8224, 2050), (63, 544, 16390)])
+def test_linear_tiles_stay_within_their_arrays(gkd, M, K, N):
+    g = rng(11)
+    x = randn(g, M, K)
+    codes, scales = gkd.quantize_fp4(randn(g, N, K, scale=1 / 32, dtype=F32))
+    want = gkd.linear_fp4(x, codes, scales)
+    buf = torch.full((M + 2, K + 24), float("nan"), dtype=BF, device="cuda")
+    buf[1:-1, 8:8 + K] = x
+    cb = torch.full((N + 2, K // 2), 0x77, dtype=U8, device="cuda")
+    sb = torch.full((N + 32, K // 32), 255, dtype=U8, device="cuda")
+    cb[1:-1], sb[16:-16] = codes, scales
+    for out in (BF, F32):
+        y = torch.full((M + 2, N + 3), 7.0, dtype=out, device="cuda")
+        got = gkd.linear_fp4(buf[1:-1, 8:8 + K], cb[1:-1], sb[16:-16], out=y[1:-1, 1:-2])
+        assert torch.equal(got.to(BF), want)
+        y[1:-1, 1:-2] = 7
+        assert bool((y == 7).all())
+    # a group of NaN reaches its column alone, a NaN in a row its row
+    sb[16 + 7, K // 32 - 1] = 255
+    x[2, K - 1] = float("nan")
+    nan = torch.isnan(gkd.linear_fp4(x, cb[1:-1], sb[16:-16]))
+    assert bool(nan[:, 7].all()) and bool(nan[2].all()) and int(nan.sum()) == M + N - 1
+
+
 def test_linear_reads_nothing_beside_its_rows(gkd):
     g = rng(5)
     for M in (3, 40, 130):
@@ -449,6 +485,62 @@ def test_attention_many_rows(gkd, D):
     check_attention(gkd, q, codes, scales, table, ints(576, 640), ints(80, 11))
     q, codes, scales, table = attn_inputs(1, 150, 6, 2, D, 64, 5, seed=5)
     check_attention(gkd, q, codes, scales, table, ints(300), causal=True)
+
+
+def many_pages(B, Tq, Hq, Hk, D, L, seed):
+    """Room for 32 L tokens a sequence on a few pages, so that columns share them: keys are
+    few to look at, and how the work is cut goes by the room."""
+    g = rng(seed)
+    codes, scales = gkd_quantised(g, 50, Hk, 32, D, 0.5)
+    return randn(g, B, Tq, Hq, D), codes, scales, torch.randint(0, 50, (B, L), generator=g, device="cuda").to(torch.int32)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,Tq,Hq,Hk", [(1, 1, 8, 1), (6, 1, 4, 2), (3, 9, 6, 3), (5, 40, 2, 2), (2, 70, 2, 1)])
+def test_attention_room_for_many_tokens(gkd, B, Tq, Hq, Hk, D, causal):
+    q, codes, scales, table = many_pages(B, Tq, Hq, Hk, D, 170, seed=Tq)
+    length = torch.randint(0, 700, (B,), generator=rng(B), device="cuda").to(torch.int32)
+    q_len = torch.randint(0, Tq + 1, (B,), generator=rng(B + 1), device="cuda").to(torch.int32)
+    length[-1], q_len[-1] = 5440, Tq
+    check_attention(gkd, q, codes, scales, table, length, q_len, causal)
+    # columns without a page, whole steps of them
+    table[:, 1:4], table[-1, 60:160], table[-1, 8] = -1, 50, 2**31 - 1
+    check_attention(gkd, q, codes, scales, table, length, None, causal)
+    # idle sequences around one, and none at all
+    length[:-1] = 0
+    check_attention(gkd, q, codes, scales, table, length, None, causal)
+    length[-1] = 0
+    assert not check_attention(gkd, q, codes, scales, table, length, None, causal).any()
+
+
+def test_attention_many_sequences_with_room(gkd):
+    for B in (1024, 1025):
+        q, codes, scales, table = many_pages(B, 1, 2, 1, 64, 270, seed=B)
+        length = torch.randint(0, 40, (B,), generator=rng(B), device="cuda").to(torch.int32)
+        length[3], length[-1], length[700:720] = 2000, 8640, 0
+        check_attention(gkd, q, codes, scales, table, length)
+
+
+def test_attention_short_tiles_beside_a_long_one(gkd):
+    """One sequence of 960 rows and 120000 tokens, and 23 of one to three tokens: more tiles
+    than one share lists at a time."""
+    B, Tq, H, D = 24, 960, 4, 128
+    q, codes, scales, table = many_pages(B, Tq, H, H, D, 3750, seed=31)
+    length = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    length[::3], length[12] = 1, 120000
+    length[1::3] = 3
+    out = gkd.cache_attention(q, codes, scales, table, length=length)
+    rows = [0, 47, 48, 500, 959]
+    for b in (0, 1, 11, 12, 13, 23):
+        want, mean_abs, worst = of.attention(np64(q[b:b + 1, rows]), arr(codes), arr(scales), arr(table[b:b + 1]),
+                                             arr(length[b:b + 1]))
+        assert np.all(np.abs(np64(out[b:b + 1, rows]) - want) <= attention_tol(want, mean_abs, worst)), b
+    # a row's result is that of its sequence by itself, up to how its keys are cut: the short
+    # ones are one step, which is never cut
+    for b in (0, 1, 11, 13, 23):
+        alone = gkd.cache_attention(q[b:b + 1], codes, scales, table[b:b + 1, :1], length=length[b:b + 1])
+        assert torch.equal(out[b:b + 1], alone), b
 
 
 def test_attention_lengths_are_clamped(gkd):
@@ -650,6 +742,48 @@ def test_captured_step_follows_its_inputs(gkd):
         torch.cuda.synchronize()
         assert torch.equal(codes, c2) and torch.equal(scales, s2), i
         assert torch.equal(out, o2) and torch.equal(y, y2), i
+
+
+def test_captured_steps_of_long_caches_and_two_streams(gkd):
+    """Two captured steps with workspaces of their own, replayed side by side on two streams
+    while their inputs change between the replays."""
+    B, Hq, Hk, D, L = 3, 8, 2, 64, 200
+    need = gkd.cache_attention_workspace_size(B, 2, Hq, Hk, D, 32, L), gkd.linear_fp4_workspace_size(128, 1030, 8192)
+    assert min(need) > 0
+    g = rng(40)
+    wc, ws = gkd.quantize_fp4(randn(g, 1030, 8192, scale=1 / 64))
+    sets = []
+    for i in range(2):
+        q, codes, scales, table = many_pages(B, 2, Hq, Hk, D, L, seed=41 + i)
+        length, x = ints(6400, 1000 * i + 17, 90), randn(g, 128, 8192)
+        work = [torch.empty(n, dtype=U8, device="cuda") for n in need]
+        out, y = torch.empty_like(q), torch.empty(128, 1030, dtype=BF, device="cuda")
+
+        def step(q=q, codes=codes, scales=scales, table=table, length=length, x=x, work=work, out=out, y=y):
+            gkd.cache_attention(q, codes, scales, table, length=length, causal=True, out=out, workspace=work[0])
+            gkd.linear_fp4(x, wc, ws, out=y, workspace=work[1])
+
+        step()
+        st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=st):
+            step()
+        sets.append((q, codes, scales, table, length, x, out, y, st, graph))
+    for n in range(3):
+        for q, _, _, _, length, x, out, y, _, _ in sets:
+            length.sub_(5)
+            q.copy_(randn(g, *q.shape))
+            x.copy_(randn(g, *x.shape))
+            out.fill_(7)
+            y.fill_(7)
+        torch.cuda.synchronize()
+        for s in sets:
+            with torch.cuda.stream(s[8]):
+                s[9].replay()
+        torch.cuda.synchronize()
+        for q, codes, scales, table, length, x, out, y, _, _ in sets:
+            assert torch.equal(out, gkd.cache_attention(q, codes, scales, table, length=length, causal=True)), n
+            assert torch.equal(y, gkd.linear_fp4(x, wc, ws)), n
 
 
 def test_results_do_not_change_from_call_to_call(gkd):
