@@ -76,8 +76,7 @@ GKD_API gkd_status gkd_quantize_fp4(const void *x, int64_t ldx, int N, int K, gk
  *            no input
  * K a multiple of 32 (else GKD_ERR_UNSUPPORTED), 32 <= K < 2^22, M < 2^26,
  * N < 2^25, M N < 2^31, ldx < 2^22 (else GKD_ERR_SHAPE). flags must be 0.
- * M == 0 or N == 0: nothing is launched. Made for few rows, where reading
- * the weights is all the time; any M is taken.
+ * M == 0 or N == 0: nothing is launched.
  *   workspace  gkd_linear_fp4_workspace_size() bytes, 256-byte aligned (NULL
  *            where that is 0)
  */
@@ -112,7 +111,7 @@ typedef struct {
  *   count  [B] int32 or NULL (T); values are clamped to 0..T
  * Two tokens of a call must not have the same place (which of them, or what
  * mixture, stays is undefined). Nothing but the tokens' places is written.
- * B T below 2^31. flags must be 0.
+ * B T below 2^31, T below 2^30. flags must be 0.
  */
 GKD_API gkd_status gkd_cache_append(const gkd_heads *k, const gkd_heads *v, int B, int T,
                                     const int32_t *start, const int32_t *count,

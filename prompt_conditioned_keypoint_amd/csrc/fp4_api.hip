@@ -77,6 +77,9 @@ gkd::Pages pages_of(const gkd_cache* c, const int32_t* table, int L) {
   return gkd::Pages{c->codes, c->scales, c->pages, c->page, c->Hk, c->D, table, L};
 }
 
+// Tokens to move: a workgroup's last token is counted in 32 bits, in use or not.
+bool move_sizes_ok(int B, int T) { return B >= 0 && T >= 0 && T < (1 << 30) && (int64_t)B * T <= 0x7fffffffLL; }
+
 bool attn_sizes_ok(int B, int Tq, int Hq, int Hk) {
   if (B < 0 || Tq < 0 || Hq < 1 || Hk < 1) return false;
   if (B == 0 || Tq == 0) return true;
@@ -165,7 +168,7 @@ gkd_status gkd_cache_append(const gkd_heads* k, const gkd_heads* v, int B, int T
   gkd_status st;
   if ((st = check_flags(fn, flags, 0)) != GKD_OK) return st;
   if ((st = check_dtype(fn, dtype)) != GKD_OK) return st;
-  if (B < 0 || T < 0 || (int64_t)B * T > 0x7fffffffLL)
+  if (!move_sizes_ok(B, T))
     return fail(GKD_ERR_SHAPE, "%s: bad shape B=%d T=%d", fn, B, T);
   if ((st = check_cache(fn, cache, L)) != GKD_OK) return st;
   if (B == 0 || T == 0) return ok();
@@ -185,7 +188,7 @@ gkd_status gkd_cache_read(const gkd_cache* cache, const int32_t* table, int L, i
   const char* fn = "gkd_cache_read";
   gkd_status st;
   if ((st = check_flags(fn, flags, 0)) != GKD_OK) return st;
-  if (B < 0 || T < 0 || (int64_t)B * T > 0x7fffffffLL)
+  if (!move_sizes_ok(B, T))
     return fail(GKD_ERR_SHAPE, "%s: bad shape B=%d T=%d", fn, B, T);
   if ((st = check_cache(fn, cache, L)) != GKD_OK) return st;
   if (B == 0 || T == 0) return ok();

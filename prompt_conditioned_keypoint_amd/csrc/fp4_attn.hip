@@ -103,6 +103,13 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("" ::: "memory");
 }
 
+// What this wave has read of LDS is in its registers.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
+  asm volatile("" ::: "memory");
+}
+
 // A sequence's work: `tiles` tiles of `sub` times 16 rows of each key head, `steps`
 // steps of keys each. A step is taken to cost 3 + sub, its conversions beside the
 // products and exponents of its rows, and a tile kStart more, the wait for its queries and
@@ -434,6 +441,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
     there[kStages - 1] = false;
     for (int stage = 0; s < w.s1; s += NW) {
       const int next = stage == 0 ? kStages - 1 : stage - 1;  // the stage of the step before: it has been read
+      wait_lds();
       there[kStages - 1] = load(next, s + kStages * NW);
       wait_vm<(kStages - 1) * St::kLoads>();
       const unsigned char* at = ring + stage * St::kBytes;

@@ -1,12 +1,20 @@
 // fp4_linear.hip - matrix product with four-bit weights (gkd_linear_fp4):
 // out = act(x w^T + bias) + residual.
 //
-// A wave takes 16 rows of w and 128 of K at a time: each lane one group of 32
-// codes (16 bytes) and its scale byte, which the conversion instructions turn into
-// the first operand of four v_mfma_f32_16x16x32_bf16. Which k a lane's place in the
-// instruction stands for is free as long as x is read alike: place (g, i) of
-// product t is k = 32 g + 8 t + i. So weights go from memory to the matrix pipe
-// through registers alone, and nothing is rounded on the way.
+// A lane holds part of one group of 32 codes of a row of w and its scale byte, which the
+// conversion instructions turn into the first operand of v_mfma_f32_16x16x32_bf16, eight
+// values at a time and exactly. Which k a lane's place in the instruction stands for is
+// free as long as x is read alike: place (g, i) of product t is k = 32 g + 8 t + i, so a
+// lane's 16 bytes of codes are its operands of four products. Both operands go through
+// rings in LDS, for loads of whole lines and many of them under way; nothing is rounded on
+// the way, and sums of ranges of K meet in a fixed order.
+//
+// What bounds it: few rows, the codes' way from memory. 1 x 4096 x 16384 takes 10.3 us,
+// 3.4 TB/s where a large copy on the same card moves 5.0; 13 x 16384 x 4095 13.4 us
+// (2.7 TB/s); 1 x 1024 x 1024 2.8 us, little more than a launch. Up to some hundreds of
+// rows, the loads that a CU has under way, x from L2 beside the codes: 37 x 1024 x 4096
+// 6.0 us, 128 x 8192 x 8192 32 us, 0.54 PF. (The registers alone, without LDS, took 13.8,
+// 21.2, 2.8, 8.4 and 128 us.)
 #include "epilogue.hpp"
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
@@ -63,9 +71,16 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("" ::: "memory");
 }
 
+// What this wave has read of LDS is in its registers.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
+  asm volatile("" ::: "memory");
+}
+
 // All waves, with what they read of LDS in their registers.
 __device__ __forceinline__ void meet() {
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
+  wait_lds();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -174,6 +189,7 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(Fp4Params p) {
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) load(i);
     for (int i = 0, stage = 0; i < n; ++i) {
+      wait_lds();
       load(stage == 0 ? STAGES - 1 : stage - 1);  // the stage before: it has been read
       wait_vm<(STAGES - 1) * St::kLoads>();
       product(stage);

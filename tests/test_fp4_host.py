@@ -110,6 +110,12 @@ def test_append_and_read_reject(lib, kw, status):
         assert lib.gkd_last_error().decode() != ""
 
 
+def test_append_and_read_reject_tokens_that_32_bits_do_not_count(lib):
+    for call in (append, read):
+        assert call(lib, B=1, T=1 << 30) == SHAPE and call(lib, B=1, T=(1 << 31) - 1) == SHAPE
+        assert call(lib, B=0, T=(1 << 30) - 1) == 0
+
+
 BAD_CACHES = [(dict(pages=-1), SHAPE), (dict(page=0), SHAPE), (dict(page=1 << 17), SHAPE), (dict(Hk=0), SHAPE),
               (dict(Hk=1 << 17), SHAPE), (dict(D=0), SHAPE), (dict(D=96), UNSUP), (dict(page=48), UNSUP),
               (dict(page=16), UNSUP), (dict(codes=None), NULL), (dict(scales=None), NULL),
