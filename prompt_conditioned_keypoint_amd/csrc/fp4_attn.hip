@@ -85,7 +85,7 @@ __device__ __forceinline__ float far_exponent(float score, float scale, float m)
 // A step's place in a wave's ring in LDS: the codes of 32 keys, those of their values,
 // and the scale bytes of both. LDS has 64 banks of 4 bytes, a row of codes is D/2 bytes,
 // and rows are placed so that no reading below meets itself in a bank:
-//   keys     16-byte piece c of row r at piece c ^ (r / 4) % 4 (D 64: c ^ (r / 8) % 2), for
+//   keys     16-byte piece c of row r at piece c ^ turned(r / 4) (D 64: c ^ (r / 8) % 2), for
 //            lanes that read the same piece of 16 rows;
 //   values   row 4 g + e of 16 at row 4 g + (e ^ g) (D 64: e ^ (g & 2)), for lanes that
 //            read all of the rows 4 g + e, g = 0 .. 3.
@@ -95,6 +95,11 @@ struct Stage {
   static constexpr int kCodes = 32 * D / 2, kValues = kCodes, kScales = 2 * kCodes;
   static constexpr int kBytes = 2 * kCodes + 256, kLoads = D == 128 ? 5 : 3;
 };
+
+// 0 1 2 3 -> 0 2 3 1. LDS serves lanes 0-3, 12-15 and 20-27 (and the like) of 16-byte reads
+// together: rows r / 4 of 0 and 3 with one g, of 1 and 2 with the next, so that
+// g ^ (r / 4) would send two lanes to a bank.
+__device__ __forceinline__ int turned(int j) { return (j & 1 ^ j >> 1 & 1) << 1 | (j >> 1 & 1); }
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -258,7 +263,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
   // What a lane loads of a step, 16 bytes of codes and 4 of scales at a time.
   constexpr int PR = D / 32;  // 16-byte pieces of a row
   const int lr = lane / PR, lc = lane % PR;
-  const int kc = lc ^ (D == 128 ? (lr >> 2) & 3 : (lr >> 3) & 1);
+  const int kc = lc ^ (D == 128 ? turned(lr >> 2) : (lr >> 3) & 1);
   const int vr = (lr & ~3) | ((lr & 3) ^ (D == 128 ? (lr >> 2) & 3 : (lr >> 2) & 2));
   const uint8_t* kcodes = p.c.codes + first_row * (D / 2) + lr * (D / 2) + kc * 16;
   const uint8_t* vcodes = p.c.codes + (first_row + head_rows) * (D / 2) + vr * (D / 2) + lc * 16;
@@ -294,7 +299,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
   // Where a lane reads: of keys fr and 16 + fr the D/4 elements from g D/4, with their
   // group's scale byte; of the values the D/16 elements from fr D/16 of eight keys, with
   // the scale bytes of four neighbouring keys at a time.
-  const int kat = D == 128 ? fr * 64 + ((g ^ (fr >> 2)) << 4) : fr * 32 + (((g >> 1) ^ (fr >> 3)) << 4) + (g & 1) * 8;
+  const int kat = D == 128 ? fr * 64 + ((g ^ turned(fr >> 2)) << 4) : fr * 32 + (((g >> 1) ^ (fr >> 3)) << 4) + (g & 1) * 8;
   const int ksat = St::kScales + fr * (D / 32) + (D == 128 ? g : g / 2);
   const int vsat = St::kScales + D + g * (D / 8);
   int vat[4];

@@ -71,6 +71,12 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("" ::: "memory");
 }
 
+// The place of piece c of row r of x, in rows of 256 bytes, is c ^ turned(r). Sixteen lanes
+// that LDS serves together are, of a wave's 16-byte reads, lanes 0-3, 12-15 and 20-27 (and
+// the like): rows of two neighbouring g, whose pieces differ in bit 2. So bit 3 is made to
+// tell them apart (c ^ r: two lanes to a bank, 43% of the LDS cycles of 128 x 8192 x 8192).
+__device__ __forceinline__ int turned(int r) { return (r & 15) ^ ((r & 4) << 1); }
+
 // What this wave has read of LDS is in its registers.
 __device__ __forceinline__ void wait_lds() {
   asm volatile("" ::: "memory");
@@ -87,7 +93,7 @@ __device__ __forceinline__ void meet() {
 
 // A stage of a wave's ring: 256 of K of 16 NT rows of w and MX rows of x (two at least, as
 // a load brings two), 16-byte piece c of a row at piece c ^ (row / 2) % 8 of w and
-// c ^ row % 16 of x, so that 16 lanes that read the same piece of 16 rows share no bank.
+// c ^ turned(row) of x, so that 16 lanes that read the same piece of 16 rows share no bank.
 // Scale bytes come four at a time where rows of them are whole words, else (BYTES) one by
 // one, each into a word.
 template <int MX, int NT, bool BYTES>
@@ -144,7 +150,7 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(Fp4Params p) {
     }
 #pragma unroll
     for (int i = 0; i < St::kRowsX / 2; ++i) {
-      const int r = 2 * i + xr, k = k0 + 8 * ((lane & 31) ^ (r & 15));
+      const int r = 2 * i + xr, k = k0 + 8 * ((lane & 31) ^ turned(r));
       const uint32_t a = k < p.K && r < MX ? (uint32_t)r * (uint32_t)p.ldx * 2u + 2 * k : kNowhere;
       load16(xb, dst + St::kX + i * 1024, a);
     }
@@ -175,7 +181,7 @@ __global__ __launch_bounds__(64 * NW) void fp4_few_kernel(Fp4Params p) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
           x[i] = frag(*reinterpret_cast<const u32x4*>(src + St::kX + (16 * i + xrow) * 512 +
-                                                      (((16 * h + 4 * g + t) ^ xrow) << 4)));
+                                                      (((16 * h + 4 * g + t) ^ turned(xrow)) << 4)));
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const bf16x8 w = frag(fp4_values(c[j][t], unit[j]));
@@ -281,7 +287,7 @@ __global__ __launch_bounds__(128 * WM * WN) void fp4_tile_kernel(TileParams tp) 
     const int k0 = left > 0 ? (from + at) * 256 + sub * KC : p.K;  // past K: zeros
 #pragma unroll
     for (int u = 0; u < St::kLoadsX; ++u) {
-      const int i = (gw + u * St::W) % St::kNX, r = i * XR + lane / XP, k = k0 + 8 * ((lane % XP) ^ (r & 15));
+      const int i = (gw + u * St::W) % St::kNX, r = i * XR + lane / XP, k = k0 + 8 * ((lane % XP) ^ turned(r));
       const uint32_t a = k < p.K ? (uint32_t)r * (uint32_t)p.ldx * 2u + 2 * k : kNowhere;
       load16(xb, dst + i * 1024, a);
     }
@@ -322,13 +328,15 @@ __global__ __launch_bounds__(128 * WM * WN) void fp4_tile_kernel(TileParams tp) 
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int wrow = wn * 16 * NT + fr, xrow = wm * 16 * MT + fr;
-  // 128 of K, the h-th of their stages; this wave's half of each group
+  // 128 of K, the h-th of their stages; this wave's half of each group, by turns the first and
+  // the second for neighbouring g, whose lanes would meet in a bank otherwise
+  const int half = kg ^ (g & 1);
   auto product = [&](const unsigned char* sx, int hx, const unsigned char* sc, int hc) {
     u32x2 c[NT];
     float unit[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      c[j] = *reinterpret_cast<const u32x2*>(sc + (wrow + 16 * j) * 128 + (((4 * hc + g) ^ (fr >> 1)) << 4) + 8 * kg);
+      c[j] = *reinterpret_cast<const u32x2*>(sc + (wrow + 16 * j) * 128 + (((4 * hc + g) ^ (fr >> 1)) << 4) + 8 * half);
       unit[j] = fp4_unit(sc[St::kScales + ((wrow + 16 * j) * 8 + 4 * hc + g) * (BYTES ? 4 : 1)]);
     }
     bf16x8 x[2][MT];
@@ -337,7 +345,7 @@ __global__ __launch_bounds__(128 * WM * WN) void fp4_tile_kernel(TileParams tp) 
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         x[u][i] = frag(*reinterpret_cast<const u32x4*>(sx + (xrow + 16 * i) * (2 * KC) +
-                                                       (((16 * hx + 4 * g + 2 * kg + u) ^ fr) << 4)));
+                                                       (((16 * hx + 4 * g + 2 * half + u) ^ turned(fr)) << 4)));
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
