@@ -487,6 +487,20 @@ def test_attention_many_rows(gkd, D):
     check_attention(gkd, q, codes, scales, table, ints(300), causal=True)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,Tq,Hq,Hk", [(90, 1, 6, 3), (45, 10, 9, 3), (30, 20, 6, 3), (20, 36, 6, 3), (70, 65, 4, 1)])
+def test_attention_more_tiles_than_compute_units(gkd, B, Tq, Hq, Hk, D, causal):
+    """One, two, three and more tiles of 16 rows of a key head, all of them or as many as a
+    sequence has."""
+    q, codes, scales, table = many_pages(B, Tq, Hq, Hk, D, 5, seed=Tq)
+    length = torch.randint(0, 161, (B,), generator=rng(B), device="cuda").to(torch.int32)
+    q_len = torch.randint(0, Tq + 1, (B,), generator=rng(B + 1), device="cuda").to(torch.int32)
+    length[0], q_len[0], length[1], q_len[2] = 160, Tq, 0, 0
+    table[3:9, 1] = -1
+    check_attention(gkd, q, codes, scales, table, length, q_len, causal)
+
+
 def many_pages(B, Tq, Hq, Hk, D, L, seed):
     """Room for 32 L tokens a sequence on a few pages, so that columns share them: keys are
     few to look at, and how the work is cut goes by the room."""
