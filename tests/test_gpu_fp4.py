@@ -623,6 +623,35 @@ def test_attention_large_scores_keep_their_largest(gkd, D):
                     assert np.array_equal(np64(got)[0, t, h], v[first, h // 2])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_large_scores_in_parts(gkd, D):
+    """As above, the keys in parts that are joined, with what lies behind them not a number."""
+    q, codes, scales, table = attn_inputs(2, 2, 4, 2, D, 32, 140, seed=21)
+    assert gkd.cache_attention_workspace_size(2, 2, 4, 2, D, 32, 140) > 0
+    n = 4433
+    flat = table.long().flatten(1)
+    for b in range(2):
+        scales[flat[b, n // 32], :, :, n % 32:] = 255
+        scales[flat[b, n // 32 + 1:]] = 255
+    length = ints(n, n)
+    check_attention(gkd, q, codes, scales, table, length)
+    for scale in (1e6, 1e20, 1e30):
+        got = gkd.cache_attention(q, codes, scales, table, length=length, scale=scale)
+        assert bool(torch.isfinite(got).all())
+        k, v = (np64(t) for t in gkd.cache_read(codes, scales, table, n))
+        for b in range(2):
+            for t in range(2):
+                for h in range(4):
+                    s = k[b, :, h // 2] @ np64(q)[b, t, h]
+                    first, second = np.argsort(-s)[:2]
+                    if s[first] - s[second] > 1e-3 * abs(s[first]):
+                        assert np.array_equal(np64(got)[b, t, h], v[b, first, h // 2])
+    q2 = q * 30
+    q2[1, 1, 2] = q[1, 1, 2]
+    a, b = (gkd.cache_attention(x, codes, scales, table, length=length) for x in (q, q2))
+    assert torch.equal(a[1, 1, 2], b[1, 1, 2])
+
+
 def test_attention_small_scale_is_the_mean(gkd):
     q, codes, scales, table = attn_inputs(1, 1, 2, 1, 64, 32, 3, seed=12)
     check_attention(gkd, q, codes, scales, table, ints(90), scale=1e-30)
