@@ -11,10 +11,10 @@
 // looked up once, while its values are on their way. (Heads neighbouring in a wave instead:
 // the same time; a place looked up for every piece: 1.6 times as long.)
 //
-// Memory bounds both. 64 x 581 tokens of 16 heads of 64, 193 MB each way: 56 us to append
-// (3.4 TB/s) and 31 us to read (6.2, what was just appended still being in the last cache;
-// a large copy on the same card moves 5.0). One token of 48 sequences, 8 heads of 128: 2.5 us
-// each, a launch's time.
+// Memory bounds both. 64 x 581 tokens of 16 heads of 64, 193 MB each way: 48 to 57 us to
+// append (3.4 to 4.0 TB/s) and 43 us to read (4.5; 31 where what was just appended is still in
+// the last cache); a large copy on the same card moves 5.0. One token of 48 sequences, 8 heads
+// of 128: 3.3 and 3.1 us, a launch's time.
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 
@@ -72,7 +72,9 @@ __global__ __launch_bounds__(256) void fp4_quantize_kernel(QuantParams p) {
   }
 }
 
-constexpr int kHeads = 4;  // a thread's heads, keys' and values'
+// A thread's heads, keys' and values': loads under way against registers (64 x 581 tokens
+// appended and read, us: 1 head 64 and 64, 2 heads 54 and 51, 4 heads 48 and 43, 8 appended 51).
+constexpr int kHeads = 4;
 
 struct MoveParams {
   Heads k, v;
