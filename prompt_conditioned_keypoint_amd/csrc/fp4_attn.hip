@@ -748,7 +748,8 @@ constexpr int kWaves = 4, kManyWaves = 8;
 // more than a tile of 16 rows for each compute unit, every tile has a workgroup of eight
 // waves (80 rows of 2 x 8 heads of 64, 2304 tokens: 11.1 us, in twos 17.3; one row of 16
 // heads and 2304 tokens: 10.8 us, with four waves 13.8; 384 tiles of 2048 tokens would take
-// 24.9 with eight, 22.2 with four). Else up to three tiles go together (37 x 40 rows of 16
+// 24.9 with eight, 22.2 with four). Else four waves (37 x 80 rows of 16 heads of 64, 2304
+// tokens: two 64 us, four 61, eight 70), and up to three tiles go together (37 x 40 rows of 16
 // heads of 64, 2304 tokens: 39 us, in twos 47), and more than three in twos: as fast as in
 // threes where all have as many (37 x 80 rows: 65 us and 62; 16 x 128 rows of 32 heads of
 // 128, 4096 tokens: 165 and 166) and ahead where not (37 sets of up to 80 rows: 35 and 44).
