@@ -743,6 +743,7 @@ struct Plan {
 };
 
 constexpr int kWaves = 4, kManyWaves = 8;
+constexpr int kLong = 128;
 
 // R, tiles of 16 rows that go through the keys together, and a workgroup's waves. With no
 // more than a tile of 16 rows for each compute unit, every tile has a workgroup of eight
@@ -759,7 +760,17 @@ constexpr int kWaves = 4, kManyWaves = 8;
 // sequence of 32 heads on 8 of 128: 2048 tokens 12.2 us in tiles and 15.2 in shares, 4096
 // 20.1 and 14.0, 32768 128 and 20; 16 of them: 4096 tokens 22 and 25, 8192 37 and 36; 48 at
 // 8192 81 and 93, at lengths from 1 to 8192 54 and 46, one at 8000 among short ones 47 and
-// 22. Among four times as many tiles as stay resident the longest one does not count.
+// 22.
+//
+// Among four times as many tiles as stay resident, a workgroup a tile again, if the longest
+// possible tile does not outlast the others by much: at most kLong steps for each round of
+// tiles (a round takes 4 to 5 us however short its tiles are, a step of the longest 0.18), or
+// a sequence that has so many tiles by itself; and if the XCDs, each of which takes whole key
+// heads, get nearly the same. Us, in tiles / in shares: 512 sequences of 32 heads on 8 of 128,
+// all of 16384 tokens 1464 / 1505, 1 to 16384 805 / 804, one of 16384 among short ones 101 / 48,
+// of 32768 193 / 50, of 262144 1493 / 89; 256 x 64 rows of 16 heads of 64, all of 32768 tokens
+// 3439 / 4364; 4096 rows of 32 heads of 128 behind 16384 tokens on 8 key heads 1093 / 1252, on
+// 4 2142 / 1268, of 24 heads on 12 1101 / 921.
 Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   const int rows = Tq * (Hq / Hk), subs = (rows + 15) / 16;
   const long long heads = (long long)B * Hk, steps = ((long long)L * page + 31) / 32;
@@ -773,7 +784,9 @@ Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   if (B > kMaxSequences || steps <= 96 + (items < 640 ? items : 640) / 4) return x;
   // (shares are even whatever the tiles are, so theirs are as large as can be)
   const int R = subs < 3 ? subs : 3, tiles = (subs + R - 1) / R, resident = 256 * waves_of(D, R);
-  if (heads * tiles >= 4 * resident) return x;
+  const bool bounded = steps * resident <= kLong * heads * tiles || (long long)Hk * tiles >= 4 * resident;
+  const bool even = 8 * ((heads + kXcds - 1) / kXcds * kXcds) <= 9 * heads;
+  if (heads * tiles >= 4 * resident && bounded && even) return x;
   const long long most = heads * tiles * steps / (2 * kWaves);
   x.R = R;
   x.tiles = tiles;

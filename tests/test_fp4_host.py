@@ -192,6 +192,19 @@ def test_attention_checks_its_workspace(lib):
         assert size(*bad) == 0, bad
 
 
+def test_attention_shares_what_one_long_sequence_would_hold_up(lib):
+    """Work is cut evenly, which takes a workspace, wherever the room lets one tile outlast
+    many others, or the key heads leave XCDs without work."""
+    size = lib.gkd_cache_attention_workspace_size
+    for B, Tq, Hq, Hk, D, room in ((512, 1, 32, 8, 128, 262144), (512, 1, 32, 8, 128, 32768),
+                                   (600, 1, 16, 8, 128, 65536),
+                                   (1, 4096, 32, 4, 128, 16384), (1, 4096, 24, 12, 128, 16384)):
+        assert size(B, Tq, Hq, Hk, D, 64, room // 64) > 0, (B, Tq, Hq, Hk, D, room)
+    for B, Tq, Hq, Hk, D, room in ((512, 1, 32, 8, 128, 16384), (1, 4096, 32, 8, 128, 65536),
+                                   (256, 64, 16, 16, 64, 32768)):
+        assert size(B, Tq, Hq, Hk, D, 64, room // 64) == 0, (B, Tq, Hq, Hk, D, room)
+
+
 def test_python_calls_reject_cpu_tensors():
     import prompt_conditioned_keypoint_amd as gkd
     bf, u8 = torch.bfloat16, torch.uint8

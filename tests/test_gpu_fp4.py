@@ -557,6 +557,43 @@ def test_attention_short_tiles_beside_a_long_one(gkd):
         assert torch.equal(out[b:b + 1], alone), b
 
 
+def test_attention_a_long_sequence_among_many_tiles(gkd):
+    """More than four times as many tiles as stay resident, and room for one sequence to
+    outlast them: its keys are shared, the short ones are as they are by themselves."""
+    B, H, D, L = 600, 8, 128, 1100
+    assert gkd.cache_attention_workspace_size(B, 1, H, H, D, 32, L) > 0
+    q, codes, scales, table = many_pages(B, 1, H, H, D, L, seed=51)
+    length = torch.randint(0, 33, (B,), generator=rng(52), device="cuda").to(torch.int32)
+    length[0], length[200], length[201], length[599] = 4000, 35011, 0, 700
+    out = gkd.cache_attention(q, codes, scales, table, length=length)
+    for b in (0, 200, 599):
+        want, mean_abs, worst = of.attention(np64(q[b:b + 1]), arr(codes), arr(scales), arr(table[b:b + 1]),
+                                             arr(length[b:b + 1]))
+        assert np.all(np.abs(np64(out[b:b + 1]) - want) <= attention_tol(want, mean_abs, worst)), b
+    alone = gkd.cache_attention(q, codes, scales, table[:, :1].contiguous(), length=length.clamp_max(32))
+    one_step = length <= 32
+    assert torch.equal(out[one_step], alone[one_step])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_attention_many_rows_of_one_key_head(gkd, causal):
+    """As many tiles, all of one key head: they are spread over the whole GPU."""
+    Tq, Hq, D, L = 9300, 16, 64, 260
+    assert gkd.cache_attention_workspace_size(1, Tq, Hq, 1, D, 32, L) > 0
+    q, codes, scales, table = many_pages(1, Tq, Hq, 1, D, L, seed=53)
+    q_len, length = 9290, 8300
+    out = torch.full_like(q, 7)
+    gkd.cache_attention(q, codes, scales, table, length=ints(length), q_len=ints(q_len), causal=causal, out=out)
+    assert bool((out[:, q_len:] == 7).all())
+    for t in (0, 1, 900, 989, 990, 991, 992, 1021, 5000, 9288, 9289):
+        sees = length - q_len + t + 1 if causal else length
+        if sees <= 0:
+            assert not out[:, t].any(), t
+            continue
+        want, mean_abs, worst = of.attention(np64(q[:, t:t + 1]), arr(codes), arr(scales), arr(table), np.array([sees]))
+        assert np.all(np.abs(np64(out[:, t:t + 1]) - want) <= attention_tol(want, mean_abs, worst)), t
+
+
 def test_attention_lengths_are_clamped(gkd):
     q, codes, scales, table = attn_inputs(3, 2, 2, 1, 64, 32, 2, seed=6)
     check_attention(gkd, q, codes, scales, table, ints(1000, -5, 2**31 - 1), ints(-3, 9, 1))
