@@ -45,6 +45,7 @@ struct CaParams {
   int causal;
   int tiles;        // tiles of 16 R rows that a sequence's key head can have
   int shares;       // workgroups that share the work; 0: each takes a tile with all its keys
+  int group;        // sequences of an entry of the running sum of the work
   int32_t* ends;    // [B Hk tiles][2] first and last share of a cut tile; first -1: not cut
   float* po;        // [shares][2][16 R][D] parts of rows
   float* ml;        // [shares][2][16 R][2]
@@ -535,7 +536,10 @@ __device__ __forceinline__ void attend_tile(const CaParams& p, const Work& w, un
 // compute unit holds.
 constexpr int waves_of(int D, int R) { return (D == 128 ? 5 : 6) - R; }
 
-constexpr int kMaxSequences = 1024;  // whose work is shared evenly
+// Entries of the running sum of the work, of a sequence each or a group of them. (1025 sequences
+// of 8 heads on 1 of 128, one of 262144 tokens among short ones: 68 us, a workgroup a tile 1480;
+// at 1 to 16384 tokens 235 and 271, all of 16384 432 and 426, all short 26 and 10.)
+constexpr int kMaxEntries = 1024;
 
 // A workgroup a tile, with all its keys.
 template <int D, int R, int NW>
@@ -549,38 +553,46 @@ __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_attn_kernel(CaP
   attend_tile<D, R, NW>(p, work_of<R>(p, q, b, at.crop - b * p.c.Hk, at.item, 0, q.steps, -1), lds);
 }
 
-// The next pieces of the workgroup's share, after those before state[1], state[2] (-1: from
-// its begin; and left so when they are all listed).
+// Where a workgroup is in its share: the next tile (of sequence b, whose work begins at
+// `base`; -1: from the share's begin) and what is listed. b -1: all of it is.
 constexpr int kPieces = 32;
+struct Listing {
+  long long begin, end, base;
+  int share, b, tile, n;
+};
 
-template <int R>
-__device__ __forceinline__ void list_pieces(const CaParams& p, const long long* cum, int32_t (*piece)[kWorkInts],
-                                            int32_t* state) {
-  const bool first = threadIdx.x == 0;
-  int n = 0, b = uniform(state[1]), tile = uniform(state[2]);
-  const long long total = uniform(cum[p.B]);
+// The workgroup's share, and the first sequence of the entry of `cum` that it begins in.
+__device__ __forceinline__ void find_share(const CaParams& p, const long long* cum, int entries, Listing* list) {
+  const long long total = uniform(cum[entries]);
   const int count = uniform(share_count(p, total));
   const bool any = (int)blockIdx.x < count && total > 0;
   // neighbouring shares, which read the same keys, on one XCD
   const int x = blockIdx.x % kXcds, share = x * (count / kXcds) + min(x, count % kXcds) + blockIdx.x / kXcds;
   const Shares shares = shares_of(total, count);
   const long long begin = any ? uniform(shares.begin(share)) : 0, end = any ? uniform(shares.begin(share + 1)) : 0;
-  if (any && b < 0) {
-    int hi = p.B;  // cum[b] <= begin < cum[hi]
-    b = 0;
-    while (hi - b > 1) {
-      const int mid = (b + hi) / 2;
-      if (uniform(cum[mid]) <= begin) b = mid;
-      else hi = mid;
-    }
+  int lo = 0, hi = entries;  // cum[lo] <= begin < cum[hi]
+  while (any && hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (uniform(cum[mid]) <= begin) lo = mid;
+    else hi = mid;
   }
-  for (; any && b < p.B; ++b, tile = -1) {
-    const long long base = uniform(cum[b]);
-    if (base >= end) break;
+  const long long base = uniform(cum[lo]);
+  if (threadIdx.x == 0) *list = Listing{begin, end, base, share, any ? lo * p.group : -1, -1, 0};
+}
+
+template <int R>
+__device__ __forceinline__ void list_pieces(const CaParams& p, int32_t (*piece)[kWorkInts], Listing* list) {
+  const bool first = threadIdx.x == 0;
+  int n = 0, b = uniform(list->b), tile = uniform(list->tile);
+  const int share = uniform(list->share);
+  const long long begin = uniform(list->begin), end = uniform(list->end);
+  long long base = uniform(list->base);
+  for (; b >= 0 && b < p.B && base < end; ++b, tile = -1) {
     const Sequence q = sequence<R>(p, b);
-    const long long per = q.tile_work();
+    const long long per = uniform(q.tile_work());
     if (per == 0 || q.tiles == 0) continue;
-    if (tile < 0) tile = begin > base ? uniform((int)quotient(begin - base, per)) : 0;
+    // (past the sequence's tiles where it lies before the share)
+    if (tile < 0) tile = begin > base ? (int)min(uniform(quotient(begin - base, per)), (1LL << 30)) : 0;
     for (; tile < q.tiles * p.c.Hk && n < kPieces; ++tile) {
       const long long at = base + tile * per;
       if (at >= end) break;
@@ -598,11 +610,13 @@ __device__ __forceinline__ void list_pieces(const CaParams& p, const long long* 
       ++n;
     }
     if (n == kPieces) break;
+    base += per * q.tiles * p.c.Hk;
   }
   if (first) {
-    state[0] = n;
-    state[1] = n == kPieces ? b : -1;
-    state[2] = tile;
+    list->n = n;
+    list->b = n == kPieces ? b : -1;
+    list->tile = tile;
+    list->base = base;
   }
 }
 
@@ -614,35 +628,42 @@ template <int D, int R, int NW>
 __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(CaParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   __shared__ int32_t piece[kPieces][kWorkInts];
-  __shared__ int32_t state[3];  // pieces, where to go on (sequence, tile)
-  long long* cum = reinterpret_cast<long long*>(lds);  // [B + 1] work before each sequence
-  if (threadIdx.x == 0) state[1] = state[2] = -1;
+  __shared__ Listing list;
+  long long* cum = reinterpret_cast<long long*>(lds);  // [entries + 1] work before each group of sequences
+  const int entries = (p.B + p.group - 1) / p.group;
+  for (int i = threadIdx.x; i < entries; i += 64 * NW) {
+    long long sum = 0;
+    for (int b = i * p.group; b < min((i + 1) * p.group, p.B); ++b) {
+      const Sequence q = sequence<R>(p, b);
+      sum += q.tile_work() * q.tiles * p.c.Hk;
+    }
+    cum[i + 1] = sum;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    long long sum = 0;
+    for (int i0 = 0; i0 < entries; i0 += 64) {
+      const int i = i0 + threadIdx.x;
+      long long v = i < entries ? cum[i + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const long long u = __shfl_up(v, d);
+        if ((int)threadIdx.x >= d) v += u;
+      }
+      if (i < entries) cum[i + 1] = sum + v;
+      sum += __shfl(v, 63);
+    }
+    if (threadIdx.x == 0) cum[0] = 0;
+    find_share(p, cum, entries, &list);
+  }
+  __syncthreads();
   // The share's pieces are listed some at a time, and nothing of the sharing stays in
   // registers while they are worked on.
   for (;;) {
-    for (int b = threadIdx.x; b < p.B; b += 64 * NW) {
-      const Sequence q = sequence<R>(p, b);
-      cum[b + 1] = q.tile_work() * q.tiles * p.c.Hk;
-    }
+    if (threadIdx.x < 64) list_pieces<R>(p, piece, &list);
     __syncthreads();
-    if (threadIdx.x < 64) {
-      long long sum = 0;
-      for (int b0 = 0; b0 < p.B; b0 += 64) {
-        const int b = b0 + threadIdx.x;
-        long long v = b < p.B ? cum[b + 1] : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-          const long long u = __shfl_up(v, d);
-          if ((int)threadIdx.x >= d) v += u;
-        }
-        if (b < p.B) cum[b + 1] = sum + v;
-        sum += __shfl(v, 63);
-      }
-      if (threadIdx.x == 0) cum[0] = 0;
-      list_pieces<R>(p, cum, piece, state);
-    }
-    __syncthreads();
-    const int n = uniform(state[0]);
+    const int n = uniform(list.n);
+    const bool last = uniform(list.b) < 0;
     for (int k = 0; k < n; ++k) {
       int32_t v[kWorkInts];
 #pragma unroll
@@ -653,7 +674,7 @@ __global__ __launch_bounds__(64 * NW, waves_of(D, R)) void cache_share_kernel(Ca
       attend_tile<D, R, NW>(p, w, lds);
     }
     __syncthreads();
-    if (uniform(state[1]) < 0) break;
+    if (last) break;
   }
 }
 
@@ -781,7 +802,7 @@ Plan plan_for(int B, int Tq, int Hq, int Hk, int D, int page, int L) {
   x.waves = few ? kManyWaves : kWaves;
   x.shares = 0;
   const long long items = heads * x.tiles;
-  if (B > kMaxSequences || steps <= 96 + (items < 640 ? items : 640) / 4) return x;
+  if (steps <= 96 + (items < 640 ? items : 640) / 4) return x;
   // (shares are even whatever the tiles are, so theirs are as large as can be)
   const int R = subs < 3 ? subs : 3, tiles = (subs + R - 1) / R, resident = 256 * waves_of(D, R);
   const bool bounded = steps * resident <= kLong * heads * tiles || (long long)Hk * tiles >= 4 * resident;
@@ -802,7 +823,7 @@ size_t po_bytes(const Plan& x, int D) { return al256((size_t)x.shares * 2 * 16 *
 template <int D, int NW>
 constexpr int lds_bytes() {
   constexpr int kRing = NW * kStages * Stage<D>::kBytes, kJoin = NW * 16 * (D + 4 + 2) * 4;
-  static_assert((kMaxSequences + 1) * 8 <= kRing, "the work before each sequence fits");
+  static_assert((kMaxEntries + 1) * 8 <= kRing, "the running sum fits");
   return kRing > kJoin ? kRing : kJoin;
 }
 
@@ -867,6 +888,7 @@ hipError_t launch_cache_attn(const CacheAttnArgs& a, hipStream_t st) {
   p.causal = a.causal;
   p.tiles = x.tiles;
   p.shares = x.shares;
+  p.group = (a.B + kMaxEntries - 1) / kMaxEntries;
   if (x.shares > 0) {
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     p.ends = reinterpret_cast<int32_t*>(ws);

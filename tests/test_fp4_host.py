@@ -205,6 +205,12 @@ def test_attention_shares_what_one_long_sequence_would_hold_up(lib):
         assert size(B, Tq, Hq, Hk, D, 64, room // 64) == 0, (B, Tq, Hq, Hk, D, room)
 
 
+def test_attention_shares_the_work_of_any_number_of_sequences(lib):
+    size = lib.gkd_cache_attention_workspace_size
+    for B in (1024, 1025, 2049, 8192):
+        assert size(B, 1, 8, 1, 128, 64, 4096) > 0, B
+
+
 def test_python_calls_reject_cpu_tensors():
     import prompt_conditioned_keypoint_amd as gkd
     bf, u8 = torch.bfloat16, torch.uint8

@@ -594,6 +594,26 @@ def test_attention_many_rows_of_one_key_head(gkd, causal):
         assert np.all(np.abs(np64(out[:, t:t + 1]) - want) <= attention_tol(want, mean_abs, worst)), t
 
 
+@pytest.mark.parametrize("B,Hk,L,long", [(2500, 1, 520, {0: 700, 3: 16600, 1026: 5000, 2499: 90}),
+                                         (10500, 4, 4300, {7: 1000, 5003: 17000, 10498: 5000})])
+def test_attention_shares_many_sequences(gkd, B, Hk, L, long):
+    """Several sequences an entry of the running sum, more than one listing's pieces a share."""
+    assert gkd.cache_attention_workspace_size(B, 1, Hk, Hk, 64, 32, L) > 0
+    q, codes, scales, table = many_pages(B, 1, Hk, Hk, 64, L, seed=B)
+    length = torch.randint(0, 33, (B,), generator=rng(B), device="cuda").to(torch.int32)
+    length[100:108], length[1030:1033] = 0, 0
+    for b, n in long.items():
+        length[b] = n
+    out = gkd.cache_attention(q, codes, scales, table, length=length)
+    for b in long:
+        want, mean_abs, worst = of.attention(np64(q[b:b + 1]), arr(codes), arr(scales), arr(table[b:b + 1]),
+                                             arr(length[b:b + 1]))
+        assert np.all(np.abs(np64(out[b:b + 1]) - want) <= attention_tol(want, mean_abs, worst)), b
+    alone = gkd.cache_attention(q, codes, scales, table[:, :1].contiguous(), length=length.clamp_max(32))
+    one_step = length <= 32
+    assert torch.equal(out[one_step], alone[one_step])
+
+
 def test_attention_lengths_are_clamped(gkd):
     q, codes, scales, table = attn_inputs(3, 2, 2, 1, 64, 32, 2, seed=6)
     check_attention(gkd, q, codes, scales, table, ints(1000, -5, 2**31 - 1), ints(-3, 9, 1))
