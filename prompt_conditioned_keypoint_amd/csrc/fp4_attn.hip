@@ -75,6 +75,10 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// A reference point 2^24 or more out, where float32 has no halves: its row's exponents are
+// rounded products less the rounded product that it is.
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= 16777216.f && m != kFar; }
+
 // score * scale, rounded, less m: 0 for the score that m is the rounded product of,
 // however far out.
 __device__ __forceinline__ float far_exponent(float score, float scale, float m) {
@@ -249,7 +253,7 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
 #pragma unroll
     for (int j = 0; j < DT; ++j) o[r][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  bool far = false;  // some reference point is 2^24 or more out
+  bool far = false;  // one of the wave's reference points is far out
 
   int s = w.s0 + wave;
   int col = 0, row = s * 32;  // the next step's page column and row in the page
@@ -352,7 +356,8 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
     return top;
   };
   // Where one passes the slack, its row's reference point moves to the row's largest
-  // score of the step.
+  // score of the step. Each row goes by its own exponents and reference point alone, so that
+  // its result does not depend on the rows beside it.
   auto move = [&](const f32x4 (&st)[R][2], f32x4 (&x)[R][2]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -360,11 +365,11 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = fmaxf(top, st[r][i / 4][i % 4]);
       top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32)) * scale;
-      const float to = top > m[r] + kSlack ? top : m[r];
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float to = fmaf(top, scale, -m[r]) > kSlack ? top * scale : m[r];
       const float f = __builtin_amdgcn_exp2f(m[r] - to);
       m[r] = to;
-      far = far || __any(fabsf(to) >= 16777216.f && to != kFar);
+      far = far || __any(is_far(to));
       l[r] *= f;
 #pragma unroll
       for (int j = 0; j < DT; ++j) o[r][j] *= f;
@@ -373,8 +378,8 @@ __device__ __forceinline__ void attend(const CaParams& p, const Work& w, unsigne
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[r][i / 4][i % 4] = far ? far_exponent(st[r][i / 4][i % 4], scale, m[r])
-                                 : fmaf(st[r][i / 4][i % 4], scale, -m[r]);
+        x[r][i / 4][i % 4] = is_far(m[r]) ? far_exponent(st[r][i / 4][i % 4], scale, m[r])
+                                          : fmaf(st[r][i / 4][i % 4], scale, -m[r]);
   };
   // P^T of a step, the row sums with it
   auto softmax = [&](const f32x4 (&st)[R][2], u32x4 (&pf)[R]) {

@@ -741,6 +741,32 @@ def test_attention_a_row_does_not_depend_on_the_rows_beside_it(gkd):
     assert torch.equal(a[1, 2], b[1, 2])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L", [30, 400])
+def test_attention_a_row_does_not_depend_on_far_rows_beside_it(gkd, D, L):
+    """Every other row's scores pass 2^24 in magnitude, of either sign: the rows between them
+    keep every bit of their results, though their own scores are far enough out (element 0
+    adds 2^20 or so to each) for a rounded product to show."""
+    g = rng(L)
+    kv = torch.randn(6 * L, 2, 2, 32, D, generator=g, device="cuda")
+    kv[:, 0, :, :, :32] = 0
+    kv[:, 0, :, :, 0] = 1
+    codes, scales = gkd.quantize_fp4(kv)
+    table = torch.randperm(6 * L, generator=g, device="cuda").reshape(6, L).to(torch.int32)
+    q = randn(g, 6, 6, 8, D)
+    q[..., 0] = 2.0 ** 22
+    length = torch.tensor([32 * L, 32 * L - 40, 17 * L, 500, 31 * L, 900], dtype=torch.int32, device="cuda")
+    a = gkd.cache_attention(q, codes, scales, table, length=length)
+    for factor in (2.0 ** 10, -2.0 ** 10):
+        q2 = q.clone()
+        q2[:, 1::2, ::3] *= factor
+        q2[:, 0::2, 1::3] *= factor
+        b = gkd.cache_attention(q2, codes, scales, table, length=length)
+        kept = (q2 == q).all(-1)
+        assert torch.equal(a[kept], b[kept])
+        assert bool(torch.isfinite(b).all())
+
+
 def test_attention_pages_past_32_bit_offsets(gkd):
     """A pool of more than 2^32 bytes of codes: the last page lies past them."""
     page, Hk, D = 1024, 16, 128
