@@ -431,7 +431,11 @@ __global__ __launch_bounds__(256) void fp4_join_kernel(TileParams tp) {
 // 64 x 8192 x 8192 35.7 / 21.8, 128 x 1024 x 4096 9.9 / 13.6, 128 x 2048 x 16384 47.8 / 22.5,
 // 128 x 8192 x 8192 67 / 31): the few rows' kernel 1.03 for each 1024 of K of 256 tiles of
 // 16 x 32, tiles 0.7, 1.4 or 2.0 for each 256 of K of as many as there are CUs, their join
-// 2.5 and the time of its bytes at 4 TB/s.
+// 2.5 and the time of its bytes at 4 TB/s. With a short K both take their starts and ends
+// instead, 2 for each 256 of the few rows' tiles and 4 to 12 for a round of tiles; 0.5 for
+// the former tells them apart (17 x 256 x 4096 3.7 / 4.4, 32 x 256 x 16384 9.9 / 4.6, 64 x 256
+// x 16384 18.4 / 7.3, 128 x 256 x 4096 9.8 / 11.8, 256 x 256 x 4096 18.2 / 11.9, 1024 x 32 x 1024
+// 19.3 / 12.1, 1024 x 256 x 16384 264 / 44).
 struct TilePlan {
   int bm, bn, splits;  // bm 0: the few rows' kernel
 };
@@ -443,8 +447,8 @@ TilePlan tile_plan(int M, int N, int K) {
   const double step = bm == 32 ? 0.7 : bm == 64 ? 1.4 : 2.0;
   auto over = [](long long a, long long b) { return (a + b - 1) / b; };
   const long long few = over(M, 16) * over(N, 32), tiles = over(M, bm) * over(N, bn), steps = over(K, 256);
-  double least = 2.5 + (double)over(few, 256) * K / 1024 * 1.03;
-  for (int s = 1; s <= 8 && 2 * s <= steps && (s == 1 || tiles * s <= 256); ++s) {
+  double least = 2.5 + (double)over(few, 256) * (K < 500 ? 0.5 : K / 1024.0 * 1.03);
+  for (int s = 1; s == 1 || (s <= 8 && 2 * s <= steps && tiles * s <= 256); ++s) {
     const double t = 3.0 + (double)over(tiles * s, 256) * (double)over(steps, s) * step +
                      (s > 1 ? 2.5 + s * 8e-6 * M * N / 4.0 : 0.0);
     if (t < least) {

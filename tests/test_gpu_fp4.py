@@ -278,6 +278,14 @@ def test_linear_tiles(gkd, M, K, N):
     check_linear(gkd, M, K, N, bias=False, residual=False, out=F32, seed=M)
 
 
+# and a K of one step of the tiles
+@pytest.mark.parametrize("M,K,N", [(20, 256, 16390), (32, 96, 16385), (64, 160, 8190), (50, 256, 16385), (1024, 32, 1025),
+                                   (400, 96, 2050), (257, 256, 4099), (1100, 224, 1030)])
+def test_linear_tiles_of_one_step(gkd, M, K, N):
+    check_linear(gkd, M, K, N, "silu", seed=N)
+    check_linear(gkd, M, K, N, bias=False, residual=False, out=F32, seed=M)
+
+
 @pytest.mark.parametrize("M,K,N", [(31, 4128, 9001), (50, 4128, 8200), (130, 8224, 2050), (63, 544, 16390)])
 def test_linear_tiles_stay_within_their_arrays(gkd, M, K, N):
     g = rng(11)
