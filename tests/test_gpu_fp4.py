@@ -389,6 +389,40 @@ def test_linear_weights_past_32_bit_offsets(gkd):
     assert bool((y[0] == 3).all()) and torch.equal(y[1], sizes[torch.arange(N, device="cuda") % 7])
 
 
+@pytest.mark.parametrize("M", [2, 20])
+def test_linear_codes_past_32_bits(gkd, M):
+    """2100 rows of 2^22 - 32 weights: codes past 2^32 bytes, for the few rows' kernel and for
+    tiles with K split."""
+    K, N = (1 << 22) - 32, 2100
+    assert N * (K // 2) > 1 << 32 and (gkd.linear_fp4_workspace_size(M, N, K) > 0) == (M > 16)
+    codes = torch.zeros(N, K // 2, dtype=U8, device="cuda")
+    scales = torch.full((N, K // 32), 127, dtype=U8, device="cuda")
+    n, m = torch.arange(N, device="cuda"), torch.arange(M, device="cuda")
+    codes[:, 0], codes[:, -1] = (n % 5).to(U8), (n % 7).to(U8) * 16
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    x[:, 0], x[:, -1] = m % 4, 1 + m % 3
+    y = gkd.linear_fp4(x, codes, scales, out_dtype=F32)
+    sizes = torch.tensor(of.SIZES, dtype=F32, device="cuda")
+    assert torch.equal(y, (m % 4)[:, None] * sizes[n % 5] + (1 + m % 3)[:, None] * sizes[n % 7])
+
+
+@pytest.mark.parametrize("K,N,split", [(1024, 130, False), (8192, 1030, True), (544, 16390, False)])
+def test_linear_rows_past_32_bits(gkd, K, N, split):
+    """Rows of x and of the output that lie 2^22 - 8 and 2^22 elements apart: the last ones past
+    2^31 elements; the few rows' kernel, tiles with K split and without."""
+    M, g = 600, rng(N)
+    assert (gkd.linear_fp4_workspace_size(M, N, K) > 0) == split
+    x = randn(g, M, K)
+    codes, scales = gkd.quantize_fp4(randn(g, N, K, scale=K ** -0.5, dtype=F32))
+    wide = torch.empty(M * (1 << 22), dtype=BF, device="cuda").as_strided((M, K), ((1 << 22) - 8, 1))
+    wide.copy_(x)
+    far = torch.empty(M * (1 << 22), dtype=F32, device="cuda").as_strided((M, N + 1), (1 << 22, 1))
+    far.fill_(7)
+    got = gkd.linear_fp4(wide, codes, scales, act="silu", out=far[:, :N])
+    assert torch.equal(got, gkd.linear_fp4(x, codes, scales, act="silu", out_dtype=F32))
+    assert bool((far[:, N] == 7).all())
+
+
 def test_linear_empty_and_refusals(gkd):
     codes, scales = gkd.quantize_fp4(torch.zeros(8, 64, dtype=BF, device="cuda"))
     x = torch.zeros(4, 64, dtype=BF, device="cuda")
