@@ -830,6 +830,55 @@ def test_attention_pages_past_32_bit_offsets(gkd):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def named_values(gkd, B, Hk, D, page, L, name):
+    """A cache whose keys are zeros and whose value at token j has a 1 at element name(j), with
+    a table in no order."""
+    table = torch.randperm(B * L, generator=rng(L), device="cuda").reshape(B, L).to(torch.int32)
+    j = torch.arange(L * page, device="cuda")
+    v = (name(j)[:, None] == torch.arange(D, device="cuda")).to(BF)
+    c, s = gkd.quantize_fp4(v)
+    codes = torch.zeros(B * L, 2, Hk, page, D // 2, dtype=U8, device="cuda")
+    scales = torch.full((B * L, 2, Hk, page, D // 32), 127, dtype=U8, device="cuda")
+    for b in range(B):
+        codes[table[b].long(), 1] = c.view(L, 1, page, -1)
+        scales[table[b].long(), 1] = s.view(L, 1, page, -1)
+    return codes, scales, table
+
+
+NAMED = [  # B, Tq, Hq, Hk, page, L, lengths, q_len: one row, several tiles, one to three of 16 rows together
+    (3, 1, 8, 2, 64, 70, (4480, 4001, 70), None), (1, 20, 8, 4, 128, 60, (7333,), None),
+    (1, 2, 3, 1, 32, 1100, (35001,), None), (6, 1, 16, 16, 64, 36, (2304, 1, 0, 33, 2000, 640), None),
+    (3, 40, 8, 8, 64, 200, (12800, 6401, 31), (40, 17, 9)), (2, 30, 16, 4, 64, 150, (9600, 9543), (30, 29)),
+    (5, 80, 16, 16, 64, 36, (2304, 77, 2303, 1000, 5), (80, 3, 65, 80, 16)), (1, 300, 8, 2, 128, 100, (12790,), None),
+    (1, 1, 8, 2, 128, 1500, (191999,), None)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("by_step", [True, False])
+@pytest.mark.parametrize("B,Tq,Hq,Hk,page,L,lengths,q_len", NAMED)
+def test_attention_counts_every_key_once(gkd, B, Tq, Hq, Hk, page, L, lengths, q_len, by_step, D):
+    """Queries of zeros see all keys alike, and an output element is the share of the keys that
+    name it, by their step of 32 or by their place in every step. Sums are whole numbers in
+    float32, and their quotient is rounded three times. Up to 94 steps name an element: one
+    that is left out, or taken twice, changes it by more than two roundings."""
+    unit = 32 if by_step else 1
+    codes, scales, table = named_values(gkd, B, Hk, D, page, L, lambda j: j // unit % D)
+    q = torch.zeros(B, Tq, Hq, D, dtype=BF, device="cuda")
+    length = ints(*lengths)
+    rows = torch.full((B,), Tq, device="cuda") if q_len is None else ints(*q_len)
+    t, d = torch.arange(Tq, device="cuda"), torch.arange(D, device="cuda")
+    for causal in (False, True):
+        out = gkd.cache_attention(q, codes, scales, table, length=length, q_len=None if q_len is None else ints(*q_len),
+                                  causal=causal)
+        n = (length[:, None] - rows[:, None] + t + 1).clamp_min(0) if causal else length[:, None].expand(B, Tq)
+        n = torch.where(t < rows[:, None], n, 0).double()[..., None]               # keys that a row sees
+        per = unit * D
+        count = (n / per).floor() * unit + (n % per - unit * d).clamp(0, unit)     # those that name each element
+        want = (count / n.clamp_min(1))[:, :, None]
+        err = (out.double() - want).abs()
+        assert bool((err <= want * (2.0 ** -8 + 2.0 ** -22)).all()), err.max()
+
+
 def test_attention_refusals(gkd):
     q, codes, scales, table = attn_inputs(2, 1, 4, 2, 64, 32, 2, seed=16)
     assert gkd.cache_attention(q[:0], codes, scales, table[:0]).shape == (0, 1, 4, 64)
