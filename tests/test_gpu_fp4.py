@@ -921,6 +921,49 @@ def test_calls_run_on_the_current_stream(gkd):
     assert torch.equal(got, want)
 
 
+def test_calls_take_their_place_on_a_busy_stream(gkd):
+    """Long work on a stream that writes the inputs last: a call that ran on any other stream
+    would take the old ones."""
+    B, H, D, page, L = 2, 2, 128, 64, 130
+    q, codes, scales, table = attn_inputs(B, 1, 8, H, D, page, L, seed=61)
+    assert gkd.cache_attention_workspace_size(B, 1, 8, H, D, page, L) > 0
+    g = rng(62)
+    new = dict(q=randn(g, B, 1, 8, D), k=randn(g, B, 3, H, D), x=randn(g, 128, 8192), w=randn(g, 1030, 8192, scale=1 / 64),
+               start=ints(5000, 900), length=ints(5003, 903))
+    assert gkd.linear_fp4_workspace_size(128, 1030, 8192) > 0
+
+    def calls(s, c, sc):
+        wc, ws = gkd.quantize_fp4(s["w"])
+        gkd.cache_append(s["k"], s["k"], c, sc, table, start=s["start"])
+        return (gkd.cache_attention(s["q"], c, sc, table, length=s["length"]), gkd.linear_fp4(s["x"], wc, ws),
+                gkd.cache_attention(s["q"], c, sc, table[:, :4].contiguous()), wc, ws,
+                *gkd.cache_read(c, sc, table, 3, start=s["start"]))
+
+    c2, s2 = codes.clone(), scales.clone()
+    want = calls(new, c2, s2)
+    old = {n: torch.zeros_like(t) for n, t in new.items()}
+    a = torch.randn(4096, 4096, device="cuda").to(BF)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        calls(old, codes.clone(), scales.clone())  # (the stream's memory is there from here on)
+        a @ a / 64
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        busy = a
+        for _ in range(60):
+            busy = busy @ a / 64
+        for n in old:
+            old[n].copy_(new[n])
+        got = calls(old, codes, scales)
+        ended = st.query()
+    st.synchronize()
+    assert not ended  # the calls were made while the work was under way
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert torch.equal(codes, c2) and torch.equal(scales, s2)
+
+
 def test_captured_step_follows_its_inputs(gkd):
     """A decoding step captured once and replayed while its inputs change in place,
     with other work between the replays: every replay equals the eager step."""
