@@ -143,8 +143,9 @@ GKD_API gkd_status gkd_cache_read(const gkd_cache *cache, const int32_t *table, 
  *   workspace  gkd_cache_attention_workspace_size() bytes, 256-byte aligned
  *            (NULL where that is 0)
  * Pages' rows past length[b] may hold anything, NaN included, and so may
- * queries past q_len; the other values must be finite, and the products
- * q . K_j, as they are and scaled, at most 1e38 in magnitude. Scores, softmax
+ * queries past q_len; the other values must be finite, the products q . K_j,
+ * as they are and scaled, at most 1e38 and the values V_j at most 1e24 in
+ * magnitude (sums hold up to 2^30 of them, times 2^16 at most). Scores, softmax
  * statistics and outputs are float32; probabilities are rounded to bfloat16
  * for the product with V and summed as they are there. Hq a multiple of Hk,
  * B Tq Hq below 2^31, B Hk ceil(Tq Hq / Hk / 16) below 2^21, 0 < scale <=

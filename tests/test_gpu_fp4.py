@@ -879,6 +879,16 @@ def test_attention_counts_every_key_once(gkd, B, Tq, Hq, Hk, page, L, lengths, q
         assert bool((err <= want * (2.0 ** -8 + 2.0 ** -22)).all()), err.max()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_largest_values(gkd, D):
+    """Values of up to 1e24, one step after another passing the reference point's slack."""
+    q, codes, scales, table = attn_inputs(2, 3, 4, 2, D, 32, 140, seed=25)
+    scales[:, 1] = 127 + 77
+    scales[:, 0] = scales[:, 0] // 8 * 8
+    assert 6 * 2.0 ** 77 < 1e24
+    check_attention(gkd, q, codes, scales, table, ints(4470, 33), causal=True)
+
+
 def test_attention_refusals(gkd):
     q, codes, scales, table = attn_inputs(2, 1, 4, 2, 64, 32, 2, seed=16)
     assert gkd.cache_attention(q[:0], codes, scales, table[:0]).shape == (0, 1, 4, 64)
