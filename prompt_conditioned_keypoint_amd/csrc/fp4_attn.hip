@@ -55,7 +55,6 @@ constexpr float kFar = -3e38f;  // a reference point before any key: below every
 constexpr float kSlack = 8.f;
 constexpr int kStages = 2;      // of a wave's ring
 
-typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;
 
 // Read through the scalar cache: the compiler does not prove that no store changes it.
@@ -67,8 +66,6 @@ __device__ __forceinline__ long long uniform(long long v) {
   const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(v >> 32));
   return (long long)((unsigned long long)hi << 32 | lo);
 }
-
-__device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
 
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
@@ -105,20 +102,6 @@ struct Stage {
 // together: rows r / 4 of 0 and 3 with one g, of 1 and 2 with the next, so that
 // g ^ (r / 4) would send two lanes to a bank.
 __device__ __forceinline__ int turned(int j) { return (j & 1 ^ j >> 1 & 1) << 1 | (j >> 1 & 1); }
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N), the other counters left alone
-  asm volatile("" ::: "memory");
-}
-
-// What this wave has read of LDS is in its registers.
-__device__ __forceinline__ void wait_lds() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
-  asm volatile("" ::: "memory");
-}
 
 // A sequence's work: `tiles` tiles of `sub` times 16 rows of each key head, `steps`
 // steps of keys each. A step is taken to cost 3 + sub, its conversions beside the

@@ -1,4 +1,5 @@
-// fp4_device.hpp - device-side conversions of the four-bit format (gkdfp4.h).
+// fp4_device.hpp - device-side conversions of the four-bit format (gkdfp4.h), and what its
+// kernels' loads and products have in common.
 #pragma once
 
 #include "gkd_device.hpp"
@@ -41,6 +42,26 @@ __device__ __forceinline__ uint32_t fp4_codes(const float (&v)[8], uint32_t scal
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], unit, 2);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], unit, 3);
   return w;
+}
+
+// Eight values as an operand of a product
+__device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+typedef __attribute__((address_space(3))) void lds_void;  // where loads straight to LDS go
+
+// All but the last N loads of this wave are here.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N), the other counters left alone
+  asm volatile("" ::: "memory");
+}
+
+// What this wave has read of LDS is in its registers.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
+  asm volatile("" ::: "memory");
 }
 
 }  // namespace gkd

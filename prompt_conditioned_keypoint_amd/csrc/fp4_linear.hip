@@ -35,15 +35,11 @@ struct Fp4Params {
   int out_f32;
 };
 
-__device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
-
 // `rows` rows of `bytes` bytes as a buffer: what lies past them comes out as zeros.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const void* base, long long rows, long long ld, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)(uint32_t)((rows - 1) * ld + bytes), 0x00020000);
 }
 constexpr uint32_t kNowhere = 0xf0000000u;  // past every such buffer: 2^31 bytes at most
-
-typedef __attribute__((address_space(3))) void lds_void;
 
 // Rows of w and x are often a multiple of 4 KB long, over which the channels of L2 and of
 // memory repeat: workgroups that went through K in step would all ask the same channel. So
@@ -64,25 +60,11 @@ __device__ __forceinline__ void load1(__amdgpu_buffer_rsrc_t b, unsigned char* d
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)dst, 1, (int)from, 0, 0, 0);
 }
 
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N), the other counters left alone
-  asm volatile("" ::: "memory");
-}
-
 // The place of piece c of row r of x, in rows of 256 bytes, is c ^ turned(r). Sixteen lanes
 // that LDS serves together are, of a wave's 16-byte reads, lanes 0-3, 12-15 and 20-27 (and
 // the like): rows of two neighbouring g, whose pieces differ in bit 2. So bit 3 is made to
 // tell them apart (c ^ r: two lanes to a bank, 43% of the LDS cycles of 128 x 8192 x 8192).
 __device__ __forceinline__ int turned(int r) { return (r & 15) ^ ((r & 4) << 1); }
-
-// What this wave has read of LDS is in its registers.
-__device__ __forceinline__ void wait_lds() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0), the other counters left alone
-  asm volatile("" ::: "memory");
-}
 
 // All waves, with what they read of LDS in their registers.
 __device__ __forceinline__ void meet() {
