@@ -21,15 +21,19 @@
 // spares the exchange between lanes and the rescaling at nearly every step.
 // Probabilities are rounded to bfloat16 (2^-8 of each) for the product with V, whose
 // instruction takes both sides in that type; l sums the rounded ones, in the same
-// product with a column of ones.
+// product with a column of ones. Outputs of thousands of random keys are 0.0023 of their
+// size off the exact ones so, 0.0017 of which is their own rounding. A second product
+// with what the rounding left would take them to 0.0017, for 158 -> 204 us (4 sequences of
+// 128 rows of 32 heads on 8 of 128), 33 -> 41 (37 x 80 rows) and 2 to 5% with few rows.
 //
 // What bounds it: few rows, memory. 48 sequences of 32 heads on 8 heads of 128 and up to
-// 8192 tokens, one new token each: 316 MB in 70 to 76 us, 4.2 to 4.5 TB/s, where a large
-// copy on the same card moves 5.0. One sequence of 262144 tokens: 279 MB in 64 to 67 us.
+// 8192 tokens, one new token each: 316 MB in 69 to 76 us, 4.2 to 4.5 TB/s, where a large
+// copy on the same card moves 5.0. One sequence of 262144 tokens: 279 MB in 61 to 67 us (the
+// less the fewer other inputs pass through the last cache between its calls).
 // Many rows, the issue of instructions: a step of 32 rows of 128 elements takes 16 products
 // for S, 16 for O and 2 for l, beside 1024 exponents and what turns codes and scores into
-// operands, and 16 sequences of 128 rows of 32 heads on 8192 tokens take 293 us, 0.94 PF
-// (a large product of the library 1.3 to 1.4).
+// operands, and 16 sequences of 128 rows of 32 heads on 8 take 298 us behind 8192 tokens,
+// 0.92 PF (a large product of the library 1.3 to 1.4).
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
 
@@ -106,8 +110,9 @@ __device__ __forceinline__ int turned(int j) { return (j & 1 ^ j >> 1 & 1) << 1 
 // A sequence's work: `tiles` tiles of `sub` times 16 rows of each key head, `steps`
 // steps of keys each. A step is taken to cost 3 + sub, its conversions beside the
 // products and exponents of its rows, and a tile kStart more, the wait for its queries and
-// first keys and its waves' join (without that 88 tiles of one step each would be one
-// share: 16 sequences of 128 rows of 32 heads, 1 to 8192 tokens, took 670 us, now 214).
+// first keys and its waves' join (without that dozens of tiles of one step each would be
+// one share: 48 sequences of one row of 32 heads on 8 of 128, 1 to 8192 tokens, 75 us, with it
+// 52; 16 of 128 rows of 32 heads on as many, in shares 436 and 241).
 constexpr int kStart = 64;
 struct Sequence {
   int len, tq, live, tiles, sub, steps;

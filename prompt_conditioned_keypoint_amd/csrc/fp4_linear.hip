@@ -13,8 +13,11 @@
 // 3.4 TB/s where a large copy on the same card moves 5.0; 13 x 16384 x 4095 13.4 us
 // (2.7 TB/s); 1 x 1024 x 1024 2.8 us, little more than a launch. Up to some hundreds of
 // rows, the loads that a CU has under way, x from L2 beside the codes: 37 x 1024 x 4096
-// 6.0 us, 128 x 8192 x 8192 32 us, 0.54 PF. (The registers alone, without LDS, took 13.8,
-// 21.2, 2.8, 8.4 and 128 us.)
+// 6.0 us, 128 x 8192 x 8192 30 to 32 us, 0.54 PF. Beyond, x's way through L2 for tiles of 128
+// rows and the conversions for each of them: 256, 1024 and 4096 x 8192 x 8192 48, 161 and
+// 607 us (0.71, 0.86 and 0.91 PF), where gkd_linear takes 67, 150 and 374 with weights in
+// bfloat16; 256 and 4096 x 1024 x 4096 20 and 83 against 8.5 and 32. (The registers alone,
+// without LDS, took 13.8, 21.2, 2.8, 8.4 and 128 us for the first five.)
 #include "epilogue.hpp"
 #include "fp4_device.hpp"
 #include "fp4_launch.hpp"
